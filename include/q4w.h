@@ -65,8 +65,16 @@ typedef enum q4_op {
   Q4_OP_GEMM_CHUNK = 1,
   Q4_OP_PLE = 2,
   Q4_OP_LMHEAD = 3,
-  Q4_OP_DECODE_PASS = 4
+  Q4_OP_DECODE_PASS = 4,
+  Q4_OP_KV_ATTENTION = 5
 } q4_op;
+
+/* Element types of the paged-cache and sampling entry points. */
+typedef enum q4_dtype {
+  Q4_F32 = 0,
+  Q4_F16 = 1,
+  Q4_BF16 = 2
+} q4_dtype;
 
 /* ---------------------------------------------------------------------- */
 /* Quantise (setup, not part of a decode step).                            */
@@ -311,6 +319,124 @@ int lmhead_softcap_argmax_noalloc(const uint8_t* codes, const uint16_t* scales,
                                   q4_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
+/* Paged key/value cache and the attention over it.                        */
+/* ---------------------------------------------------------------------- */
+/* The state of n_seqs sequences at one layer.  K and V are stored in pages of
+ * page_size positions; position c of sequence s lies in page
+ * block_table[s][c / page_size], slot c % page_size.  The new tokens of all
+ * sequences are packed one after the other: sequence s has tokens
+ * cu_tokens[s] .. cu_tokens[s+1] - 1 of the call, and kv_lens[s] is the length
+ * of its cache WITH them, so token t is at position
+ *   P(t) = kv_lens[s] - cu_tokens[s+1] + t.
+ * Tokens at or behind cu_tokens[n_seqs] are padding: nothing is read or
+ * written for them.  A sequence may have no new tokens, or a cache length of
+ * zero.  The arrays below are device memory; the struct itself is HOST memory,
+ * read during the call only. */
+typedef struct q4_kv_cache {
+  void* k;                     /* [n_pages][n_kv][page_size][head_dim], fp16 or bf16 */
+  void* v;                     /* as k */
+  const int32_t* block_table;  /* [n_seqs][max_pages]; entries that hold no position may be anything */
+  const int32_t* cu_tokens;    /* [n_seqs + 1], from 0, not decreasing */
+  const int32_t* kv_lens;      /* [n_seqs] */
+  int dtype;                   /* Q4_F16 or Q4_BF16 */
+  int n_pages;                 /* >= 1 */
+  int n_kv;                    /* KV heads, >= 1 */
+  int page_size;               /* a multiple of 16, 16 .. 1024 */
+  int head_dim;                /* 64, 128, 256 or 512 */
+  int n_seqs;                  /* 1 .. 4096 */
+  int max_pages;               /* columns of block_table, >= 1 */
+} q4_kv_cache;
+
+/* kv_append: stores the K and V rows of T new tokens in the cache, K turned by
+ * the rotary positions, and optionally turns the tokens' queries.
+ * Pair i of a row turns by the angle 2 pi frac(p * steps[i] / 2^64), p the
+ * rotary position of the token: positions[t], or P(t) when positions is NULL:
+ *   x' = x cos - y sin,  y' = y cos + x sin
+ * for (x, y) = elements (i, i + rot_dim/2) of the row, or (2i, 2i+1) when
+ * interleaved is 1.  Elements from rot_dim on, and V, are copied.  steps[i] =
+ * round(2^64 f_i / (2 pi)) for a frequency of f_i radians per position
+ * (f_i = theta^(-2i/rot_dim) as a rule; 0 leaves a pair as it is); the product
+ * is taken modulo 2^64, so far positions lose no precision.  Arithmetic in
+ * fp32, one rounding (nearest even) to the cache's type.
+ *   k, v: [T][n_kv][head_dim], q: [T][n_q][head_dim] of in_dtype (any
+ *   q4_dtype), token strides in elements (heads and elements of a token are
+ *   contiguous); stride * element size a multiple of 16 bytes.
+ *   q and q_out both or neither; q_out: [T][n_q][head_dim] contiguous, of the
+ *   cache's type; n_q >= 1 with q, ignored without (no relation to n_kv is needed).
+ *   steps: device uint64 [rot_dim / 2]; rot_dim a multiple of 16 in
+ *   [0, head_dim]; 0 rotates nothing (steps may be NULL then).
+ *   positions: optional device int32 [T].
+ *   T >= 1.  A token whose position is negative, behind max_pages pages, or in
+ *   a page outside [0, n_pages) is not stored and sets the optional device
+ *   int32 *err to 1 (never cleared by the kernel); its query is still turned.
+ *   Two tokens of one call must not share a position of a page.  The inputs
+ *   must not overlap the outputs.                                          */
+int kv_append(const q4_kv_cache* cache, int T, const void* k, long long k_stride,
+              const void* v, long long v_stride, int in_dtype, const void* q,
+              long long q_stride, int n_q, void* q_out, const uint64_t* steps,
+              int rot_dim, int interleaved, const int32_t* positions, int32_t* err,
+              q4_stream_t stream);
+
+/* kv_attention: attention of T new tokens over the cache that holds them
+ * (kv_append first).  For query head h, its KV head h / (n_q / n_kv):
+ *   s_c = scale * q . k_c,  o = sum_c e^(s_c) v_c / sum_c e^(s_c),
+ *   lse = ln sum_c e^(s_c)
+ * over the positions c in (P(t) - window, P(t)], c >= 0 (window 0: all of
+ * them).  A token that sees no position (P(t) < 0) gets o = 0, lse = -inf.
+ *   q: [T][n_q][head_dim] of the cache's type, token stride in elements
+ *   (stride * 2 a multiple of 16 bytes); out: [T][n_q][head_dim] contiguous;
+ *   lse_opt: f32 [T][n_q], or NULL.  n_q a multiple of n_kv, n_q / n_kv <= 128.
+ *   max_q: no sequence has more new tokens than this (1 <= max_q <= T): it
+ *   selects the kernels.  A longer one gets its first max_q tokens only and
+ *   sets *err.
+ *   Positions outside every token's reach are never read, so their pages may
+ *   be freed; what lies in a page behind kv_lens may be anything.  A page
+ *   outside [0, n_pages), or kv_lens beyond max_pages pages, leaves out those
+ *   positions and sets the optional device int32 *err to 1 (never cleared).
+ *   A NaN or infinity in V of a position reaches every token of its sequence
+ *   whose head reads the same tile, masked or not, unless the position is
+ *   outside the reach of all of them.
+ *   Arithmetic: scores, maximum, sum and output are fp32; the probabilities
+ *   enter the second product rounded once to the cache's type.  The split of
+ *   the keys over CTAs depends on the lengths only: repeated calls give the
+ *   same bits.
+ *   ws: q4_workspace_bytes(Q4_OP_KV_ATTENTION, max_q * n_q / n_kv, head_dim,
+ *   n_seqs * n_kv) bytes, contents on entry do not matter; calls that share
+ *   one must not overlap.                                                  */
+int kv_attention(const q4_kv_cache* cache, int T, int max_q, const void* q,
+                 long long q_stride, int n_q, float scale, int window, void* out,
+                 float* lse_opt, int32_t* err, void* ws, size_t ws_bytes,
+                 q4_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Sampling from the head's logits.                                        */
+/* ---------------------------------------------------------------------- */
+/* logits_sample: one token per row of logits.  With M = max z,
+ * w_i = e^((z_i - M) / temperature):
+ *   S_k  the top_k largest logits (ties: lower index first),
+ *   S_p  the shortest prefix of S_k, in that order, of mass >= top_p mass(S_k),
+ *   S    those of S_p with w_i >= min_p (the largest logit always stays);
+ *   token = the first index, in the order of the vocabulary, at which the
+ *   running mass of S exceeds u mass(S);  logprob = ln(w_token / mass(S)).
+ * A NaN counts as -inf, which is never chosen; a row of nothing else gives
+ * token -1 and logprob -inf.  temperature <= 0 (or NaN), top_k = 1 and
+ * top_p <= 0 give the lowest index of the largest logit.
+ *   logits: [b][V] of `dtype` (any q4_dtype), row stride in elements;
+ *   u: f32 [b] in [0, 1) (clamped); temperature, top_p, min_p: f32 [b],
+ *   top_k: int32 [b]; NULL, or a row's top_k <= 0, top_p >= 1, min_p <= 0,
+ *   turn a filter off (temperature NULL: 1).
+ *   token: int32 [b]; logprob_opt: f32 [b], or NULL.
+ *   1 <= b <= 65535; 1 <= V <= 1048576; stride >= V.  No workspace.
+ * Masses are sums of integers (weights in units of 2^-42 of the largest, each
+ * within about 2^-29 of itself; weights below 2^-128 count as zero): the
+ * result does not depend on the order of the sums, so the same inputs give
+ * the same token on every call.                                            */
+int logits_sample(const void* logits, long long stride, int dtype, int b, int V,
+                  const float* u, const float* temperature, const int32_t* top_k,
+                  const float* top_p, const float* min_p, int32_t* token,
+                  float* logprob_opt, q4_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
 /* Decode weight pass over a stack of layers (S=1).                        */
 /* ---------------------------------------------------------------------- */
 typedef struct q4_matrix {
@@ -396,8 +522,10 @@ int q4_rmsnorm_f16(const float* in, int H, float eps, uint16_t* out_f16, q4_stre
 /* ---------------------------------------------------------------------- */
 /* Bytes of workspace an operation needs (0 = none).  Arguments per op:
  *   Q4_OP_GEMV (N, K, batch), Q4_OP_GEMM_CHUNK (N, K, 64), Q4_OP_PLE (S, D, L),
- *   Q4_OP_LMHEAD (V, K, b), Q4_OP_DECODE_PASS (H, max q+2kv rows, max mlp).
- * Depends on the current device's SM count for Q4_OP_LMHEAD; returns 0 when
+ *   Q4_OP_LMHEAD (V, K, b), Q4_OP_DECODE_PASS (H, max q+2kv rows, max mlp),
+ *   Q4_OP_KV_ATTENTION (max_q * n_q / n_kv, head_dim, n_seqs * n_kv).
+ * Depends on the current device's SM count for Q4_OP_LMHEAD and
+ * Q4_OP_KV_ATTENTION; returns 0 when
  * the current device cannot be queried.                                   */
 size_t q4_workspace_bytes(int op, int a, int b, int c);
 

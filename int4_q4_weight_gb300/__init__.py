@@ -10,6 +10,7 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -18,16 +19,18 @@ __all__ = [
     "load", "build", "Q4Error", "q4_quantize", "q4_gemv", "q4_gemv_weights_ro", "q4_gemv_stage", "q4_rmsnorm_f16",
     "q4_decode_pass", "q4_decode_pass_launches", "q2_gemv", "lmhead_softcap_argmax", "ple_gather_project", "q4_gemm_chunk",
     "q8_quantize", "ple_gather_project_q8", "q4_gemv_a8", "q4_gemm_chunk_a8", "q4_act_calibrate_a8",
+    "kv_append", "kv_rope_steps", "kv_attention", "logits_sample",
     "q4_workspace_bytes", "q4_version", "Q4_IN_F16", "Q4_IN_RMS_F16", "Q4_IN_RMS_F32",
     "Q4_IN_RMS2_F32", "Q4_OP_GEMV", "Q4_OP_GEMM_CHUNK", "Q4_OP_PLE", "Q4_OP_LMHEAD",
-    "Q4_OP_DECODE_PASS", "q4_layer", "q4_matrix",
+    "Q4_OP_DECODE_PASS", "Q4_OP_KV_ATTENTION", "q4_layer", "q4_matrix", "q4_kv_cache",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libq4w.so")
 
 Q4_IN_F16, Q4_IN_RMS_F16, Q4_IN_RMS_F32, Q4_IN_RMS2_F32 = 0, 1, 2, 3
-Q4_OP_GEMV, Q4_OP_GEMM_CHUNK, Q4_OP_PLE, Q4_OP_LMHEAD, Q4_OP_DECODE_PASS = 0, 1, 2, 3, 4
+Q4_OP_GEMV, Q4_OP_GEMM_CHUNK, Q4_OP_PLE, Q4_OP_LMHEAD, Q4_OP_DECODE_PASS, Q4_OP_KV_ATTENTION = 0, 1, 2, 3, 4, 5
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4_dtype
 
 _lib = None
 
@@ -35,6 +38,7 @@ vp = ctypes.c_void_p
 ci = ctypes.c_int
 cf = ctypes.c_float
 csz = ctypes.c_size_t
+cll = ctypes.c_longlong
 
 
 class q4_matrix(ctypes.Structure):
@@ -45,6 +49,12 @@ class q4_layer(ctypes.Structure):
     _fields_ = [("q_rows", ci), ("kv_rows", ci), ("mlp_rows", ci),
                 ("q", q4_matrix), ("k", q4_matrix), ("v", q4_matrix), ("o", q4_matrix),
                 ("gate", q4_matrix), ("up", q4_matrix), ("down", q4_matrix)]
+
+
+class q4_kv_cache(ctypes.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("block_table", vp), ("cu_tokens", vp), ("kv_lens", vp),
+                ("dtype", ci), ("n_pages", ci), ("n_kv", ci), ("page_size", ci), ("head_dim", ci),
+                ("n_seqs", ci), ("max_pages", ci)]
 
 
 _SIGS = {
@@ -66,6 +76,10 @@ _SIGS = {
     "q4_gemv_stage": (ci, [ctypes.POINTER(q4_matrix), ctypes.POINTER(ci), ci, ci, vp, ci, cf, ci,
                            ctypes.POINTER(vp), ctypes.POINTER(vp), vp]),
     "q4_rmsnorm_f16": (ci, [vp, ci, cf, vp, vp]),
+    "kv_append": (ci, [ctypes.POINTER(q4_kv_cache), ci, vp, cll, vp, cll, ci, vp, cll, ci, vp, vp, ci, ci, vp, vp,
+                       vp]),
+    "kv_attention": (ci, [ctypes.POINTER(q4_kv_cache), ci, ci, vp, cll, ci, cf, ci, vp, vp, vp, vp, csz, vp]),
+    "logits_sample": (ci, [vp, cll, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp]),
     "q4_workspace_bytes": (csz, [ci, ci, ci, ci]),
     "q4_status_string": (ctypes.c_char_p, [ci]),
     "q4_last_error": (ctypes.c_char_p, []),
@@ -544,6 +558,146 @@ def q2_gemv(codes, scales, x, y=None):
     _numel(y, N, "y")
     _check(lib.q2_gemv(_ptr(codes), _ptr(scales), _ptr(x), _ptr(y), N, K, _stream()), "q2_gemv")
     return y
+
+
+def kv_rope_steps(rot_dim, theta=10000.0, device="cuda", freqs=None):
+    """Rotary steps of kv_append: int64 [rot_dim/2] (uint64 bits), the turns per
+    position in units of 2^-64.  ``freqs``: the frequencies in radians per
+    position (float64, any sequence of rot_dim/2; 0 leaves a pair as it is)
+    instead of theta^(-2i/rot_dim)."""
+    if freqs is None:
+        freqs = [theta ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    freqs = [float(f) for f in freqs]
+    if len(freqs) != rot_dim // 2:
+        raise Q4Error(f"freqs has {len(freqs)} entries; rot_dim implies {rot_dim // 2}")
+    turns = [int(round(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64)) % 2 ** 64 for f in freqs]
+    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def _heads(t, dtype, heads, dim, T, name):
+    """A [T, heads, dim] tensor whose heads and elements are contiguous; returns the token stride."""
+    if t.dim() != 3 or tuple(t.shape) != (T, heads, dim):
+        raise Q4Error(f"{name} has shape {tuple(t.shape)}; the sizes imply ({T}, {heads}, {dim})")
+    _dev(t[0], dtype, name)   # checks the device, the type and that a token's heads are contiguous
+    return t.stride(0) if T > 1 else heads * dim
+
+
+def _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens):
+    if k_cache.dtype not in (torch.float16, torch.bfloat16):
+        raise Q4Error(f"k_cache must be torch.float16 or torch.bfloat16, got {k_cache.dtype}")
+    _dev(k_cache, k_cache.dtype, "k_cache")
+    _dev(v_cache, k_cache.dtype, "v_cache")
+    for t, nm in ((block_table, "block_table"), (cu_tokens, "cu_tokens"), (kv_lens, "kv_lens")):
+        _dev(t, torch.int32, nm)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise Q4Error(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} must both be "
+                      "[n_pages, n_kv, page_size, head_dim]")
+    n = kv_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise Q4Error(f"block_table has shape {tuple(block_table.shape)}; kv_lens implies ({n}, max_pages)")
+    _numel(cu_tokens, n + 1, "cu_tokens")
+    pages, heads, page, dim = k_cache.shape
+    return q4_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_tokens.data_ptr(),
+                       kv_lens.data_ptr(), _DTYPES[k_cache.dtype], pages, heads, page, dim, n, block_table.shape[1])
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, cu_tokens, kv_lens, steps=None, q=None, positions=None,
+              interleaved=False, q_out=None, err=None):
+    """Store the K and V rows of new tokens (k, v [T, n_kv, D], f32/f16/bf16, any
+    token stride) in the paged cache [n_pages, n_kv, page_size, D], K turned by
+    the rotary ``steps`` (kv_rope_steps; None: not turned); returns the turned
+    queries q [T, n_q, D] in the cache's type, or None without q.  kv_lens
+    counts the new tokens already; see include/q4w.h for the layout."""
+    lib = load()
+    cache = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
+    T, D = k.shape[0], cache.head_dim
+    if k.dtype not in _DTYPES:
+        raise Q4Error(f"k must be float32, float16 or bfloat16, got {k.dtype}")
+    if T == 0:
+        return None if q is None else torch.empty((0, q.shape[1], D), dtype=k_cache.dtype, device=k.device)
+    ks = _heads(k, k.dtype, cache.n_kv, D, T, "k")
+    vs = _heads(v, k.dtype, cache.n_kv, D, T, "v")
+    qs = n_q = 0
+    if q is not None:
+        n_q = q.shape[1] if q.dim() == 3 else 0
+        qs = _heads(q, k.dtype, n_q, D, T, "q")
+        if q_out is None:
+            q_out = torch.empty((T, n_q, D), dtype=k_cache.dtype, device=q.device)
+        _dev(q_out, k_cache.dtype, "q_out")
+        _numel(q_out, T * n_q * D, "q_out")
+    elif q_out is not None:
+        raise Q4Error("q_out without q")
+    _dev(steps, torch.int64, "steps")
+    _dev(positions, torch.int32, "positions")
+    _dev(err, torch.int32, "err")
+    if positions is not None:
+        _numel(positions, T, "positions")
+    _check(lib.kv_append(ctypes.byref(cache), T, _ptr(k), ks, _ptr(v), vs, _DTYPES[k.dtype], _ptr(q), qs, n_q,
+                         _ptr(q_out), _ptr(steps), 0 if steps is None else 2 * steps.numel(), int(interleaved),
+                         _ptr(positions), _ptr(err), _stream()), "kv_append")
+    return q_out
+
+
+def kv_attention_ws(max_q, n_q, n_kv, head_dim, n_seqs, device):
+    n = q4_workspace_bytes(Q4_OP_KV_ATTENTION, max_q * (n_q // n_kv), head_dim, n_seqs * n_kv)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def kv_attention(q, k_cache, v_cache, block_table, cu_tokens, kv_lens, max_q=None, scale=None, window=0, out=None,
+                 lse=None, ws=None, err=None):
+    """Attention of the new tokens' queries q [T, n_q, D] over the paged cache
+    that holds them: returns (out [T, n_q, D], lse).  max_q: an upper bound of
+    the new tokens of a sequence (None: T); scale None: 1/sqrt(D); window: how
+    many positions a token sees (0: all); lse: f32 [T, n_q] to fill, or None."""
+    lib = load()
+    cache = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
+    if q.dim() != 3:
+        raise Q4Error(f"q has shape {tuple(q.shape)}; [T, n_q, head_dim] is wanted")
+    T, n_q, D = q.shape[0], q.shape[1], cache.head_dim
+    if T == 0:
+        return (torch.empty_like(q) if out is None else out), lse
+    qs = _heads(q, k_cache.dtype, n_q, D, T, "q")
+    if out is None:
+        out = torch.empty((T, n_q, D), dtype=q.dtype, device=q.device)
+    _dev(out, k_cache.dtype, "out")
+    _dev(lse, torch.float32, "lse")
+    _dev(err, torch.int32, "err")
+    _dev(ws, torch.uint8, "ws")
+    _numel(out, T * n_q * D, "out")
+    _numel(lse, T * n_q, "lse")
+    max_q = T if max_q is None else max_q
+    if n_q < 1 or n_q % cache.n_kv:
+        raise Q4Error(f"n_q={n_q} must be a multiple of n_kv={cache.n_kv}")
+    if ws is None:
+        ws = kv_attention_ws(max_q, n_q, cache.n_kv, D, cache.n_seqs, q.device)
+    _check(lib.kv_attention(ctypes.byref(cache), T, max_q, _ptr(q), qs, n_q, D ** -0.5 if scale is None else scale,
+                            window, _ptr(out), _ptr(lse), _ptr(err), _ptr(ws), ws.numel(), _stream()), "kv_attention")
+    return out, lse
+
+
+def logits_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprobs=None):
+    """One token per row of logits [b, V] (f32/f16/bf16, any row stride) from the
+    random numbers u [b] in [0, 1): returns (tokens int32 [b], logprobs f32 [b]).
+    temperature, top_p, min_p: f32 [b]; top_k: int32 [b]; None turns one off."""
+    lib = load()
+    if logits.dim() != 2 or logits.dtype not in _DTYPES:
+        raise Q4Error(f"logits must be [b, V] of float32, float16 or bfloat16, got {tuple(logits.shape)} {logits.dtype}")
+    b, V = logits.shape
+    tokens = torch.empty(b, dtype=torch.int32, device=logits.device) if tokens is None else tokens
+    logprobs = torch.empty(b, dtype=torch.float32, device=logits.device) if logprobs is None else logprobs
+    if b == 0:
+        return tokens, logprobs
+    _dev(logits[0], logits.dtype, "logits")
+    for t, dt, nm in ((u, torch.float32, "u"), (temperature, torch.float32, "temperature"),
+                      (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"),
+                      (min_p, torch.float32, "min_p"), (tokens, torch.int32, "tokens"),
+                      (logprobs, torch.float32, "logprobs")):
+        _dev(t, dt, nm)
+        _numel(t, b, nm)
+    _check(lib.logits_sample(_ptr(logits), logits.stride(0) if b > 1 else V, _DTYPES[logits.dtype], b, V, _ptr(u),
+                             _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens), _ptr(logprobs),
+                             _stream()), "logits_sample")
+    return tokens, logprobs
 
 
 def q4_decode_pass_launches(descs, H):

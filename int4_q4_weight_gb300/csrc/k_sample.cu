@@ -1,0 +1,773 @@
+// Sampling a token per row of logits: temperature, top-k, top-p and min-p,
+// from a given random number.
+//
+// With M = max z and w_i = 2^-t_i, t_i = (M - z_i) log2(e) / T:
+//   S_k  the k largest z (ties: lower index first),
+//   S_p  the shortest prefix of S_k in that order whose mass reaches
+//        p mass(S_k),
+//   S    those of S_p with w_i >= min_p,
+//   token = the first index, in vocabulary order, whose running mass in S
+//        exceeds u mass(S);  logprob = ln(w_token / mass(S)).
+// All three sets are prefixes of one order, so S is given by a threshold
+// (the key of a logit and how many of its ties, lowest index first) and the
+// min-p test.  Nothing is sorted over the vocabulary.
+//
+// Arithmetic.  A token that lies next to a border has to fall on the side
+// that the definition says, and a border is a sum of up to 2^20 weights, so
+// fp32 sums of expf would be too coarse: masses are integers.  t is formed as
+// an fp32 pair (the difference exactly, log2(e)/T in two pieces), cut into
+// eighths of an octave, n = floor(8 t), and the rest f in [0, 1/8] goes
+// through a degree-6 polynomial of 2^-f to a 28-bit mantissa; the weight is
+// mantissa * 2^(-(n mod 8)/8) * 2^-(n div 8) rounded to units of 2^-42.
+// Integer sums have no order, so atomics and cluster reductions give the same
+// bits on every run.  A weight is off by about 2^-29 of itself, unbiased.
+//
+// Work.  A cluster of CTAs takes a row, each an index range of it:
+//   A  the maximum (and its lowest index, the answer of greedy rows);
+//   B  a histogram of n over the row (1024 bins: 128 octaves), which bounds
+//      the last bin that S can reach;
+//   C  few candidates (<= 1024) up to that bin: they are gathered into the
+//      leader CTA, sorted, cut and sampled there;
+//   D  many: the bin that holds a border is refined by histograms of the
+//      order-preserving integer key (1024 sub-bins a level) until the
+//      threshold is a single key; then masses of 128-index segments, a scan of
+//      them, and the one segment that holds the target.
+// The row is read from HBM once; the later passes find it in L2.
+#include <math_constants.h>
+
+#include "q4w_device.cuh"
+#include "q4w_internal.cuh"
+#include "q4w_kv.cuh"
+#include "q4w_tc.cuh"
+
+namespace q4w {
+namespace sample {
+
+constexpr int kThr = 512;
+constexpr int kWarpsS = kThr / 32;
+constexpr int kBins = 1024;
+constexpr int kCap = 1024;          // candidates that the leader takes
+constexpr int kSeg = 128;           // indices per segment of the final pass
+constexpr int kMaxSegs = 1024;      // segments of a CTA: 2^17 indices, so a 32-bit bin never overflows
+constexpr int kMaxCluster = 8;
+typedef unsigned long long u64;
+
+struct Params {
+  const void* z;               // [rows][V]
+  long long stride;            // elements
+  const float* u;
+  const float* temperature;    // NULL: 1
+  const int32_t* top_k;        // NULL or <= 0: off
+  const float* top_p;          // NULL or >= 1: off
+  const float* min_p;          // NULL or <= 0: off
+  int32_t* token;
+  float* logprob;              // NULL: not written
+  int V;
+  int range;                   // indices per CTA of the cluster, a multiple of kSeg
+};
+
+// Order-preserving integer of a logit: larger logit, larger key.
+__device__ __forceinline__ uint32_t key_of(float z) {
+  const uint32_t b = __float_as_uint(z);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float logit_of(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// What turns a logit of this row into a weight.
+struct Scale {
+  float top;       // M
+  float ch, cl;    // log2(e) / T in two pieces
+  float mh, ml;    // log2(1 / min_p) in two pieces: kept while t <= it
+};
+
+// t = (M - z) log2(e) / T as p + e, |e| small against p.  Zero at z = M
+// whatever T is; +inf for z = -inf.
+__device__ __forceinline__ void octaves(const Scale& s, float z, float& p, float& e) {
+  const float d = s.top - z;
+  if (z == s.top) {
+    p = e = 0.f;
+    return;
+  }
+  p = d * s.ch;
+  if (!(p < 128.f)) {
+    e = 0.f;
+    return;
+  }
+  // the exact difference is d + dl
+  const float bb = d - s.top;
+  const float dl = (s.top - (d - bb)) - (z + bb);
+  e = fmaf(d, s.ch, -p) + fmaf(d, s.cl, dl * s.ch);
+}
+
+// Bin of a logit, kBins when its weight is below 2^-128 (it never counts).
+__device__ __forceinline__ int bin_of(float p) { return p < 128.f ? (int)(p * 8.f) : kBins; }
+
+// 28-bit mantissa of the weight inside its bin: 2^-(t - n/8), in (0.9, 1] * 2^28.
+__device__ __forceinline__ uint32_t mantissa(float p, float e, int n) {
+  const float f = fmaf((float)n, -0.125f, p) + e;
+  // 2^-f - 1 on [0, 1/8]: the series of exp(-f ln 2), whose next term is below 2^-37
+  float g = 1.5403530393381608e-4f;
+  g = fmaf(g, f, -1.3333558146428443e-3f);
+  g = fmaf(g, f, 9.618129107628477e-3f);
+  g = fmaf(g, f, -5.550410866482158e-2f);
+  g = fmaf(g, f, 2.402265069591007e-1f);
+  g = fmaf(g, f, -6.931471805599453e-1f);
+  g = g * f;
+  return (uint32_t)((1 << 28) + __float2int_rn(g * 268435456.f));
+}
+
+// 2^(-j/8) * 2^31, rounded
+__device__ __constant__ uint32_t kEighth[8] = {2147483648u, 1969251188u, 1805811301u, 1655936265u,
+                                               1518500250u, 1392470869u, 1276901417u, 1170923762u};
+
+// The weight in units of 2^-42.
+__device__ __forceinline__ u64 weight_of(uint32_t mant, int n) {
+  const u64 w = (u64)mant * kEighth[n & 7];        // 2^59 scale
+  const int sh = 17 + (n >> 3);
+  return sh > 60 ? 0ull : (w + (1ull << (sh - 1))) >> sh;
+}
+__device__ __forceinline__ u64 weight(const Scale& s, float z) {
+  float p, e;
+  octaves(s, z, p, e);
+  const int n = bin_of(p);
+  return n < kBins ? weight_of(mantissa(p, e, n), n) : 0ull;
+}
+__device__ __forceinline__ bool passes_minp(const Scale& s, float z) {
+  float p, e;
+  octaves(s, z, p, e);
+  return z == s.top || (p - s.mh) + (e - s.ml) <= 0.f;
+}
+
+template <typename T>
+__device__ __forceinline__ float load_logit(const T* p) {
+  float z;
+  if constexpr (sizeof(T) == 4) z = *p;
+  else if constexpr (std::is_same<T, __half>::value) z = __half2float(*p);
+  else z = __bfloat162float(*p);
+  return z != z ? -CUDART_INF_F : z + 0.f;   // a NaN is never chosen; -0 and 0 tie
+}
+
+// Calls f(z, index) for every index of [i0, i1) of the row, a warp taking
+// consecutive indices.
+template <typename T, typename F>
+__device__ __forceinline__ void for_range(const T* row, int i0, int i1, F f) {
+#pragma unroll 4
+  for (int i = i0 + (int)threadIdx.x; i < i1; i += kThr) f(load_logit(row + i), i);
+}
+
+__device__ __forceinline__ u64 ld_cluster_u64(uint32_t a) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  tc::cluster_arrive_release();
+  tc::cluster_wait();
+}
+
+struct Shared {
+  uint32_t cnt[kBins], lo[kBins], hi[kBins];   // per bin: elements, sums of the mantissa's low 14 and high bits
+  union {
+    u64 list[kCap];                            // candidates: inverted key, index
+    u64 seg[kMaxSegs];                         // masses of the segments
+  };
+  uint32_t tie[kMaxSegs];                      // elements equal to the threshold, per segment
+  u64 total;                                   // this CTA's mass (phase B), then of S
+  u64 best;                                    // this CTA's maximum: key, inverted index
+  u64 mine;                                    // this CTA's mass of S
+  uint32_t ties;                               // this CTA's elements equal to the threshold
+  uint32_t n_list;
+  u64 red[kWarpsS];
+  uint32_t red32[kWarpsS];
+  u64 scan_total;
+  Scale scale;
+  u64 goal;
+  // the crossing bin of a scan
+  int cross_bin;
+  uint32_t cross_cnt;
+  u64 cross_mass;
+};
+
+template <typename V>
+__device__ __forceinline__ V warp_incl(V v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const V t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+// Inclusive scan over the CTA's threads; *total: the sum.
+template <typename V>
+__device__ __forceinline__ V block_incl(V v, V* red, V* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  v = warp_incl(v);
+  __syncthreads();
+  if (lane == 31) red[warp] = v;
+  __syncthreads();
+  V before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWarpsS; ++w) {
+    if (w < warp) before += red[w];
+    sum += red[w];
+  }
+  *total = sum;
+  return v + before;
+}
+
+// Ascending bitonic sort of n values in shared memory, n a power of two.
+__device__ __forceinline__ void bitonic(u64* v, int n) {
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += kThr) {
+        const int x = i ^ j;
+        if (x > i) {
+          const u64 a = v[i], b = v[x];
+          if ((a > b) == ((i & k) == 0)) v[i] = b, v[x] = a;
+        }
+      }
+    }
+  __syncthreads();
+}
+
+// Adds every CTA's histogram, in every CTA: bins 2 threadIdx.x and + 1.
+__device__ __forceinline__ void merge_bins(Shared& sh, uint32_t ctas, bool masses, u64 (&cnt)[2], u64 (&mant)[2]) {
+  cnt[0] = cnt[1] = mant[0] = mant[1] = 0;
+  for (uint32_t r = 0; r < ctas; ++r) {
+    const u64 c = ld_cluster_u64(tc::cluster_addr(&sh.cnt[2 * threadIdx.x], r));
+    cnt[0] += (uint32_t)c, cnt[1] += c >> 32;
+    if (masses) {
+      const u64 l = ld_cluster_u64(tc::cluster_addr(&sh.lo[2 * threadIdx.x], r));
+      const u64 h = ld_cluster_u64(tc::cluster_addr(&sh.hi[2 * threadIdx.x], r));
+      mant[0] += (uint32_t)l + ((u64)(uint32_t)h << 14);
+      mant[1] += (l >> 32) + ((h >> 32) << 14);
+    }
+  }
+}
+
+__device__ __forceinline__ void clear_bins(Shared& sh) {
+  for (int i = threadIdx.x; i < kBins; i += kThr) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
+}
+
+__device__ __forceinline__ void add_to_bin(Shared& sh, int b, uint32_t mant) {
+  atomicAdd(&sh.cnt[b], 1u);
+  atomicAdd(&sh.lo[b], mant & 0x3fffu);
+  atomicAdd(&sh.hi[b], mant >> 14);
+}
+
+// Mass of a bin whose elements' mantissas sum to m, in units of 2^-42.
+__device__ __forceinline__ u64 bin_mass(u64 m, int n) {
+  // m < 2^49: in two pieces so that the product with the 32-bit factor fits
+  const u64 e = kEighth[n & 7];
+  const u64 a = (m >> 24) * e, b = (m & 0xffffffu) * e;   // 2^59 scale: a << 24 + b
+  const int sh = 17 + (n >> 3);
+  if (sh > 80) return 0ull;
+  return (sh >= 24 ? a >> (sh - 24) : a << (24 - sh)) + (sh < 60 ? b >> sh : 0ull);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Params p) {
+  __shared__ Shared sh;
+  uint32_t rank, ctas;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const int row = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) sh.n_list = 0;
+  clear_bins(sh);
+  pdl_wait();
+  const T* z = static_cast<const T*>(p.z) + row * p.stride;
+  const int i0 = min((int)rank * p.range, p.V), i1 = min(i0 + p.range, p.V);
+
+  const float temp = p.temperature ? p.temperature[row] : 1.f;
+  const int k_in = p.top_k ? p.top_k[row] : 0;
+  const float top_p = p.top_p ? p.top_p[row] : 1.f;
+  const float min_p = p.min_p ? p.min_p[row] : 0.f;
+  const float u = fminf(fmaxf(p.u[row], 0.f), 0.99999994f);
+  const bool has_k = k_in > 0 && k_in < p.V;
+  const bool has_p = top_p < 1.f;
+  const bool has_m = min_p > 0.f;
+
+  // ---- A: the maximum and its lowest index
+  u64 best = 0;
+  {
+    for_range(z, i0, i1, [&](float v, int i) {
+      const u64 c = ((u64)key_of(v) << 32) | (uint32_t)~i;
+      best = c > best ? c : best;
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const u64 t = __shfl_xor_sync(0xffffffffu, best, o);
+      best = t > best ? t : best;
+    }
+    if (lane == 0) sh.red[warp] = best;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 0; w < kWarpsS; ++w) best = sh.red[w] > best ? sh.red[w] : best;
+      sh.best = best;
+    }
+    cluster_sync();
+    best = 0;
+    for (uint32_t r = 0; r < ctas; ++r) {
+      const u64 t = ld_cluster_u64(tc::cluster_addr(&sh.best, r));
+      best = t > best ? t : best;
+    }
+  }
+  Scale s;
+  s.top = logit_of((uint32_t)(best >> 32));
+  const bool nothing = s.top == -CUDART_INF_F;
+  const bool greedy = !(temp > 0.f) || k_in == 1 || top_p <= 0.f;
+  if (nothing || greedy) {   // the same in every CTA of the cluster
+    if (rank == 0 && threadIdx.x == 0) {
+      p.token[row] = nothing ? -1 : (int)~(uint32_t)best;
+      if (p.logprob) p.logprob[row] = nothing ? -CUDART_INF_F : 0.f;
+    }
+    cluster_sync();   // no CTA leaves while another reads its shared memory
+    return;
+  }
+  // fp64 runs at a small fraction of the fp32 rate: one thread's work
+  if (threadIdx.x == 0) {
+    const double c = fmin(1.4426950408889634 / (double)temp, 1e30);
+    s.ch = (float)c;
+    s.cl = (float)(c - (double)s.ch);
+    const double l = has_m ? fmax(-log2((double)min_p), 0.0) : 0.0;
+    s.mh = (float)l;
+    s.ml = (float)(l - (double)s.mh);
+    sh.scale = s;
+  }
+  __syncthreads();
+  s = sh.scale;
+
+  // ---- B: histogram over the row; its mass when the row has no top-k
+  const bool need_total = has_p && !has_k;
+  {
+    u64 sum = 0;
+    for_range(z, i0, i1, [&](float v, int) {
+      float pp, e;
+      octaves(s, v, pp, e);
+      const int n = bin_of(pp);
+      if (n < kBins) {
+        atomicAdd(&sh.cnt[n], 1u);
+        if (need_total) sum += weight_of(mantissa(pp, e, n), n);
+      }
+    });
+    u64 tot;
+    block_incl(sum, sh.red, &tot);
+    if (threadIdx.x == 0) sh.total = tot;
+  }
+  cluster_sync();
+  u64 total = 0;
+  for (uint32_t r = 0; r < ctas; ++r) total += ld_cluster_u64(tc::cluster_addr(&sh.total, r));
+  int last;            // last bin that S can reach
+  uint32_t n_cand;     // elements up to it
+  {
+    u64 cnt[2], mant[2];
+    merge_bins(sh, ctas, false, cnt, mant);
+    u64 all;
+    const u64 incl = block_incl(cnt[0] + cnt[1], sh.red, &all);
+    const u64 c0 = incl - cnt[1], c1 = incl;   // elements up to bin 2 tid and 2 tid + 1
+    // bounds on the mass of the bins: 2^-((n + 1)/8) .. 2^-(n/8) per element
+    const int b0 = 2 * threadIdx.x;
+    const float h0 = exp2f(-0.125f * b0), q = 0.91700404f;   // 2^(-1/8)
+    float mass = 0.f, mtot;
+    {
+      const float lower = ((float)cnt[0] + (float)cnt[1] * q) * h0 * q * 0.9999f;
+      const float li = block_incl(lower, reinterpret_cast<float*>(sh.red32), &mtot);
+      mass = li;
+    }
+    const float m0 = mass - (float)cnt[1] * q * q * h0;   // up to bin b0 (a little less)
+    // The first bin where one of the sets must have ended.  With both top-k and
+    // top-p the mass of all of S_k is wanted, so only top-k ends it.
+    const float target = has_p ? top_p * ((float)total * 2.2737368e-13f) * 1.0002f : CUDART_INF_F;
+    const float mbin = has_m ? s.mh * 8.f + 1.f : 2000.f;
+    const bool k_only = has_k && has_p;
+    const bool e0 = (has_k && c0 >= (u64)k_in) || c0 == all || (!k_only && (m0 >= target || (float)b0 >= mbin));
+    const bool e1 = (has_k && c1 >= (u64)k_in) || c1 == all || (!k_only && (mass >= target || (float)(b0 + 1) >= mbin));
+    int mine = e0 ? b0 : e1 ? b0 + 1 : kBins - 1;
+    mine = __reduce_min_sync(0xffffffffu, mine);
+    __syncthreads();
+    if (lane == 0) sh.red32[warp] = (uint32_t)mine;
+    __syncthreads();
+    last = kBins - 1;
+    for (int w = 0; w < kWarpsS; ++w) last = min(last, (int)sh.red32[w]);
+    if (b0 == (last & ~1)) sh.scan_total = (last & 1) ? c1 : c0;
+    __syncthreads();
+    n_cand = (uint32_t)sh.scan_total;
+  }
+
+  if (n_cand <= (uint32_t)kCap) {
+    // ---- C: the candidates into the leader
+    const uint32_t list0 = tc::cluster_addr(sh.list, 0), count0 = tc::cluster_addr(&sh.n_list, 0);
+    for_range(z, i0, i1, [&](float v, int i) {
+      float pp, e;
+      octaves(s, v, pp, e);
+      if (bin_of(pp) <= last) {
+        uint32_t at;
+        asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(count0) : "memory");
+        const u64 c = ((u64)~key_of(v) << 32) | (uint32_t)i;
+        if (at < (uint32_t)kCap) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list0 + 8 * at), "l"(c) : "memory");
+      }
+    });
+    cluster_sync();
+    if (rank != 0) return;   // only the leader's own memory is used from here
+    const int n = (int)min(n_cand, (uint32_t)kCap);
+    int n2 = 32;
+    while (n2 < n) n2 <<= 1;
+    for (int i = n + threadIdx.x; i < n2; i += kThr) sh.list[i] = ~0ull;
+    bitonic(sh.list, n2);
+    // cut: thread i holds elements 2 i and 2 i + 1
+    constexpr int kPer = kCap / kThr;
+    u64 w[kPer], mass_k = 0, sum = 0;
+    const int nk = has_k ? min(n, k_in) : n;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = kPer * threadIdx.x + j;
+      w[j] = i < nk ? weight(s, logit_of(~(uint32_t)(sh.list[i] >> 32))) : 0ull;
+      sum += w[j];
+    }
+    const u64 incl = block_incl(sum, sh.red, &mass_k);
+    if (threadIdx.x == 0)   // kept while the mass before it is below this
+      sh.goal = has_p ? (u64)ceil((double)top_p * (double)(has_k ? mass_k : total)) : ~0ull;
+    __syncthreads();
+    const u64 limit = sh.goal;
+    u64 before = incl - sum;
+    int keep = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = kPer * threadIdx.x + j;
+      const bool k = i < nk && (i == 0 || (before < limit && (!has_m || passes_minp(s, logit_of(~(uint32_t)(sh.list[i] >> 32))))));
+      before += w[j];
+      keep += k;
+    }
+    keep = (int)__reduce_add_sync(0xffffffffu, (unsigned)keep);
+    __syncthreads();
+    if (lane == 0) sh.red32[warp] = (uint32_t)keep;
+    __syncthreads();
+    keep = 0;
+    for (int x = 0; x < kWarpsS; ++x) keep += (int)sh.red32[x];
+    // back in vocabulary order: index in the upper half
+    n2 = 32;
+    while (n2 < keep) n2 <<= 1;
+    for (int i = threadIdx.x; i < n2; i += kThr) {
+      const u64 c = sh.list[i];
+      sh.list[i] = i < keep ? (c << 32) | (c >> 32) : ~0ull;
+    }
+    bitonic(sh.list, n2);
+    sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = kPer * threadIdx.x + j;
+      w[j] = i < keep ? weight(s, logit_of(~(uint32_t)sh.list[i])) : 0ull;
+      sum += w[j];
+    }
+    u64 mass;
+    u64 run = block_incl(sum, sh.red, &mass) - sum;
+    if (threadIdx.x == 0) sh.goal = min((u64)floor((double)u * (double)mass), mass - 1);
+    __syncthreads();
+    const u64 goal = sh.goal;   // the token's running mass is the first above it
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = kPer * threadIdx.x + j;
+      if (i < keep && run <= goal && run + w[j] > goal) {
+        p.token[row] = (int)(sh.list[i] >> 32);
+        if (p.logprob) p.logprob[row] = (float)log((double)w[j] / (double)mass);
+      }
+      run += w[j];
+    }
+    return;
+  }
+
+  // ---- D: the threshold by refinement.  Kept: key > thr_key, and the first
+  // thr_ties (by index) of those equal to it.
+  uint32_t thr_key = 0;
+  u64 thr_ties = ~0ull;
+  if (has_k || has_p) {
+    // histogram with masses
+    cluster_sync();   // every CTA has read the counts
+    clear_bins(sh);
+    __syncthreads();
+    for_range(z, i0, i1, [&](float v, int) {
+      float pp, e;
+      octaves(s, v, pp, e);
+      const int n = bin_of(pp);
+      if (n < kBins) add_to_bin(sh, n, mantissa(pp, e, n));
+    });
+    cluster_sync();
+    u64 cnt[2], mant[2];
+    merge_bins(sh, ctas, true, cnt, mant);
+    u64 mass[2] = {bin_mass(mant[0], 2 * threadIdx.x), bin_mass(mant[1], 2 * threadIdx.x + 1)};
+    u64 dummy;
+    const u64 cnt_incl = block_incl(cnt[0] + cnt[1], sh.red, &dummy);
+    const u64 mass_incl = block_incl(mass[0] + mass[1], sh.red, &dummy);
+
+    // Descends into one bin until a single key is left.  by_mass: the first
+    // element whose mass including it reaches `goal`; else the goal-th element.
+    auto descend = [&](bool by_mass, u64 goal, u64* mass_out) {
+      // the crossing bin of the first level
+      __syncthreads();
+      if (threadIdx.x == 0) sh.cross_bin = -1;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u64 c_in = j ? cnt_incl : cnt_incl - cnt[1], m_in = j ? mass_incl : mass_incl - mass[1];
+        const u64 c_ex = c_in - cnt[j], m_ex = m_in - mass[j];
+        const bool hit = by_mass ? m_ex < goal && m_in >= goal : c_ex < goal && c_in >= goal;
+        if (hit) sh.cross_bin = 2 * threadIdx.x + j, sh.cross_cnt = (uint32_t)c_ex, sh.cross_mass = m_ex;
+      }
+      __syncthreads();
+      const int bin = sh.cross_bin;
+      if (bin < 0) {   // the goal lies behind everything that counts
+        thr_key = 0, thr_ties = ~0ull;
+        *mass_out = dummy;
+        return;
+      }
+      u64 c_before = sh.cross_cnt, m_before = sh.cross_mass;
+      // the keys of the bin: from the smallest z with p*8 >= bin .. ; the range
+      // is found by bisection on the key, as bin_of is monotone in z
+      uint32_t k_lo, k_hi;   // keys of the bin: [k_lo, k_hi]
+      {
+        const uint32_t top_key = key_of(s.top), inf_key = key_of(-CUDART_INF_F);
+        auto bin_at = [&](uint32_t k) {
+          float pp, e;
+          octaves(s, logit_of(k), pp, e);
+          return bin_of(pp);
+        };
+        uint32_t a = inf_key, b = top_key;   // smallest key with bin_at <= bin
+        while (a < b) {
+          const uint32_t mid = a + ((b - a) >> 1);
+          if (bin_at(mid) <= bin) b = mid; else a = mid + 1;
+        }
+        k_lo = a;
+        a = k_lo, b = top_key;               // largest key with bin_at >= bin
+        while (a < b) {
+          const uint32_t mid = b - ((b - a) >> 1);
+          if (bin_at(mid) >= bin) a = mid; else b = mid - 1;
+        }
+        k_hi = a;
+      }
+      for (;;) {
+        const uint32_t width = k_hi - k_lo;   // keys - 1
+        int shift = 0;
+        while ((width >> shift) >= (uint32_t)kBins) ++shift;
+        cluster_sync();   // every CTA has read the last histogram
+        clear_bins(sh);
+        __syncthreads();
+        for_range(z, i0, i1, [&](float v, int) {
+          const uint32_t k = key_of(v);
+          if (k >= k_lo && k <= k_hi) {
+            float pp, e;
+            octaves(s, v, pp, e);
+            add_to_bin(sh, (int)((k_hi - k) >> shift), mantissa(pp, e, bin));
+          }
+        });
+        cluster_sync();
+        u64 c[2], m[2];
+        merge_bins(sh, ctas, true, c, m);
+        u64 t;
+        const u64 ci = block_incl(c[0] + c[1], sh.red, &t);
+        const u64 m_sub[2] = {bin_mass(m[0], bin), bin_mass(m[1], bin)};
+        const u64 mi = block_incl(m_sub[0] + m_sub[1], sh.red, &t);
+        if (threadIdx.x == 0) sh.cross_bin = -1;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const u64 c_in = c_before + (j ? ci : ci - c[1]), m_in = m_before + (j ? mi : mi - m_sub[1]);
+          const u64 c_ex = c_in - c[j], m_ex = m_in - m_sub[j];
+          const bool hit = by_mass ? m_ex < goal && m_in >= goal : c_ex < goal && c_in >= goal;
+          if (hit) sh.cross_bin = 2 * threadIdx.x + j, sh.cross_cnt = (uint32_t)c_ex, sh.cross_mass = m_ex;
+        }
+        __syncthreads();
+        int sub = sh.cross_bin;
+        if (sub < 0) {   // rounding of the bin masses: the goal is the bin's very end
+          // the last occupied sub-bin
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (c[j]) atomicMax(&sh.cross_bin, 2 * (int)threadIdx.x + j);
+          __syncthreads();
+          sub = sh.cross_bin;
+          if (2 * (int)threadIdx.x == (sub & ~1)) {
+            const int j = sub & 1;
+            sh.cross_cnt = (uint32_t)(c_before + (j ? ci : ci - c[1]) - c[j]);
+            sh.cross_mass = m_before + (j ? mi : mi - m_sub[1]) - m_sub[j];
+          }
+          __syncthreads();
+        }
+        c_before = sh.cross_cnt, m_before = sh.cross_mass;
+        const uint32_t hi = k_hi - ((uint32_t)sub << shift);
+        const uint32_t span = (1u << shift) - 1u;
+        k_lo = hi - k_lo > span ? hi - span : k_lo;
+        k_hi = hi;
+        if (shift == 0) {
+          thr_key = k_hi;
+          float pp, e;
+          octaves(s, logit_of(k_hi), pp, e);
+          const u64 w = weight_of(mantissa(pp, e, bin), bin);
+          const u64 rest = goal > (by_mass ? m_before : c_before) ? goal - (by_mass ? m_before : c_before) : 1ull;
+          thr_ties = by_mass ? (w ? (rest + w - 1) / w : ~0ull) : rest;
+          *mass_out = m_before + w * (by_mass ? 0ull : thr_ties);
+          return;
+        }
+      }
+    };
+    u64 mass_k = dummy;
+    if (has_k) descend(false, (u64)k_in, &mass_k);
+    if (has_p) {
+      const uint32_t kk = thr_key;
+      const u64 kt = thr_ties;
+      u64 unused;
+      __syncthreads();
+      if (threadIdx.x == 0) sh.goal = max((u64)ceil((double)top_p * (double)(has_k ? mass_k : total)), 1ull);
+      __syncthreads();
+      descend(true, sh.goal, &unused);
+      if (has_k && (thr_key < kk || (thr_key == kk && thr_ties > kt))) thr_key = kk, thr_ties = kt;
+    }
+  }
+
+  // masses and ties of the segments of this CTA's range
+  cluster_sync();   // sh.list / sh.seg are free, every histogram read
+  const int n_seg = (i1 - i0 + kSeg - 1) / kSeg;
+  auto kept = [&](float v) { return key_of(v) > thr_key && (!has_m || passes_minp(s, v)); };
+  auto tied = [&](float v) { return key_of(v) == thr_key && thr_key != 0 && (!has_m || passes_minp(s, v)); };
+  for (int g = warp; g < n_seg; g += kWarpsS) {
+    u64 sum = 0;
+    uint32_t ties = 0;
+#pragma unroll
+    for (int j = 0; j < kSeg / 32; ++j) {
+      const int i = i0 + g * kSeg + j * 32 + lane;
+      if (i < i1) {
+        const float v = load_logit(z + i);
+        if (kept(v)) sum += weight(s, v);
+        ties += tied(v);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    if (lane == 0) sh.seg[g] = sum, sh.tie[g] = ties;
+  }
+  __syncthreads();
+  // prefix of the ties: how many of a segment's are kept
+  constexpr int kPerS = kMaxSegs / kThr;
+  u64 t_sum = 0, m_sum = 0;
+  for (int j = 0; j < kPerS; ++j) {
+    const int g = threadIdx.x * kPerS + j;
+    if (g < n_seg) t_sum += sh.tie[g], m_sum += sh.seg[g];
+  }
+  u64 cta_ties, cta_mass;
+  u64 t_run = block_incl(t_sum, sh.red, &cta_ties) - t_sum;
+  if (threadIdx.x == 0) sh.ties = (uint32_t)cta_ties;
+  cluster_sync();
+  for (uint32_t r = 0; r < rank; ++r) t_run += ld_cluster_u32(tc::cluster_addr(&sh.ties, r));
+  const u64 w_tie = thr_key ? weight(s, logit_of(thr_key)) : 0ull;
+  const u64 t_first = t_run;
+  m_sum = 0;
+  for (int j = 0; j < kPerS; ++j) {
+    const int g = threadIdx.x * kPerS + j;
+    if (g < n_seg) {
+      const u64 left = thr_ties > t_run ? thr_ties - t_run : 0ull;
+      t_run += sh.tie[g];
+      sh.seg[g] += w_tie * min((u64)sh.tie[g], left);
+      m_sum += sh.seg[g];
+    }
+  }
+  u64 m_run = block_incl(m_sum, sh.red, &cta_mass) - m_sum;
+  if (threadIdx.x == 0) sh.mine = cta_mass;
+  cluster_sync();
+  u64 mass = 0, before = 0;
+  for (uint32_t r = 0; r < ctas; ++r) {
+    const u64 t = ld_cluster_u64(tc::cluster_addr(&sh.mine, r));
+    if (r < rank) before += t;
+    mass += t;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) sh.goal = min((u64)floor((double)u * (double)mass), mass - 1);
+  m_run += before;
+  t_run = t_first;
+  if (threadIdx.x == 0) sh.cross_bin = -1;
+  __syncthreads();
+  const u64 goal = sh.goal;
+  for (int j = 0; j < kPerS; ++j) {
+    const int g = threadIdx.x * kPerS + j;
+    if (g < n_seg) {
+      if (m_run <= goal && m_run + sh.seg[g] > goal) {
+        sh.cross_bin = g;
+        sh.cross_mass = m_run;
+        sh.scan_total = t_run;
+      }
+      m_run += sh.seg[g];
+      t_run += sh.tie[g];
+    }
+  }
+  __syncthreads();
+  if (warp == 0 && sh.cross_bin >= 0) {
+    u64 run = sh.cross_mass, ties = sh.scan_total;
+    bool done = false;
+    for (int j = 0; j < kSeg / 32 && !done; ++j) {
+      const int i = i0 + sh.cross_bin * kSeg + j * 32 + lane;
+      u64 w = 0;
+      bool tie = false;
+      if (i < i1) {
+        const float v = load_logit(z + i);
+        if (kept(v)) w = weight(s, v);
+        tie = tied(v);
+      }
+      const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie);
+      if (tie && ties + __popc(tie_mask & ((1u << lane) - 1u)) < thr_ties) w = w_tie;
+      ties += __popc(tie_mask);
+      const u64 incl = warp_incl(w) + run;
+      if (incl > goal && incl - w <= goal) {
+        p.token[row] = i;
+        if (p.logprob) p.logprob[row] = (float)log((double)w / (double)mass);
+      }
+      run = __shfl_sync(0xffffffffu, incl, 31);
+      done = run > goal;
+    }
+  }
+  cluster_sync();   // no CTA leaves while another reads its shared memory
+}
+
+template <typename T>
+static int launch(const Params& p, int rows, int cluster, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster, rows);
+  cfg.blockDim = dim3(kThr);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
+  return e == cudaSuccess ? Q4_OK : cuda_fail(e, "sampling launch");
+}
+
+}  // namespace sample
+
+int launch_logits_sample(const void* z, long long stride, int dtype, int rows, int V, const float* u,
+                         const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                         int32_t* token, float* logprob, const DeviceInfo& dev, cudaStream_t s) {
+  (void)dev;
+  sample::Params p = {z, stride, u, temperature, top_k, top_p, min_p, token, logprob, V, 0};
+  const int cluster = V > 16384 ? 8 : V > 4096 ? 2 : 1;
+  const int segs = (V + sample::kSeg * cluster - 1) / (sample::kSeg * cluster);
+  p.range = segs * sample::kSeg;
+  return dtype == Q4_F32   ? sample::launch<float>(p, rows, cluster, s)
+         : dtype == Q4_F16 ? sample::launch<__half>(p, rows, cluster, s)
+                           : sample::launch<__nv_bfloat16>(p, rows, cluster, s);
+}
+
+}  // namespace q4w

@@ -1,0 +1,163 @@
+"""logits_sample against the fp64 oracle: tokens exactly, log probabilities to
+the rounding of an fp32 (eps/2 of the value) and the weights' 2^-28."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+def check(q4w, z, u, t=None, k=None, p=None, m=None):
+    """z [b, V] on the GPU; scalars stand for every row."""
+    b = z.shape[0]
+    dev = lambda x, dt: None if x is None else (x if torch.is_tensor(x) else torch.full((b,), x, dtype=dt, device="cuda"))   # noqa: E731
+    t, k, p, m = dev(t, F32), dev(k, torch.int32), dev(p, F32), dev(m, F32)
+    tok, lp = q4w.logits_sample(z, u, t, k, p, m)
+    torch.cuda.synchronize()
+    zh = z.float().cpu().numpy()
+    at = lambda x, i: None if x is None else x[i].item()   # noqa: E731
+    for i in range(b):
+        rt, rl, _ = O.sample(zh[i], u[i].item(), at(t, i), at(k, i), at(p, i), at(m, i))
+        assert int(tok[i]) == rt, (i, int(tok[i]), rt)
+        if rl == -np.inf:
+            assert float(lp[i]) == -np.inf
+        else:
+            assert abs(float(lp[i]) - rl) <= 2.0 ** -24 * abs(rl) + 2.0 ** -26, (i, float(lp[i]), rl)
+    return tok, lp
+
+
+def rows(b, V, seed=0, dtype=F32, std=2.5):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(b, V, generator=g, device="cuda") * std).to(dtype), torch.rand(b, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("V", [1, 2, 31, 128, 129, 1000, 5003, 20001])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("kw", [dict(), dict(k=40), dict(p=0.9), dict(m=0.05), dict(k=50, p=0.95, t=0.7), dict(k=3000, p=0.9, m=0.001, t=1.5)])
+def test_filters(cuda_lib, V, dtype, kw):
+    z, u = rows(5, V, seed=V, dtype=dtype)
+    check(cuda_lib, z, u, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(t=3.0), dict(t=2.0, p=0.99), dict(k=100000, t=2.0), dict(k=100000, p=0.9, t=2.0), dict(t=2.0, m=1e-4), dict(t=1.0, k=64, p=0.95)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_wide_sets_of_a_large_vocabulary(cuda_lib, kw, dtype):
+    z, u = rows(3, 262144, seed=7, dtype=dtype)
+    check(cuda_lib, z, u, **kw)
+
+
+@pytest.mark.parametrize("V", [1000, 40000, 262144])
+def test_equal_logits(cuda_lib, V):
+    """Ties: the set is the lowest indices, the token the index that u points at."""
+    z = torch.full((6, V), 3.25, device="cuda")
+    u = torch.tensor([0.0, 0.25, 0.5, 0.75, 0.999, 1 - 2.0 ** -24], device="cuda")
+    for kw, n in ((dict(), V), (dict(k=V // 3), V // 3), (dict(p=0.25), V // 4), (dict(m=1.0), V)):
+        tok, lp = cuda_lib.logits_sample(z, u, None, *(torch.full((6,), kw[x], dtype=d, device="cuda") if x in kw else None
+                                                        for x, d in (("k", torch.int32), ("p", F32), ("m", F32))))
+        torch.cuda.synchronize()
+        want = [min(int(np.floor(float(x) * n)), n - 1) for x in u]
+        assert tok.tolist() == want, kw
+        assert np.allclose(lp.cpu().numpy(), -np.log(n), rtol=2.0 ** -23)
+
+
+def test_many_ties_at_the_border(cuda_lib):
+    """Logits on a coarse grid: thousands of equal ones at each border."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    z = torch.randint(0, 12, (4, 50000), generator=g, device="cuda").float()
+    u = torch.rand(4, generator=g, device="cuda")
+    for kw in (dict(k=5000), dict(p=0.5), dict(k=9000, p=0.7), dict(k=1500, m=0.5), dict(t=4.0, p=0.8)):
+        check(cuda_lib, z, u, **kw)
+
+
+@pytest.mark.parametrize("V", [70, 3001, 200000])
+def test_infinities_and_nan(cuda_lib, V):
+    z, u = rows(8, V, seed=9)
+    z[0, :] = float("-inf")
+    z[1, :] = float("nan")
+    z[2, 5:] = float("-inf")                       # a grammar that leaves five
+    z[3, ::2] = float("nan")
+    z[4, 11] = float("inf")
+    z[5, 7] = z[5, 60] = float("inf")
+    z[6, :] = torch.finfo(F32).min                 # masks of the type's lowest value
+    z[6, 3] = 1.0
+    z[7, :] = torch.finfo(F32).min
+    check(cuda_lib, z, u)
+    check(cuda_lib, z, u, k=20, p=0.9)
+    check(cuda_lib, z, u, p=0.5, t=0.1)
+    check(cuda_lib, z, u, m=0.1, t=5.0)
+    check(cuda_lib, z, u, k=V - 1)
+
+
+def test_greedy_and_extreme_settings(cuda_lib):
+    z, u = rows(4, 9000, seed=4, std=1.0)
+    z[1, 77] = z[1, 400] = 9.0
+    for kw in (dict(t=0.0), dict(t=-1.0), dict(k=1), dict(p=0.0), dict(t=1e-30), dict(t=float("inf")), dict(t=1e30, k=10),
+               dict(t=1e-4, p=0.5), dict(m=1.0), dict(m=1e-30), dict(k=9000), dict(k=2 ** 31 - 1), dict(k=-3), dict(p=2.0), dict(p=1e-20)):
+        check(cuda_lib, z, u, **kw)
+    tok, lp = cuda_lib.logits_sample(z, u, torch.full((4,), float("nan"), device="cuda"))
+    assert tok.tolist() == z.argmax(1).tolist() and lp.tolist() == [0.0] * 4
+    # u outside [0, 1) is clamped
+    edge = torch.tensor([-1.0, 1.0, 5.0, float("nan")], device="cuda")
+    tok, _ = cuda_lib.logits_sample(z, edge, top_k=torch.full((4,), 10, dtype=torch.int32, device="cuda"))
+    for i, x in enumerate((0.0, 1 - 2.0 ** -24, 1 - 2.0 ** -24, 0.0)):
+        assert int(tok[i]) == O.sample(z[i].cpu().numpy(), x, top_k=10)[0]
+
+
+def test_signed_zeros_tie(cuda_lib):
+    z = torch.zeros(1, 300, device="cuda")
+    z[0, ::2] = -0.0
+    for x, want in ((0.0, 0), (0.99, 9)):
+        tok, _ = cuda_lib.logits_sample(z, torch.tensor([x], device="cuda"), top_k=torch.tensor([10], dtype=torch.int32, device="cuda"))
+        assert int(tok) == want
+
+
+def test_rows_with_their_own_settings_strides_streams_graphs(cuda_lib):
+    q4w = cuda_lib
+    z, u = rows(9, 30007, seed=11)
+    i = torch.arange(9, device="cuda")
+    k = torch.tensor([0, 64, 1, 2000, 0, 40, 0, 30006, 5], dtype=torch.int32, device="cuda")
+    p = torch.tensor([0.9, 0.95, 1.0, 0.8, 1.0, 0.5, 0.99, 1.0, 0.1], device="cuda")
+    m = torch.tensor([0.0, 0.0, 0.0, 0.01, 0.02, 0.3, 0.0, 0.0, 0.9], device="cuda")
+    t = 0.5 + 0.25 * i.float()
+    tok, lp = check(q4w, z, u, t, k, p, m)
+    wide = torch.zeros(9, 30100, device="cuda")
+    wide[:, 33:33 + 30007] = z
+    with pytest.raises(q4w.Q4Error):
+        q4w.logits_sample(wide[:, 33:33 + 30007], u, t, k, p, m)        # not 16-byte aligned
+    wide[:, 32:32 + 30007] = z
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        tok2, lp2 = q4w.logits_sample(wide[:, 32:32 + 30007], u, t, k, p, m)
+    torch.cuda.synchronize()
+    assert torch.equal(tok, tok2) and torch.equal(lp, lp2)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q4w.logits_sample(z, u, t, k, p, m, tokens=tok2, logprobs=lp2)
+    u.copy_(torch.rand_like(u))
+    g.replay()
+    torch.cuda.synchronize()
+    tok, lp = check(q4w, z, u, t, k, p, m)
+    assert torch.equal(tok, tok2) and torch.equal(lp, lp2)
+
+
+def test_frequencies_follow_the_distribution(cuda_lib):
+    """Evenly spread u: each token is drawn in proportion to its probability."""
+    z = torch.tensor([0.1, 0.4, 0.1, 0.3, 0.1], device="cuda").log()
+    n = 10000
+    u = (torch.arange(n, device="cuda") + 0.5) / n
+    tok, _ = cuda_lib.logits_sample(z.expand(n, 5).contiguous(), u)
+    got = torch.bincount(tok.long(), minlength=5).tolist()
+    assert all(abs(a - n * b) <= 1 for a, b in zip(got, (0.1, 0.4, 0.1, 0.3, 0.1)))
+
+
+def test_largest_vocabulary(cuda_lib):
+    z, u = rows(1, 1048576, seed=12)
+    check(cuda_lib, z, u, t=2.0)
+    check(cuda_lib, z, u, k=500000, p=0.9, t=2.0)
