@@ -33,6 +33,7 @@ Q4_OP_GEMV, Q4_OP_GEMM_CHUNK, Q4_OP_PLE, Q4_OP_LMHEAD, Q4_OP_DECODE_PASS, Q4_OP_
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4_dtype
 
 _lib = None
+_one_device = False   # set by load(): asking for the current device costs 1 us a tensor
 
 vp = ctypes.c_void_p
 ci = ctypes.c_int
@@ -102,7 +103,7 @@ def build(force: bool = False) -> str:
 
 def load():
     """Load libq4w.so (raises if it is missing: there is no fallback path)."""
-    global _lib
+    global _lib, _one_device
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -113,6 +114,7 @@ def load():
         fn.restype = res
         fn.argtypes = args
     _lib = lib
+    _one_device = torch.cuda.device_count() == 1
     return lib
 
 
@@ -124,11 +126,17 @@ def _check(status: int, name: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream's handle without building a Stream object
+    return torch._C._cuda_getCurrentRawStream(0 if _one_device else torch.cuda.current_device())
+
+
+def _here(t):
+    """Whether t is on the current CUDA device (the only one there is, as a rule)."""
+    return t.is_cuda and t.device.index == (0 if _one_device else torch.cuda.current_device())
 
 
 def _numel(t, n, name):
@@ -140,6 +148,8 @@ def _numel(t, n, name):
 
 def _dev(t, dtype, name):
     if t is None:
+        return
+    if t.dtype is dtype and _here(t) and t.is_contiguous():
         return
     if not t.is_cuda:
         raise Q4Error(f"{name} must be a CUDA tensor")
@@ -576,29 +586,36 @@ def kv_rope_steps(rot_dim, theta=10000.0, device="cuda", freqs=None):
 
 def _heads(t, dtype, heads, dim, T, name):
     """A [T, heads, dim] tensor whose heads and elements are contiguous; returns the token stride."""
-    if t.dim() != 3 or tuple(t.shape) != (T, heads, dim):
+    if t.dtype is not dtype or not _here(t):
+        _dev(t[:0], dtype, name)   # names the fault
+    if t.shape != (T, heads, dim):
         raise Q4Error(f"{name} has shape {tuple(t.shape)}; the sizes imply ({T}, {heads}, {dim})")
-    _dev(t[0], dtype, name)   # checks the device, the type and that a token's heads are contiguous
-    return t.stride(0) if T > 1 else heads * dim
+    st, sh, se = t.stride()
+    if se != 1 or (sh != dim and heads > 1):
+        raise Q4Error(f"{name}: the heads and elements of a token must be contiguous, its strides are {(st, sh, se)}")
+    return st if T > 1 else heads * dim
 
 
 def _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens):
-    if k_cache.dtype not in (torch.float16, torch.bfloat16):
-        raise Q4Error(f"k_cache must be torch.float16 or torch.bfloat16, got {k_cache.dtype}")
-    _dev(k_cache, k_cache.dtype, "k_cache")
-    _dev(v_cache, k_cache.dtype, "v_cache")
-    for t, nm in ((block_table, "block_table"), (cu_tokens, "cu_tokens"), (kv_lens, "kv_lens")):
-        _dev(t, torch.int32, nm)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise Q4Error(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} must both be "
+    dtype = k_cache.dtype
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise Q4Error(f"k_cache must be torch.float16 or torch.bfloat16, got {dtype}")
+    _dev(k_cache, dtype, "k_cache")
+    _dev(v_cache, dtype, "v_cache")
+    _dev(block_table, torch.int32, "block_table")
+    _dev(cu_tokens, torch.int32, "cu_tokens")
+    _dev(kv_lens, torch.int32, "kv_lens")
+    shape, tshape = k_cache.shape, block_table.shape
+    if len(shape) != 4 or shape != v_cache.shape:
+        raise Q4Error(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} must both be "
                       "[n_pages, n_kv, page_size, head_dim]")
     n = kv_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != n:
-        raise Q4Error(f"block_table has shape {tuple(block_table.shape)}; kv_lens implies ({n}, max_pages)")
+    if len(tshape) != 2 or tshape[0] != n:
+        raise Q4Error(f"block_table has shape {tuple(tshape)}; kv_lens implies ({n}, max_pages)")
     _numel(cu_tokens, n + 1, "cu_tokens")
-    pages, heads, page, dim = k_cache.shape
+    pages, heads, page, dim = shape
     return q4_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_tokens.data_ptr(),
-                       kv_lens.data_ptr(), _DTYPES[k_cache.dtype], pages, heads, page, dim, n, block_table.shape[1])
+                       kv_lens.data_ptr(), _DTYPES[dtype], pages, heads, page, dim, n, tshape[1])
 
 
 def kv_append(k, v, k_cache, v_cache, block_table, cu_tokens, kv_lens, steps=None, q=None, positions=None,
@@ -687,7 +704,10 @@ def logits_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
     logprobs = torch.empty(b, dtype=torch.float32, device=logits.device) if logprobs is None else logprobs
     if b == 0:
         return tokens, logprobs
-    _dev(logits[0], logits.dtype, "logits")
+    if not _here(logits):
+        _dev(logits[:0], logits.dtype, "logits")   # names the fault
+    if V > 1 and logits.stride(1) != 1:
+        raise Q4Error(f"a row of logits must be contiguous, the strides are {tuple(logits.stride())}")
     for t, dt, nm in ((u, torch.float32, "u"), (temperature, torch.float32, "temperature"),
                       (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"),
                       (min_p, torch.float32, "min_p"), (tokens, torch.int32, "tokens"),

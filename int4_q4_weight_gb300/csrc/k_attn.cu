@@ -102,12 +102,12 @@ static int launch_t(const AttnParams& p, int D, cudaStream_t s) {
 }  // namespace attn
 
 size_t attn_ws_bytes(int max_rows, int D, int n_seqs, const DeviceInfo& dev) {
-  (void)max_rows, (void)D, (void)n_seqs, (void)dev;
-  return 0;
+  (void)n_seqs;
+  return attn_decode_fits(max_rows, D) ? attn_decode_ws_bytes(max_rows, D, dev) : 0;
 }
 
 int launch_kv_attention(const AttnParams& p, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s) {
-  (void)ws, (void)dev;
+  if (attn_decode_fits(p.max_q * (p.n_q / c.n_kv), c.head_dim)) return launch_attn_decode(p, c, ws, dev, s);
   return c.dtype == Q4_F16 ? attn::launch_t<__half>(p, c.head_dim, s)
                            : attn::launch_t<__nv_bfloat16>(p, c.head_dim, s);
 }

@@ -1,0 +1,661 @@
+// Attention of few query rows per KV head over a paged cache (decode, and a few
+// drafted tokens): rows = new tokens x query heads of the group <= 8 NT.
+//
+// Mathematics: one pass over the keys with the running maximum and sum of a
+// softmax (scores in units of log2 e, so that e^s is one 2^x); the maximum is
+// moved only when a score passes it by 2^8, so that most steps rescale nothing.
+// The final division makes the result independent of that choice.
+//
+// Bound: HBM.  A 16-bit cache element takes part in 8 to 64 multiply-adds, too
+// many for the CUDA cores at 6.8 TB/s (3.4e12 elements/s x 8 x 2 is 54 TFLOP/s)
+// and too few to fill a 128-row tensor tile, so the keys are the M rows of
+// m16n8k16 (no row is padding at 8 query rows) and the query rows its N:
+//   S^T[16 keys][8 rows]   = K[16][D] Q^T         (K by ldmatrix as it lies)
+//   O^T[D][8 rows]        += V^T[D][16] P^T       (V by transposing ldmatrix)
+// P^T is S^T's own registers after a transposition of 8x8 blocks in registers.
+// Every warp streams its own units of 16 keys (K, then V) through a private
+// ring of TMA boxes in the 128-byte swizzle and synchronises with no other warp
+// until its CTA's part of the keys is done; 192 KB are in flight on an SM.
+//
+// Split: one CTA per SM.  The steps (one unit per warp) of all (sequence, KV
+// head) pairs form one line that is cut into equal shares, so ragged lengths
+// and a single long sequence fill the device alike.  A pair that one CTA has
+// whole is written out there; else its parts go to the workspace and a second
+// kernel, launched ahead (programmatic dependent launch), joins them in the
+// order of the keys: the same lengths give the same bits.
+#include <math_constants.h>
+
+#include "q4w_device.cuh"
+#include "q4w_internal.cuh"
+#include "q4w_kv.cuh"
+#include "q4w_tc.cuh"
+
+namespace q4w {
+namespace dec {
+
+constexpr int kUnit = 16;              // keys per unit
+constexpr int kRingBytes = 196608;     // of a CTA
+
+template <int D>
+struct Shape {
+  static constexpr int kWarps = D == 512 ? 4 : 8;
+  static constexpr int kSlotBytes = kUnit * D * 2;
+  static constexpr int kSlots = kRingBytes / kWarps / kSlotBytes;   // 3, 3, 6, 12: K and V alternate
+  static constexpr int kThr = kWarps * 32;
+  static constexpr int kStep = kWarps * kUnit;                      // keys per step of the CTA
+  static constexpr int kRowPad = D + 4;                             // floats per row of the output staging
+  static constexpr int kMergeBytes = kWarps / 2 * 8 * D * 4;         // half the warps' outputs of 8 rows
+  static_assert(kMergeBytes >= 8 * kRowPad * 4, "the output staging shares it");
+  static constexpr size_t kSmem = 1024 + kRingBytes + kMergeBytes;
+};
+
+struct Params {
+  CUtensorMap tm_k, tm_v;
+  AttnParams a;
+  float* part_o;         // [2 grid][rows][D]
+  float2* part_ml;       // [2 grid][rows]: maximum, sum
+  long long* starts;     // [n_seqs]: first step of each sequence; then the share
+  unsigned* dev_err;
+  long long wait_limit;
+  int group, rows;       // query heads per KV head, 8 NT
+  int total_rows;        // of the cache
+  int grid;
+};
+
+// The part of one sequence's work that its lengths determine.
+struct Seq {
+  int n, pos0;           // new tokens taken, position of the first
+  int base, end;         // keys [base, end), base a multiple of 16
+  int cu;
+};
+
+__device__ __forceinline__ Seq seq_of(const AttnParams& a, int seq) {
+  Seq s;
+  s.cu = a.kv.cu_tokens[seq];
+  const int n = a.kv.cu_tokens[seq + 1] - s.cu, len = max(a.kv.kv_lens[seq], 0);
+  s.n = s.cu >= 0 ? min(min(max(n, 0), a.max_q), max(a.T - s.cu, 0)) : 0;
+  s.pos0 = len - n;
+  s.base = kv_first(s.pos0, a.window) & ~(kUnit - 1);
+  s.end = s.n > 0 ? min(s.pos0 + s.n, a.kv.max_pages * a.kv.page_size) : 0;
+  return s;
+}
+__device__ __forceinline__ bool seq_bad(const AttnParams& a, int seq) {
+  const int n = a.kv.cu_tokens[seq + 1] - a.kv.cu_tokens[seq];
+  return n > a.max_q || (n > 0 && a.kv.kv_lens[seq] > a.kv.max_pages * a.kv.page_size);
+}
+template <int STEP>
+__device__ __forceinline__ int steps_of(const Seq& s) {
+  return s.end > s.base ? (s.end - s.base + STEP - 1) / STEP : 0;
+}
+
+// ------------------------------------------------------------ instructions ---
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A walk over the steps of a CTA's share.
+template <int STEP>
+struct Walk {
+  int seq, head, local, n_local;
+  Seq s;
+  __device__ __forceinline__ void enter(const AttnParams& a) {
+    while (seq < a.kv.n_seqs) {
+      s = seq_of(a, seq);
+      n_local = steps_of<STEP>(s);
+      if (n_local > 0) return;
+      ++seq;
+    }
+  }
+  // One step on; true when a new (sequence, head) begins.
+  __device__ __forceinline__ bool next(const AttnParams& a) {
+    if (++local < n_local) return false;
+    local = 0;
+    if (++head == a.kv.n_kv) {
+      head = 0;
+      ++seq;
+      enter(a);
+    }
+    return true;
+  }
+};
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_constant__ Params p) {
+  using S = Shape<D>;
+  constexpr int W = S::kWarps, SLOTS = S::kSlots, KS = D / 16, SLABS = D / 64;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* merge = reinterpret_cast<float*>(ring + kRingBytes);
+  __shared__ uint64_t bars[W * SLOTS];
+  __shared__ float2 ml_sh[W][8 * NT];
+  __shared__ long long scan_sh[W];
+  __shared__ int start_sh[3];
+  __shared__ int abort_sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const AttnParams& a = p.a;
+
+  for (int i = threadIdx.x; i < W * SLOTS; i += S::kThr) tc::mbar_init(tc::smem_u32(bars + i), 1);
+  if (threadIdx.x == 0) abort_sh = 0, start_sh[0] = a.kv.n_seqs;
+  tc::mbar_fence_init();
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the shares: every thread sums the steps of a run of sequences
+  long long total, share;
+  {
+    const int per = (a.kv.n_seqs + S::kThr - 1) / S::kThr;
+    const int q0 = min((int)threadIdx.x * per, a.kv.n_seqs), q1 = min(q0 + per, a.kv.n_seqs);
+    long long sum = 0;
+    for (int q = q0; q < q1; ++q) sum += (long long)steps_of<S::kStep>(seq_of(a, q)) * a.kv.n_kv;
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) scan_sh[warp] = incl;
+    __syncthreads();
+    total = 0;
+    long long before = incl - sum;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) before += scan_sh[w];
+      total += scan_sh[w];
+    }
+    share = (total + p.grid - 1) / p.grid;
+    const long long mine = share * blockIdx.x;
+    if (blockIdx.x == 0) {
+      if (threadIdx.x == 0) p.starts[a.kv.n_seqs] = share;
+      long long at = before;
+      for (int q = q0; q < q1; ++q) {
+        p.starts[q] = at;
+        at += (long long)steps_of<S::kStep>(seq_of(a, q)) * a.kv.n_kv;
+        if (a.err && seq_bad(a, q)) *a.err = 1;
+      }
+    }
+    if (sum > 0 && mine >= before && mine < before + sum) {
+      long long left = mine - before;
+      int q = q0, n;
+      for (;; ++q) {
+        n = steps_of<S::kStep>(seq_of(a, q));
+        if (left < (long long)n * a.kv.n_kv) break;
+        left -= (long long)n * a.kv.n_kv;
+      }
+      start_sh[0] = q;
+      start_sh[1] = (int)(left / n);
+      start_sh[2] = (int)(left % n);
+    }
+    __syncthreads();
+  }
+  const long long first_step = share * blockIdx.x;
+  const int n_steps = (int)max(0ll, min(share, total - first_step));
+  if (n_steps == 0) return;
+
+  const uint32_t ring0 = tc::smem_u32(ring) + warp * SLOTS * S::kSlotBytes;
+  const uint32_t bar0 = tc::smem_u32(bars) + warp * SLOTS * 8;
+  const uint64_t policy = tc::policy_evict_first();
+  bool dead = false;   // a wait ran out: nothing more is loaded or computed
+
+  Walk<S::kStep> lw;   // of the loads, ahead of the computation
+  lw.seq = start_sh[0], lw.head = start_sh[1], lw.local = start_sh[2];
+  lw.enter(a);
+  Walk<S::kStep> cw = lw;
+
+  // pages of the next 32 units of this warp in the walk's sequence, one per lane
+  int l_step = 0, l_half = 0;        // next load: step of the share, 0 = K, 1 = V
+  int pg_base = -32, pg = -1;
+  int l_row = 0;                     // cache row of the unit, total_rows: out of the cache (zero fill)
+  uint32_t l_slot = 0;               // loads issued
+  auto issue = [&]() {
+    if (l_step >= n_steps || dead) return;
+    const int slot = (int)(l_slot % SLOTS);
+    if (l_half == 0) {
+      if (lw.local < pg_base || lw.local >= pg_base + 32) {
+        pg_base = lw.local;
+        const int pos = lw.s.base + ((pg_base + lane) * W + warp) * kUnit;
+        pg = -1;
+        if (pos < lw.s.end) {
+          pg = kv_page(a.kv, lw.seq, pos);
+          if (pg < 0 && a.err) *a.err = 1;
+        }
+      }
+      const int pos = lw.s.base + (lw.local * W + warp) * kUnit;
+      const int page = __shfl_sync(0xffffffffu, pg, lw.local - pg_base);
+      l_row = page < 0 ? p.total_rows : (int)kv_row(a.kv, page, lw.head) + pos % a.kv.page_size;
+    }
+    if (lane == 0) {
+      const uint32_t bar = bar0 + 8 * slot;
+      tc::mbar_expect_tx(bar, S::kSlotBytes);
+      tc::tma_load_3d(ring0 + slot * S::kSlotBytes, l_half ? &p.tm_v : &p.tm_k, 0, l_row, 0, bar, policy);
+    }
+    ++l_slot;
+    if (l_half) {
+      l_half = 0;
+      ++l_step;
+      if (l_step < n_steps && lw.next(a)) pg_base = -32;
+    } else {
+      l_half = 1;
+    }
+  };
+  for (int i = 0; i < SLOTS; ++i) issue();
+
+  // ---- per (sequence, head): the query rows in registers
+  uint32_t qf[NT][KS][2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
+  const float sc = a.scale * 1.4426950408889634f;
+  auto begin = [&]() {
+    const int R = cw.s.n * p.group;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = 8 * t + (lane >> 2);
+      const bool in = r < R;
+      const int tok = in ? r / p.group : 0;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + (cw.s.cu + tok) * a.q_stride +
+                                                            (long long)(cw.head * p.group + r - tok * p.group) * D);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qf[t][k][0] = in ? q[k * 8 + (lane & 3)] : 0u;
+        qf[t][k][1] = in ? q[k * 8 + 4 + (lane & 3)] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) m[t][j] = -CUDART_INF_F, l[t][j] = 0.f;
+    }
+  };
+  begin();
+
+  uint32_t c_slot = 0;   // slots consumed
+  bool opens = cw.local == 0;
+  for (int step = 0; step < n_steps; ++step) {
+    // ------------------------------------------------ one unit of 16 keys
+    const int k0 = cw.s.base + (cw.local * W + warp) * kUnit;
+    const uint32_t ks = ring0 + (c_slot % SLOTS) * S::kSlotBytes, kb = bar0 + 8 * (c_slot % SLOTS);
+    const uint32_t kpar = (c_slot / SLOTS) & 1;
+    ++c_slot;
+    const uint32_t vs = ring0 + (c_slot % SLOTS) * S::kSlotBytes, vb = bar0 + 8 * (c_slot % SLOTS);
+    const uint32_t vpar = (c_slot / SLOTS) & 1;
+    ++c_slot;
+    const bool any = k0 < cw.s.end;
+    const bool valid = any && kv_page(a.kv, cw.seq, k0) >= 0;
+    if (!dead) dead = !__all_sync(0xffffffffu, tc::mbar_wait(kb, kpar, p.wait_limit, &abort_sh, p.dev_err));
+    float s[NT][4];
+    if (valid && !dead) {
+      float acc[NT][2][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[t][h][j] = 0.f;
+      const int row = lane & 15;
+      const uint32_t rbase = ks + row * 128;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t kf[4];
+        ldsm4(rbase + (k >> 2) * 2048 + (((((k & 3) << 1) + (lane >> 4)) ^ (row & 7)) << 4), kf);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma<T>(acc[t][k & 1], kf, qf[t][k][0], qf[t][k][1]);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[t][j] = (acc[t][0][j] + acc[t][1][j]) * sc;
+    }
+    __syncwarp();
+    issue();   // into the slot of K
+    uint32_t pf[NT][2];
+    if (valid && !dead) {
+      // masks: only units at the ends of what the tokens see
+      const int last = cw.s.pos0 + cw.s.n - 1;
+      if (k0 + kUnit - 1 > cw.s.pos0 || k0 < kv_first(last, a.window) || k0 + kUnit > cw.s.end) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = 8 * t + 2 * (lane & 3) + (j & 1), c = k0 + (lane >> 2) + 8 * (j >> 1);
+            const int pos = cw.s.pos0 + r / p.group;
+            if (c > pos || c < kv_first(pos, a.window) || c >= cw.s.end) s[t][j] = -CUDART_INF_F;
+          }
+      }
+      // the maximum over the 16 keys; moved when it is passed by 2^8
+      bool move = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v = fmaxf(s[t][j], s[t][j + 2]);
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          mx[t][j] = v;
+          move |= v > m[t][j] + 8.f;
+        }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float f[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float m2 = fmaxf(m[t][j], mx[t][j]);
+            f[j] = m2 == -CUDART_INF_F ? 1.f : ex2(m[t][j] - m2);
+            m[t][j] = m2;
+            l[t][j] *= f[j];
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) o[t][i][0] *= f[0], o[t][i][1] *= f[1], o[t][i][2] *= f[0], o[t][i][3] *= f[1];
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float m0 = m[t][0] == -CUDART_INF_F ? 0.f : m[t][0], m1 = m[t][1] == -CUDART_INF_F ? 0.f : m[t][1];
+        const float e0 = ex2(s[t][0] - m0), e1 = ex2(s[t][1] - m1), e2 = ex2(s[t][2] - m0), e3 = ex2(s[t][3] - m1);
+        l[t][0] += e0 + e2;
+        l[t][1] += e1 + e3;
+        pf[t][0] = transpose8(Half16<T>::pack(e0, e1));
+        pf[t][1] = transpose8(Half16<T>::pack(e2, e3));
+      }
+    }
+    if (!dead) dead = !__all_sync(0xffffffffu, tc::mbar_wait(vb, vpar, p.wait_limit, &abort_sh, p.dev_err));
+    if (valid && !dead) {
+      // what no token sees may be anything, and 0 times infinity is no zero
+      const int see0 = kv_first(cw.s.pos0, a.window);
+      if (k0 < see0 || k0 + kUnit > cw.s.end) {
+        for (int i = lane; i < kUnit * SLABS * 8; i += 32) {
+          const int r = (i >> 3) & 15, c = k0 + r;
+          if (c < see0 || c >= cw.s.end)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs + i * 16), "r"(0) : "memory");
+        }
+        tc::fence_proxy_async();   // before the slot's next load
+        __syncwarp();
+      }
+      const int row = (lane & 7) + ((lane >> 4) << 3);
+      const uint32_t rbase = vs + row * 128;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t vf[4];
+        ldsm4t(rbase + (i >> 2) * 2048 + (((((i & 3) << 1) + ((lane >> 3) & 1)) ^ (row & 7)) << 4), vf);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma<T>(o[t][i], vf, pf[t][0], pf[t][1]);
+      }
+    }
+    __syncwarp();
+    issue();   // into the slot of V
+
+    // ------------------------------------------------ end of this pair's part
+    const bool closes = cw.local + 1 == cw.n_local;
+    if (!closes && step + 1 < n_steps) {
+      ++cw.local;
+      continue;
+    }
+    {
+      // the warps' maxima and sums
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v = l[t][j];
+          v += __shfl_xor_sync(0xffffffffu, v, 4);
+          v += __shfl_xor_sync(0xffffffffu, v, 8);
+          v += __shfl_xor_sync(0xffffffffu, v, 16);
+          if (lane < 4) ml_sh[warp][8 * t + 2 * lane + j] = make_float2(m[t][j], v);
+        }
+      __syncthreads();
+      const int R = cw.s.n * p.group;
+      const bool whole = opens && closes;
+      const long long slot = 2ll * blockIdx.x + (opens ? 1 : 0);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        // every warp to the common maximum
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * t + 2 * (lane & 3) + j;
+          float mm = -CUDART_INF_F;
+#pragma unroll
+          for (int w = 0; w < W; ++w) mm = fmaxf(mm, ml_sh[w][r].x);
+          const float f = m[t][j] == -CUDART_INF_F ? 0.f : ex2(m[t][j] - mm);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) o[t][i][j] *= f, o[t][i][j + 2] *= f;
+        }
+        // their sum, pairwise
+#pragma unroll
+        for (int half = W / 2; half > 0; half >>= 1) {
+          if (warp >= half && warp < 2 * half) {
+            float* b = merge + (warp - half) * 8 * D + lane;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) b[(4 * i + j) * 32] = o[t][i][j];
+          }
+          __syncthreads();
+          if (warp < half) {
+            const float* b = merge + warp * 8 * D + lane;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[t][i][j] += b[(4 * i + j) * 32];
+          }
+          __syncthreads();
+        }
+        if (warp == 0) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              merge[(2 * (lane & 3) + (j & 1)) * S::kRowPad + 16 * i + (lane >> 2) + 8 * (j >> 1)] = o[t][i][j];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 8 * (D / 4); i += S::kThr) {
+          const int rr = i / (D / 4), r = 8 * t + rr, d = 4 * (i % (D / 4));
+          if (r >= R) continue;
+          float mm = -CUDART_INF_F, ll = 0.f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) mm = fmaxf(mm, ml_sh[w][r].x);
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float2 x = ml_sh[w][r];
+            ll += x.x == -CUDART_INF_F ? 0.f : x.y * ex2(x.x - mm);
+          }
+          const float4 v = *reinterpret_cast<const float4*>(merge + rr * S::kRowPad + d);
+          if (whole) {
+            const int tok = r / p.group;
+            const long long row = (long long)(cw.s.cu + tok) * a.n_q + cw.head * p.group + r - tok * p.group;
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + d) =
+                make_uint2(Half16<T>::pack(v.x * inv, v.y * inv), Half16<T>::pack(v.z * inv, v.w * inv));
+            if (d == 0 && a.lse) a.lse[row] = ll == 0.f ? -CUDART_INF_F : (mm + log2f(ll)) * 0.6931471805599453f;
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + (slot * p.rows + r) * D + d) = v;
+            if (d == 0) p.part_ml[slot * p.rows + r] = make_float2(mm, ll);
+          }
+        }
+        __syncthreads();
+      }
+    }
+    if (step + 1 < n_steps) {
+      cw.next(a);
+      opens = true;
+      begin();
+    }
+  }
+  if (dead) {   // what is in flight lands before the CTA leaves
+    for (uint32_t q = l_slot > (uint32_t)SLOTS ? l_slot - SLOTS : 0u; q < l_slot; ++q)
+      tc::mbar_drain(bar0 + 8 * (q % SLOTS), (q / SLOTS) & 1, 2000000000LL, p.dev_err);
+  }
+}
+
+// Joins the parts of the pairs that several CTAs had, and writes the rows of
+// sequences without any key.  Block: 64 elements of 8 rows of one pair; four
+// groups of threads take every fourth part.
+constexpr int kJoinThr = 512;
+template <typename T, int STEP>
+__global__ void __launch_bounds__(kJoinThr) join_kernel(const __grid_constant__ Params p, int D) {
+  __shared__ float4 sum_sh[kJoinThr];
+  __shared__ float l_sh[4][8];
+  pdl_wait();
+  const AttnParams& a = p.a;
+  const int seq = blockIdx.x / a.kv.n_kv, head = blockIdx.x % a.kv.n_kv;
+  const Seq s = seq_of(a, seq);
+  if (s.n == 0) return;
+  const int n = steps_of<STEP>(s);
+  const long long share = p.starts[a.kv.n_seqs];
+  const long long s0 = n ? p.starts[seq] + (long long)head * n : 0, s1 = s0 + n;
+  const long long c0 = n ? s0 / share : 0, c1 = n ? (s1 - 1) / share : 0;
+  if (n && c0 == c1) return;
+  const int part = threadIdx.x >> 7, rr = (threadIdx.x >> 4) & 7, d = blockIdx.y * 64 + 4 * (threadIdx.x & 15);
+  const int r = blockIdx.z * 8 + rr;
+  const bool in = r < s.n * p.group;
+  const int np = n ? (int)(c1 - c0) + 1 : 0;
+  auto slot = [&](int i) { return (i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * p.rows + r; };
+  float mm = -CUDART_INF_F;
+  if (in) {
+    for (int i = threadIdx.x & 15; i < np; i += 16) mm = fmaxf(mm, p.part_ml[slot(i)].x);
+  }
+#pragma unroll
+  for (int x = 8; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  if (in) {
+#pragma unroll 4
+    for (int i = part; i < np; i += 4) {
+      const float2 ml = p.part_ml[slot(i)];
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * D + d);
+      const float f = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - mm);
+      l = fmaf(ml.y, f, l);
+      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  sum_sh[threadIdx.x] = o;
+  if ((threadIdx.x & 15) == 0) l_sh[part][rr] = l;
+  __syncthreads();
+  if (part == 0 && in) {
+    l = (l_sh[0][rr] + l_sh[1][rr]) + (l_sh[2][rr] + l_sh[3][rr]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      const float4 v = sum_sh[threadIdx.x + 128 * i];
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    const int tok = r / p.group;
+    const long long row = (long long)(s.cu + tok) * a.n_q + head * p.group + r - tok * p.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + d) =
+        make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
+    if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+template <typename T, int D, int NT>
+static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
+  using S = Shape<D>;
+  static PerDevice attr;
+  if (!attr.get(dev.ordinal)) {
+    const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)S::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "decode attention smem attribute");
+    attr.set(dev.ordinal);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(S::kThr);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, D, NT>, p);
+  if (e != cudaSuccess) return cuda_fail(e, "decode attention launch");
+  cfg.gridDim = dim3(p.a.kv.n_seqs * p.a.kv.n_kv, D / 64, NT);
+  cfg.blockDim = dim3(kJoinThr);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T, S::kStep>, p, D);
+  return e == cudaSuccess ? Q4_OK : cuda_fail(e, "attention join launch");
+}
+
+// The largest NT: registers hold NT (D/8 + D/4) values of Q and O.
+constexpr int max_nt(int D) { return D >= 512 ? 1 : D == 256 ? 2 : 4; }
+
+template <typename T>
+static int launch_t(Params& p, int D, int nt, const DeviceInfo& dev, cudaStream_t s) {
+  switch (D) {
+    case 64: return nt == 1 ? launch<T, 64, 1>(p, dev, s) : nt == 2 ? launch<T, 64, 2>(p, dev, s) : launch<T, 64, 4>(p, dev, s);
+    case 128: return nt == 1 ? launch<T, 128, 1>(p, dev, s) : nt == 2 ? launch<T, 128, 2>(p, dev, s) : launch<T, 128, 4>(p, dev, s);
+    case 256: return nt == 1 ? launch<T, 256, 1>(p, dev, s) : launch<T, 256, 2>(p, dev, s);
+    default: return launch<T, 512, 1>(p, dev, s);
+  }
+}
+
+static int nt_of(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+}  // namespace dec
+
+bool attn_decode_fits(int max_rows, int D) { return max_rows <= 8 * dec::max_nt(D); }
+
+static size_t up256_(size_t n) { return (n + 255) & ~(size_t)255; }
+
+size_t attn_decode_ws_bytes(int max_rows, int D, const DeviceInfo& dev) {
+  const size_t slots = 2 * (size_t)dev.sms, rows = 8 * dec::nt_of(max_rows);
+  return up256_((kMaxSeqs + 1) * sizeof(long long)) + up256_(slots * rows * sizeof(float2)) + up256_(slots * rows * D * 4);
+}
+
+int launch_attn_decode(const AttnParams& a, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s) {
+  dec::Params p = {};
+  const bool bf16 = c.dtype == Q4_BF16;
+  const uint64_t rows = (uint64_t)c.n_pages * c.n_kv * c.page_size;
+  int st = encode_cache_rows(&p.tm_k, c.k, bf16, c.head_dim, rows, dec::kUnit, c.head_dim / 64, "the K cache");
+  if (st == Q4_OK) st = encode_cache_rows(&p.tm_v, c.v, bf16, c.head_dim, rows, dec::kUnit, c.head_dim / 64, "the V cache");
+  if (st != Q4_OK) return st;
+  p.a = a;
+  p.group = a.n_q / c.n_kv;
+  const int nt = dec::nt_of(a.max_q * p.group);
+  p.rows = 8 * nt;
+  p.grid = dev.sms;
+  p.total_rows = (int)rows;
+  p.wait_limit = wait_limit();
+  p.dev_err = device_error_word();
+  char* w = static_cast<char*>(ws);
+  p.starts = reinterpret_cast<long long*>(w);
+  w += up256_((kMaxSeqs + 1) * sizeof(long long));
+  p.part_ml = reinterpret_cast<float2*>(w);
+  w += up256_(2 * (size_t)p.grid * p.rows * sizeof(float2));
+  p.part_o = reinterpret_cast<float*>(w);
+  return bf16 ? dec::launch_t<__nv_bfloat16>(p, c.head_dim, nt, dev, s)
+              : dec::launch_t<__half>(p, c.head_dim, nt, dev, s);
+}
+
+}  // namespace q4w

@@ -800,6 +800,22 @@ int encode_tensor_2d(CUtensorMap* tm, const void* base, CUtensorMapDataType type
   return Q4_OK;
 }
 
+int encode_cache_rows(CUtensorMap* tm, const void* base, bool bf16, int D, uint64_t rows, uint32_t box_rows,
+                      uint32_t box_slabs, const char* what) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(Q4_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {64, rows, (cuuint64_t)D / 64};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
+  const cuuint32_t box[3] = {64, box_rows, box_slabs};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(Q4_ERR_CUDA, "tensor map for %s: driver error %d", what, (int)r);
+  return Q4_OK;
+}
+
 size_t gemm_ws_bytes(int K) { return ((size_t)gemm::kTok * K * 2 + 255) & ~(size_t)255; }
 size_t mma16_ws_bytes(int K) { return ((size_t)16 * K * 2 + 255) & ~(size_t)255; }
 

@@ -612,7 +612,8 @@ static int check_cache(const q4_kv_cache* cache) {
   // rows of the cache and positions of a sequence are indexed in 32 bits
   CHECK((long long)cache->n_pages * cache->n_kv * cache->page_size < (1ll << 31),
         "n_pages * n_kv * page_size must be below 2^31");
-  CHECK((long long)cache->max_pages * cache->page_size < (1ll << 31), "max_pages * page_size must be below 2^31");
+  CHECK((long long)cache->max_pages * cache->page_size <= (1ll << 31) - 8192,
+        "max_pages * page_size must be at most 2^31 - 8192");
   return Q4_OK;
 }
 

@@ -54,6 +54,10 @@ int launch_kv_append(const q4_kv_cache& c, int T, const void* k, long long k_str
 // Workspace of an attention call whose sequences have up to max_rows query
 // rows (tokens x query heads) per KV head.
 size_t attn_ws_bytes(int max_rows, int D, int n_seqs, const DeviceInfo& dev);
+// Few query rows per KV head (k_attn_decode.cu).
+bool attn_decode_fits(int max_rows, int D);
+size_t attn_decode_ws_bytes(int max_rows, int D, const DeviceInfo& dev);
+int launch_attn_decode(const AttnParams& a, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s);
 int launch_kv_attention(const AttnParams& p, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s);
 
 int launch_logits_sample(const void* z, long long stride, int dtype, int rows, int V, const float* u,

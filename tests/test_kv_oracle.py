@@ -189,6 +189,7 @@ def fake(monkeypatch):
     f = _Lib()
     monkeypatch.setattr(q4w, "load", lambda: f)
     monkeypatch.setattr(q4w, "_dev", lambda t, dtype, name: None)
+    monkeypatch.setattr(q4w, "_here", lambda t: True)
     monkeypatch.setattr(q4w, "_stream", lambda: None)
     return f
 
