@@ -1,115 +1,95 @@
-// Attention of new tokens over a paged cache, the plain form: one warp per
-// (token, query head), one key at a time, fp32 throughout.
-//
-// o = sum_c softmax_c(scale q.k_c) v_c over the cache positions c in
-// (P - window, P], c >= 0, P the token's own position; one pass over the keys
-// with the running maximum m and sum l of the softmax: a key of score s takes
-// m' = max(m, s), l' = l e^(m - m') + e^(s - m'), o' = o e^(m - m') + e^(s - m') v.
-#include <math_constants.h>
-
+// kv_attention: the choice between its kernels, and the joining of split work.
+#include "q4w_attn.cuh"
 #include "q4w_device.cuh"
-#include "q4w_internal.cuh"
-#include "q4w_kv.cuh"
 
 namespace q4w {
 namespace attn {
 
-constexpr int kThr = 128;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kThr) attn_kernel(const __grid_constant__ AttnParams p) {
-  pdl_wait();
-  constexpr int N = D / 64;   // pairs of elements per lane
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long id = (long long)blockIdx.x * (kThr / 32) + warp;
-  const int tok = (int)(id / p.n_q), h = (int)(id % p.n_q);
-  if (tok >= p.T) return;
-  int lo = 0, hi = p.kv.n_seqs;   // the first sequence that ends behind tok
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.kv.cu_tokens[mid + 1] <= tok) lo = mid + 1; else hi = mid;
-  }
-  const int seq = lo;
-  if (seq >= p.kv.n_seqs) return;
-  if (tok - p.kv.cu_tokens[seq] >= p.max_q) {
-    if (p.err && lane == 0) *p.err = 1;
-    return;
-  }
-  const int pos = p.kv.kv_lens[seq] - p.kv.cu_tokens[seq + 1] + tok;
-  const int kvh = h / (p.n_q / p.kv.n_kv);
-  const T* q = static_cast<const T*>(p.q) + tok * p.q_stride + (long long)h * D;
-  float2 qf[N], o[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    qf[i] = Half16<T>::unpack(*reinterpret_cast<const uint32_t*>(q + 2 * (lane + 32 * i)));
-    o[i] = make_float2(0.f, 0.f);
-  }
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int c = kv_first(pos, p.window); c <= pos; ++c) {
-    const int page = kv_page(p.kv, seq, c);
-    if (page < 0) {
-      if (p.err && lane == 0) *p.err = 1;
-      continue;
-    }
-    const long long row = kv_row(p.kv, page, kvh) + c % p.kv.page_size;
-    const uint32_t* kr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.k) + row * D);
-    const uint32_t* vr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.v) + row * D);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 kf = Half16<T>::unpack(kr[lane + 32 * i]);
-      s = fmaf(qf[i].x, kf.x, fmaf(qf[i].y, kf.y, s));
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale;
-    const float m2 = fmaxf(m, s);
-    const float f = m2 == -CUDART_INF_F ? 1.f : expf(m - m2), e = m2 == -CUDART_INF_F ? 0.f : expf(s - m2);
-    m = m2;
-    l = l * f + e;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 vf = Half16<T>::unpack(vr[lane + 32 * i]);
-      o[i].x = fmaf(e, vf.x, o[i].x * f);
-      o[i].y = fmaf(e, vf.y, o[i].y * f);
-    }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + ((long long)tok * p.n_q + h) * D);
-#pragma unroll
-  for (int i = 0; i < N; ++i) out[lane + 32 * i] = Half16<T>::pack(o[i].x * inv, o[i].y * inv);
-  if (p.lse && lane == 0) p.lse[(long long)tok * p.n_q + h] = l == 0.f ? -CUDART_INF_F : m + logf(l);
-}
-
-template <typename T, int D>
-static int launch(const AttnParams& p, cudaStream_t s) {
-  const long long n = (long long)p.T * p.n_q;
-  attn_kernel<T, D><<<(unsigned)((n + kThr / 32 - 1) / (kThr / 32)), kThr, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? Q4_OK : cuda_fail(e, "attention launch");
-}
+// Block: 64 elements of 8 rows of one item; four groups of threads take every
+// fourth part.
+constexpr int kJoinThr = 512;
 
 template <typename T>
-static int launch_t(const AttnParams& p, int D, cudaStream_t s) {
-  switch (D) {
-    case 64: return launch<T, 64>(p, s);
-    case 128: return launch<T, 128>(p, s);
-    case 256: return launch<T, 256>(p, s);
-    default: return launch<T, 512>(p, s);
+__global__ void __launch_bounds__(kJoinThr) join_kernel(const __grid_constant__ AttnParams a, const AttnSplit p,
+                                                        int group, int rows, int D, int dv, int align) {
+  __shared__ float4 sum_sh[kJoinThr];
+  __shared__ float l_sh[4][8];
+  pdl_wait();
+  const int c0 = blockIdx.x;
+  const SplitRec rec = p.recs[c0];
+  if (rec.last < 0) return;
+  const Seq s = seq_of(a, rec.seq, align);
+  const int cols = D / dv, tile = rec.tile / cols;
+  const int part = threadIdx.x >> 7, rr = (threadIdx.x >> 4) & 7, d = blockIdx.y * 64 + 4 * (threadIdx.x & 15);
+  const int lr = blockIdx.z * 8 + rr, r = tile * rows + lr;   // row of the tile, of the sequence
+  if (tile * rows + (int)blockIdx.z * 8 >= s.n * group) return;
+  const bool in = r < s.n * group;
+  const int np = rec.last - c0 + 1;
+  auto slot = [&](int i) { return (i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i)) * rows + lr; };
+  float mm = -CUDART_INF_F;
+  if (in) {
+    for (int i = threadIdx.x & 15; i < np; i += 16) mm = fmaxf(mm, p.part_ml[slot(i)].x);
+  }
+#pragma unroll
+  for (int x = 8; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  if (in) {
+#pragma unroll 4
+    for (int i = part; i < np; i += 4) {
+      const float2 ml = p.part_ml[slot(i)];
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * dv + d);
+      const float f = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - mm);
+      l = fmaf(ml.y, f, l);
+      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  sum_sh[threadIdx.x] = o;
+  if ((threadIdx.x & 15) == 0) l_sh[part][rr] = l;
+  __syncthreads();
+  if (part == 0 && in) {
+    l = (l_sh[0][rr] + l_sh[1][rr]) + (l_sh[2][rr] + l_sh[3][rr]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      const float4 v = sum_sh[threadIdx.x + 128 * i];
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    const int tok = r / group, col = rec.tile % cols;
+    const long long row = (long long)(s.cu + tok) * a.n_q + rec.head * group + r - tok * group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + col * dv + d) =
+        make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
+    if (d == 0 && col == 0 && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
   }
 }
 
 }  // namespace attn
 
+int launch_attn_join(const AttnParams& a, const AttnSplit& split, int group, int rows, int D, int dv, int align,
+                     bool bf16, int grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, dv / 64, rows / 8);
+  cfg.blockDim = dim3(attn::kJoinThr);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e =
+      bf16 ? cudaLaunchKernelEx(&cfg, attn::join_kernel<__nv_bfloat16>, a, split, group, rows, D, dv, align)
+           : cudaLaunchKernelEx(&cfg, attn::join_kernel<__half>, a, split, group, rows, D, dv, align);
+  return e == cudaSuccess ? Q4_OK : cuda_fail(e, "attention join launch");
+}
+
 size_t attn_ws_bytes(int max_rows, int D, int n_seqs, const DeviceInfo& dev) {
   (void)n_seqs;
-  return attn_decode_fits(max_rows, D) ? attn_decode_ws_bytes(max_rows, D, dev) : 0;
+  return attn_decode_fits(max_rows, D) ? attn_decode_ws_bytes(max_rows, D, dev) : attn_tile_ws_bytes(D, dev);
 }
 
 int launch_kv_attention(const AttnParams& p, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s) {
-  if (attn_decode_fits(p.max_q * (p.n_q / c.n_kv), c.head_dim)) return launch_attn_decode(p, c, ws, dev, s);
-  return c.dtype == Q4_F16 ? attn::launch_t<__half>(p, c.head_dim, s)
-                           : attn::launch_t<__nv_bfloat16>(p, c.head_dim, s);
+  return attn_decode_fits(p.max_q * (p.n_q / c.n_kv), c.head_dim) ? launch_attn_decode(p, c, ws, dev, s)
+                                                                  : launch_attn_tile(p, c, ws, dev, s);
 }
 
 }  // namespace q4w

@@ -25,9 +25,9 @@
 // order of the keys: the same lengths give the same bits.
 #include <math_constants.h>
 
+#include "q4w_attn.cuh"
 #include "q4w_device.cuh"
 #include "q4w_internal.cuh"
-#include "q4w_kv.cuh"
 #include "q4w_tc.cuh"
 
 namespace q4w {
@@ -52,40 +52,17 @@ struct Shape {
 struct Params {
   CUtensorMap tm_k, tm_v;
   AttnParams a;
-  float* part_o;         // [2 grid][rows][D]
-  float2* part_ml;       // [2 grid][rows]: maximum, sum
-  long long* starts;     // [n_seqs]: first step of each sequence; then the share
+  AttnSplit split;
   unsigned* dev_err;
   long long wait_limit;
-  int group, rows;       // query heads per KV head, 8 NT
+  int group;             // query heads per KV head
   int total_rows;        // of the cache
   int grid;
 };
 
-// The part of one sequence's work that its lengths determine.
-struct Seq {
-  int n, pos0;           // new tokens taken, position of the first
-  int base, end;         // keys [base, end), base a multiple of 16
-  int cu;
-};
-
-__device__ __forceinline__ Seq seq_of(const AttnParams& a, int seq) {
-  Seq s;
-  s.cu = a.kv.cu_tokens[seq];
-  const int n = a.kv.cu_tokens[seq + 1] - s.cu, len = max(a.kv.kv_lens[seq], 0);
-  s.n = s.cu >= 0 ? min(min(max(n, 0), a.max_q), max(a.T - s.cu, 0)) : 0;
-  s.pos0 = len - n;
-  s.base = kv_first(s.pos0, a.window) & ~(kUnit - 1);
-  s.end = s.n > 0 ? min(s.pos0 + s.n, a.kv.max_pages * a.kv.page_size) : 0;
-  return s;
-}
-__device__ __forceinline__ bool seq_bad(const AttnParams& a, int seq) {
-  const int n = a.kv.cu_tokens[seq + 1] - a.kv.cu_tokens[seq];
-  return n > a.max_q || (n > 0 && a.kv.kv_lens[seq] > a.kv.max_pages * a.kv.page_size);
-}
 template <int STEP>
 __device__ __forceinline__ int steps_of(const Seq& s) {
-  return s.end > s.base ? (s.end - s.base + STEP - 1) / STEP : 0;
+  return s.n == 0 ? 0 : s.end > s.base ? (s.end - s.base + STEP - 1) / STEP : 1;
 }
 
 // ------------------------------------------------------------ instructions ---
@@ -117,12 +94,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // A walk over the steps of a CTA's share.
 template <int STEP>
 struct Walk {
@@ -130,7 +101,7 @@ struct Walk {
   Seq s;
   __device__ __forceinline__ void enter(const AttnParams& a) {
     while (seq < a.kv.n_seqs) {
-      s = seq_of(a, seq);
+      s = seq_of(a, seq, kUnit);
       n_local = steps_of<STEP>(s);
       if (n_local > 0) return;
       ++seq;
@@ -176,7 +147,7 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
     const int per = (a.kv.n_seqs + S::kThr - 1) / S::kThr;
     const int q0 = min((int)threadIdx.x * per, a.kv.n_seqs), q1 = min(q0 + per, a.kv.n_seqs);
     long long sum = 0;
-    for (int q = q0; q < q1; ++q) sum += (long long)steps_of<S::kStep>(seq_of(a, q)) * a.kv.n_kv;
+    for (int q = q0; q < q1; ++q) sum += (long long)steps_of<S::kStep>(seq_of(a, q, kUnit)) * a.kv.n_kv;
     long long incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -194,20 +165,16 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
     }
     share = (total + p.grid - 1) / p.grid;
     const long long mine = share * blockIdx.x;
-    if (blockIdx.x == 0) {
-      if (threadIdx.x == 0) p.starts[a.kv.n_seqs] = share;
-      long long at = before;
-      for (int q = q0; q < q1; ++q) {
-        p.starts[q] = at;
-        at += (long long)steps_of<S::kStep>(seq_of(a, q)) * a.kv.n_kv;
-        if (a.err && seq_bad(a, q)) *a.err = 1;
-      }
+    if (blockIdx.x == 0 && a.err) {
+      for (int q = q0; q < q1; ++q)
+        if (seq_bad(a, q)) *a.err = 1;
     }
+    if (threadIdx.x == 0) p.split.recs[blockIdx.x].last = -1;
     if (sum > 0 && mine >= before && mine < before + sum) {
       long long left = mine - before;
       int q = q0, n;
       for (;; ++q) {
-        n = steps_of<S::kStep>(seq_of(a, q));
+        n = steps_of<S::kStep>(seq_of(a, q, kUnit));
         if (left < (long long)n * a.kv.n_kv) break;
         left -= (long long)n * a.kv.n_kv;
       }
@@ -438,6 +405,8 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
       const int R = cw.s.n * p.group;
       const bool whole = opens && closes;
       const long long slot = 2ll * blockIdx.x + (opens ? 1 : 0);
+      if (opens && !closes && threadIdx.x == 0)   // goes on in the next CTAs
+        p.split.recs[blockIdx.x] = {cw.seq, cw.head, 0, (int)((first_step + step - cw.local + cw.n_local - 1) / share)};
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         // every warp to the common maximum
@@ -499,8 +468,8 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
                 make_uint2(Half16<T>::pack(v.x * inv, v.y * inv), Half16<T>::pack(v.z * inv, v.w * inv));
             if (d == 0 && a.lse) a.lse[row] = ll == 0.f ? -CUDART_INF_F : (mm + log2f(ll)) * 0.6931471805599453f;
           } else {
-            *reinterpret_cast<float4*>(p.part_o + (slot * p.rows + r) * D + d) = v;
-            if (d == 0) p.part_ml[slot * p.rows + r] = make_float2(mm, ll);
+            *reinterpret_cast<float4*>(p.split.part_o + (slot * (8 * NT) + r) * D + d) = v;
+            if (d == 0) p.split.part_ml[slot * (8 * NT) + r] = make_float2(mm, ll);
           }
         }
         __syncthreads();
@@ -515,66 +484,6 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
   if (dead) {   // what is in flight lands before the CTA leaves
     for (uint32_t q = l_slot > (uint32_t)SLOTS ? l_slot - SLOTS : 0u; q < l_slot; ++q)
       tc::mbar_drain(bar0 + 8 * (q % SLOTS), (q / SLOTS) & 1, 2000000000LL, p.dev_err);
-  }
-}
-
-// Joins the parts of the pairs that several CTAs had, and writes the rows of
-// sequences without any key.  Block: 64 elements of 8 rows of one pair; four
-// groups of threads take every fourth part.
-constexpr int kJoinThr = 512;
-template <typename T, int STEP>
-__global__ void __launch_bounds__(kJoinThr) join_kernel(const __grid_constant__ Params p, int D) {
-  __shared__ float4 sum_sh[kJoinThr];
-  __shared__ float l_sh[4][8];
-  pdl_wait();
-  const AttnParams& a = p.a;
-  const int seq = blockIdx.x / a.kv.n_kv, head = blockIdx.x % a.kv.n_kv;
-  const Seq s = seq_of(a, seq);
-  if (s.n == 0) return;
-  const int n = steps_of<STEP>(s);
-  const long long share = p.starts[a.kv.n_seqs];
-  const long long s0 = n ? p.starts[seq] + (long long)head * n : 0, s1 = s0 + n;
-  const long long c0 = n ? s0 / share : 0, c1 = n ? (s1 - 1) / share : 0;
-  if (n && c0 == c1) return;
-  const int part = threadIdx.x >> 7, rr = (threadIdx.x >> 4) & 7, d = blockIdx.y * 64 + 4 * (threadIdx.x & 15);
-  const int r = blockIdx.z * 8 + rr;
-  const bool in = r < s.n * p.group;
-  const int np = n ? (int)(c1 - c0) + 1 : 0;
-  auto slot = [&](int i) { return (i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * p.rows + r; };
-  float mm = -CUDART_INF_F;
-  if (in) {
-    for (int i = threadIdx.x & 15; i < np; i += 16) mm = fmaxf(mm, p.part_ml[slot(i)].x);
-  }
-#pragma unroll
-  for (int x = 8; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  if (in) {
-#pragma unroll 4
-    for (int i = part; i < np; i += 4) {
-      const float2 ml = p.part_ml[slot(i)];
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * D + d);
-      const float f = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - mm);
-      l = fmaf(ml.y, f, l);
-      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-    }
-  }
-  sum_sh[threadIdx.x] = o;
-  if ((threadIdx.x & 15) == 0) l_sh[part][rr] = l;
-  __syncthreads();
-  if (part == 0 && in) {
-    l = (l_sh[0][rr] + l_sh[1][rr]) + (l_sh[2][rr] + l_sh[3][rr]);
-#pragma unroll
-    for (int i = 1; i < 4; ++i) {
-      const float4 v = sum_sh[threadIdx.x + 128 * i];
-      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-    }
-    const int tok = r / p.group;
-    const long long row = (long long)(s.cu + tok) * a.n_q + head * p.group + r - tok * p.group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + d) =
-        make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
-    if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -598,13 +507,9 @@ static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, D, NT>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, D, NT>, p);
   if (e != cudaSuccess) return cuda_fail(e, "decode attention launch");
-  cfg.gridDim = dim3(p.a.kv.n_seqs * p.a.kv.n_kv, D / 64, NT);
-  cfg.blockDim = dim3(kJoinThr);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<T, S::kStep>, p, D);
-  return e == cudaSuccess ? Q4_OK : cuda_fail(e, "attention join launch");
+  return launch_attn_join(p.a, p.split, p.group, 8 * NT, D, D, kUnit, std::is_same<T, __nv_bfloat16>::value, p.grid, s);
 }
 
 // The largest NT: registers hold NT (D/8 + D/4) values of Q and O.
@@ -626,11 +531,8 @@ static int nt_of(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 bool attn_decode_fits(int max_rows, int D) { return max_rows <= 8 * dec::max_nt(D); }
 
-static size_t up256_(size_t n) { return (n + 255) & ~(size_t)255; }
-
 size_t attn_decode_ws_bytes(int max_rows, int D, const DeviceInfo& dev) {
-  const size_t slots = 2 * (size_t)dev.sms, rows = 8 * dec::nt_of(max_rows);
-  return up256_((kMaxSeqs + 1) * sizeof(long long)) + up256_(slots * rows * sizeof(float2)) + up256_(slots * rows * D * 4);
+  return attn_split_bytes(dev.sms, 8 * dec::nt_of(max_rows), D);
 }
 
 int launch_attn_decode(const AttnParams& a, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s) {
@@ -643,17 +545,11 @@ int launch_attn_decode(const AttnParams& a, const q4_kv_cache& c, void* ws, cons
   p.a = a;
   p.group = a.n_q / c.n_kv;
   const int nt = dec::nt_of(a.max_q * p.group);
-  p.rows = 8 * nt;
   p.grid = dev.sms;
   p.total_rows = (int)rows;
   p.wait_limit = wait_limit();
   p.dev_err = device_error_word();
-  char* w = static_cast<char*>(ws);
-  p.starts = reinterpret_cast<long long*>(w);
-  w += up256_((kMaxSeqs + 1) * sizeof(long long));
-  p.part_ml = reinterpret_cast<float2*>(w);
-  w += up256_(2 * (size_t)p.grid * p.rows * sizeof(float2));
-  p.part_o = reinterpret_cast<float*>(w);
+  p.split = attn_split(ws, p.grid, 8 * nt, c.head_dim);
   return bf16 ? dec::launch_t<__nv_bfloat16>(p, c.head_dim, nt, dev, s)
               : dec::launch_t<__half>(p, c.head_dim, nt, dev, s);
 }

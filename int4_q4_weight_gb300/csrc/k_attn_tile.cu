@@ -1,0 +1,692 @@
+// Attention of many query rows per KV head over a paged cache (prefill chunks,
+// prompts): tiles of 128 query rows on the 5th-generation tensor cores.
+//
+// A tile's rows are (token, query head of the group) pairs, so all heads of a
+// group share the keys that are read.  One pass over the keys, 128 a step:
+//   S[128 rows][128 keys] = Q K^T     A = Q, B = K, both in shared memory
+//   P = 2^(S scale log2(e) - m)       one thread per row, S read from TMEM,
+//                                     P (16 bits) written over it
+//   O[128 rows][DV]      += P V       A = P in TMEM, B = V in shared memory
+// with the running maximum m and sum of each row in its thread.  m is moved
+// only when a score passes it by 2^8, so O (in TMEM) is rarely rescaled.
+// Two S tiles alternate: the scores of step j + 1 are formed while the softmax
+// of step j runs.  TMEM: S 2 x 128 columns, O 256 = all 512.  Head size 512 does
+// not fit: its two column halves of O are items of their own, which form the
+// scores twice (1.5 times the products).
+//
+// Warps: 0-3 softmax (warp w the rows 32 w ..), 4 issues the MMAs, 5 the TMA
+// loads, 6-7 load the query rows of the next item.  K and V go through one ring
+// of slots in the order in which the MMAs take them: K slots of [128 keys][<=
+// 128 dims], V slots of [64 or 128 keys][DV], loaded in boxes of 16 to 64 rows
+// (the page size's share), 128-byte swizzle.
+//
+// Split: the steps of all items (sequence, KV head, tile) form one line that is
+// cut into equal shares, one CTA per SM; causal tiles of any length and ragged
+// sequences balance, and a short chunk over a long cache is split along the
+// keys.  Parts are joined by a second kernel in the order of the keys.
+#include <cuda.h>
+
+#include "q4w_attn.cuh"
+#include "q4w_device.cuh"
+#include "q4w_tc.cuh"
+
+namespace q4w {
+namespace tile {
+
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kThr = 256;
+constexpr int kMmaWarp = 4, kTmaWarp = 5, kQWarp = 6;
+constexpr long long kDrainCycles = 2000000000LL;
+constexpr int kBadRing = 16;
+
+template <int D>
+struct Shape {
+  static constexpr int kDV = D < 256 ? D : 256;              // columns of O of an item
+  static constexpr int kParts = D / kDV;                     // items per tile
+  static constexpr int kKD = D < 128 ? D : 128;              // dims of a K slot
+  static constexpr int kNK = D / kKD;                        // K slots per step
+  static constexpr int kSlot = kKeys * kKD * 2;              // bytes: 32 KB, 16 KB for D = 64
+  static constexpr int kVK = kSlot / (kDV * 2);              // keys of a V slot
+  static constexpr int kNV = kKeys / kVK;                    // V slots per step
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kSlots = (229376 - kQBytes) / kSlot < 12 ? (229376 - kQBytes) / kSlot : 12;   // 3, 5, 6, 12
+  static constexpr size_t kSmem = 1024 + kQBytes + (size_t)kSlots * kSlot;
+};
+
+struct Params {
+  CUtensorMap tm_k, tm_v;
+  AttnParams a;
+  AttnSplit split;
+  unsigned* dev_err;
+  long long wait_limit;
+  int group, total_rows, grid;
+  int box;               // rows of a TMA box: 16, 32 or 64, a divisor of the page size
+};
+
+// Keys that tile t of a sequence sees: [base, end), and its steps.
+struct Span {
+  int lo, base, end, steps;   // lo: the first key that its first token sees
+};
+__device__ __forceinline__ Span span_of(const AttnParams& a, const Seq& s, int group, int t, int box) {
+  Span x;
+  const int j0 = t * kRows / group, j1 = min((t * kRows + kRows - 1) / group, s.n - 1);
+  x.lo = kv_first(s.pos0 + j0, a.window);
+  x.base = x.lo & ~(box - 1);
+  x.end = min(s.end, s.pos0 + j1 + 1);
+  x.steps = x.end > x.base ? (x.end - x.base + kKeys - 1) / kKeys : 1;
+  return x;
+}
+__device__ __forceinline__ int tiles_of(const Seq& s, int group) { return (s.n * group + kRows - 1) / kRows; }
+
+// A walk over the items of a CTA's share: for each sequence its heads, their
+// column parts, their tiles.
+struct Walk {
+  int seq, head, part, t, n_tiles;
+  int local;             // step of the item
+  Seq s;
+  Span x;
+};
+template <int PARTS>
+__device__ __forceinline__ void walk_item(Walk& w, const Params& p) { w.x = span_of(p.a, w.s, p.group, w.t, p.box); }
+// To the next item (the caller knows that there is one).
+template <int PARTS>
+__device__ __forceinline__ void walk_next(Walk& w, const Params& p) {
+  w.local = 0;
+  if (++w.t == w.n_tiles) {
+    w.t = 0;
+    if (++w.part == PARTS) {
+      w.part = 0;
+      if (++w.head == p.a.kv.n_kv) {
+        w.head = 0;
+        do {
+          ++w.seq;
+          if (w.seq >= p.a.kv.n_seqs) return;
+          w.s = seq_of(p.a, w.seq, p.box);
+          w.n_tiles = tiles_of(w.s, p.group);
+        } while (w.n_tiles == 0);
+      }
+    }
+  }
+  walk_item<PARTS>(w, p);
+}
+
+// Instruction descriptor, kind::f16: fp32 accumulators, A and B of one 16-bit
+// type, M = 128, N = n; bit 16: B is MN-major (its N index is the contiguous one).
+__host__ __device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(accum)
+      : "memory");
+}
+// MN-major operand in the 128-byte swizzle: 64 elements of MN are one 128-byte
+// row per K index, eight K rows (1024 bytes) a group (stride byte offset), the
+// next 64 elements of MN `lbo` bytes further (leading byte offset).
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ Params p) {
+  using S = Shape<D>;
+  constexpr int NS = S::kSlots, PARTS = S::kParts;
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = smem + S::kQBytes;
+  __shared__ uint64_t bars[2 * NS + 8];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+  __shared__ int start_sh[6];
+  __shared__ long long scan_sh[kThr / 32];
+  __shared__ uint32_t bad_sh[kBadRing];   // per step: boxes whose page is none of the cache
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const AttnParams& a = p.a;
+  const uint32_t full0 = tc::smem_u32(bars), empty0 = full0 + 8 * NS;
+  const uint32_t qfull = empty0 + 8 * NS, qempty = qfull + 8, sfull0 = qempty + 8, pready0 = sfull0 + 16,
+                 odone = pready0 + 16, drain = odone + 8;
+  volatile int* abort_flag = &abort_sh;
+
+  if (warp == 0) {
+    if (lane == 0) abort_sh = 0, start_sh[0] = -1;
+    if (lane < 2 * NS + 8) {
+      unsigned count = 1;
+      if (lane == 2 * NS) count = 64;                                // qfull: the loading threads
+      else if (lane == 2 * NS + 4 || lane == 2 * NS + 5) count = 4;  // pready: the softmax warps
+      tc::mbar_init(tc::smem_u32(bars + lane), count);
+    }
+    tc::mbar_fence_init();
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&tmem_sh), 512);
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the shares: a warp per sequence, a lane per tile; the sums in the ring,
+  // which holds nothing yet
+  long long total, share;
+  {
+    int* steps_sh = reinterpret_cast<int*>(ring);   // steps of one head and part of each sequence
+    for (int q = warp; q < a.kv.n_seqs; q += kThr / 32) {
+      const Seq s = seq_of(a, q, p.box);
+      const int nt = tiles_of(s, p.group);
+      int sum = 0;
+      for (int t = lane; t < nt; t += 32) sum += span_of(a, s, p.group, t, p.box).steps;
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == 0) {
+        steps_sh[q] = sum;
+        if (blockIdx.x == 0 && a.err && seq_bad(a, q)) *a.err = 1;
+      }
+    }
+    __syncthreads();
+    const int per = (a.kv.n_seqs + kThr - 1) / kThr;
+    const int q0 = min((int)threadIdx.x * per, a.kv.n_seqs), q1 = min(q0 + per, a.kv.n_seqs);
+    const long long times = (long long)a.kv.n_kv * PARTS;
+    long long sum = 0;
+    for (int q = q0; q < q1; ++q) sum += steps_sh[q] * times;
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) scan_sh[warp] = incl;
+    __syncthreads();
+    total = 0;
+    long long before = incl - sum;
+#pragma unroll
+    for (int w = 0; w < kThr / 32; ++w) {
+      if (w < warp) before += scan_sh[w];
+      total += scan_sh[w];
+    }
+    share = (total + p.grid - 1) / p.grid;
+    const long long mine = share * blockIdx.x;
+    if (sum > 0 && mine >= before && mine < before + sum) {
+      long long left = mine - before;
+      int q = q0;
+      while (left >= steps_sh[q] * times) left -= steps_sh[q++] * times;
+      const int hp = (int)(left / steps_sh[q]);
+      start_sh[0] = q;
+      start_sh[1] = hp / PARTS;
+      start_sh[2] = hp % PARTS;
+      start_sh[3] = (int)(left % steps_sh[q]);
+    }
+    if (threadIdx.x == 0) p.split.recs[blockIdx.x].last = -1;
+    tc::fence_proxy_async();   // the sums' last use, before the ring's first loads
+    __syncthreads();
+  }
+  const long long first_step = share * blockIdx.x;
+  const int n_steps = start_sh[0] < 0 ? 0 : (int)max(0ll, min(share, total - first_step));
+  Walk w = {};
+  if (n_steps > 0) {
+    // the tile: every warp scans the sequence's tiles, 32 at a time
+    w.seq = start_sh[0], w.head = start_sh[1], w.part = start_sh[2];
+    w.s = seq_of(a, w.seq, p.box);
+    w.n_tiles = tiles_of(w.s, p.group);
+    int left = start_sh[3];
+    for (int t0 = 0;; t0 += 32) {
+      const int n = t0 + lane < w.n_tiles ? span_of(a, w.s, p.group, t0 + lane, p.box).steps : 0;
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > left);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        w.t = t0 + at;
+        w.local = left - __shfl_sync(0xffffffffu, incl - n, at);
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    walk_item<PARTS>(w, p);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_sh;
+  const uint32_t q_addr = tc::smem_u32(smem), ring0 = tc::smem_u32(ring);
+  const uint32_t o_tmem = tmem + 256;
+
+  // Whether step j + 1 of the share belongs to the same item as step j: then its
+  // scores are formed before the values of step j, else after them.
+  if (warp == kTmaWarp) {
+    // ---------------------------------------------------------- TMA loads
+    const uint64_t policy = tc::policy_evict_last();
+    const int nb = kKeys / p.box;
+    uint32_t q = 0;   // slots filled
+    bool ok = true;
+    // cache rows of a step's boxes, lane b the box b
+    auto rows_of = [&](const Walk& y, int j) {
+      int row = p.total_rows;   // out of the cache: zeros
+      bool bad = false;
+      const int pos = y.x.base + y.local * kKeys + lane * p.box;
+      if (lane < nb && pos < y.x.end && pos + p.box > y.x.lo) {
+        const int page = kv_page(a.kv, y.seq, pos);
+        bad = page < 0;
+        if (!bad) row = (int)kv_row(a.kv, page, y.head) + pos % a.kv.page_size;
+      }
+      const uint32_t mask = __ballot_sync(0xffffffffu, bad);
+      if (lane == 0) {
+        bad_sh[j % kBadRing] = mask;
+        if (mask && a.err) *a.err = 1;
+      }
+      __syncwarp();
+      return row;
+    };
+    auto acquire = [&]() {
+      const uint32_t slot = q % NS;
+      const bool f = tc::mbar_wait(empty0 + 8 * slot, ((q / NS) & 1) ^ 1, p.wait_limit, abort_flag, p.dev_err);
+      if (!__all_sync(0xffffffffu, f)) return ok = false;
+      if (lane == 0) tc::mbar_expect_tx(full0 + 8 * slot, S::kSlot);
+      __syncwarp();
+      return true;
+    };
+    auto load_k = [&](int row) {
+      for (int h = 0; h < S::kNK && ok; ++h) {
+        if (!acquire()) return;
+        const uint32_t slot = q % NS, dst = ring0 + slot * S::kSlot;
+        constexpr int slabs = S::kKD / 64;
+        const int b = lane % nb, sl = lane / nb, r = __shfl_sync(0xffffffffu, row, b);
+        if (sl < slabs)
+          tc::tma_load_3d(dst + sl * (kKeys * 128) + b * p.box * 128, &p.tm_k, 0, r, h * slabs + sl, full0 + 8 * slot, policy);
+        ++q;
+      }
+    };
+    auto load_v = [&](int row, int part) {
+      for (int h = 0; h < S::kNV && ok; ++h) {
+        if (!acquire()) return;
+        const uint32_t slot = q % NS, dst = ring0 + slot * S::kSlot;
+        constexpr int slabs = S::kDV / 64;
+        const int vb = S::kVK / p.box;   // boxes of the slot's keys
+        const int b = lane % vb, sl = lane / vb, r = __shfl_sync(0xffffffffu, row, h * vb + b);
+        if (sl < slabs)
+          tc::tma_load_3d(dst + sl * (S::kVK * 128) + b * p.box * 128, &p.tm_v, 0, r, part * slabs + sl, full0 + 8 * slot, policy);
+        ++q;
+      }
+    };
+    if (n_steps > 0) {
+      int row = rows_of(w, 0);
+      load_k(row);
+      for (int j = 0; j < n_steps && ok; ++j) {
+        const int part = w.part;
+        bool same = false;
+        int next_row = 0;
+        if (j + 1 < n_steps) {
+          same = w.local + 1 < w.x.steps;
+          if (same) ++w.local; else walk_next<PARTS>(w, p);
+          next_row = rows_of(w, j + 1);
+        }
+        if (same) load_k(next_row);
+        load_v(row, part);
+        if (!same && j + 1 < n_steps) load_k(next_row);
+        row = next_row;
+      }
+      // what was issued lands before the CTA leaves
+      for (uint32_t i = q > (uint32_t)NS ? q - NS : 0u; i < q; ++i)
+        tc::mbar_drain(full0 + 8 * (i % NS), (i / NS) & 1, kDrainCycles, p.dev_err);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------- MMA issuer
+    constexpr uint32_t id_s = idesc(kKeys, BF16, false), id_o = idesc(S::kDV, BF16, true);
+    uint32_t q = 0;
+    int item = 0;
+    bool ok = n_steps > 0;
+    auto wait_all = [&](uint32_t bar, uint32_t par) {
+      const bool f = tc::mbar_wait(bar, par, p.wait_limit, abort_flag, p.dev_err);
+      ok = __all_sync(0xffffffffu, f);
+      return ok;
+    };
+    auto scores = [&](int j, bool first, bool last) {
+      if (first && !wait_all(qfull, item & 1)) return;
+      for (int h = 0; h < S::kNK; ++h) {
+        const uint32_t slot = q % NS;
+        if (!wait_all(full0 + 8 * slot, (q / NS) & 1)) return;
+        tc::fence_after();
+        if (tc::elect_one()) {
+          const uint32_t kb = ring0 + slot * S::kSlot, qb = q_addr + h * (S::kKD / 64) * (kRows * 128);
+#pragma unroll
+          for (int k = 0; k < S::kKD / 16; ++k) {
+            const uint32_t off = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
+            mma_ss(tmem + (j & 1) * 128, tc::desc_sw128(qb + off), tc::desc_sw128(kb + off), id_s, (h > 0 || k > 0) ? 1u : 0u);
+          }
+          tc::commit(empty0 + 8 * slot);
+        }
+        __syncwarp();
+        ++q;
+      }
+      if (tc::elect_one()) {
+        tc::commit(sfull0 + 8 * (j & 1));
+        if (last) tc::commit(qempty);
+      }
+      __syncwarp();
+      if (last) ++item;
+    };
+    auto values = [&](int j, bool first) {
+      if (!wait_all(pready0 + 8 * (j & 1), (j >> 1) & 1)) return;
+      for (int h = 0; h < S::kNV; ++h) {
+        const uint32_t slot = q % NS;
+        if (!wait_all(full0 + 8 * slot, (q / NS) & 1)) return;
+        tc::fence_after();
+        if (tc::elect_one()) {
+          const uint32_t vb = ring0 + slot * S::kSlot, pa = tmem + (j & 1) * 128 + h * (S::kVK / 2);
+#pragma unroll
+          for (int k = 0; k < S::kVK / 16; ++k)
+            mma_ts(o_tmem, pa + 8 * k, desc_mn_sw128(vb + k * 2048, S::kVK * 128), id_o, (first && h == 0 && k == 0) ? 0u : 1u);
+          tc::commit(empty0 + 8 * slot);
+        }
+        __syncwarp();
+        ++q;
+      }
+      if (tc::elect_one()) tc::commit(odone);
+      __syncwarp();
+    };
+    // per step: whether it is the first of an item in this share, and whether the
+    // next step belongs to the same item
+    bool first = true, has = false;
+    if (ok) {
+      has = 1 < n_steps && w.local + 1 < w.x.steps;
+      scores(0, true, !has);
+    }
+    for (int j = 0; j < n_steps && ok; ++j) {
+      const bool same = has;
+      bool next_has = false;
+      if (j + 1 < n_steps) {
+        if (same) ++w.local; else walk_next<PARTS>(w, p);
+        next_has = j + 2 < n_steps && w.local + 1 < w.x.steps;
+      }
+      if (same) scores(j + 1, false, !next_has);
+      if (ok) values(j, first);
+      if (ok && !same && j + 1 < n_steps) scores(j + 1, true, !next_has);
+      first = !same;
+      has = next_has;
+    }
+    // every tcgen05 operation has finished before TMEM is freed
+    if (tc::elect_one()) tc::commit(drain);
+    __syncwarp();
+    tc::mbar_drain(drain, 0, kDrainCycles, p.dev_err);
+    __syncwarp();
+  } else if (warp >= kQWarp) {
+    // ------------------------------------------------------- query rows
+    const int th = threadIdx.x - kQWarp * 32;
+    int item = 0;
+    for (int j = 0; j < n_steps;) {
+      if (!tc::mbar_wait(qempty, (item & 1) ^ 1, p.wait_limit, abort_flag, p.dev_err)) break;
+      const int R = w.s.n * p.group;
+      constexpr int per_row = D / 8;   // 16-byte pieces
+      for (int i = th; i < kRows * per_row; i += 64) {
+        const int row = i / per_row, c = i % per_row, r = w.t * kRows + row;
+        const bool in = r < R;
+        const int tok = in ? r / p.group : 0, h = in ? r - tok * p.group : 0;
+        const T* src = static_cast<const T*>(a.q) + (long long)(w.s.cu + tok) * a.q_stride +
+                       (long long)(w.head * p.group + h) * D + c * 8;
+        cp_async16(q_addr + (c >> 3) * (kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), src, in);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      tc::fence_proxy_async();
+      tc::mbar_arrive(qfull);
+      ++item;
+      j += w.x.steps - w.local;
+      if (j < n_steps) walk_next<PARTS>(w, p);
+    }
+  } else {
+    // ----------------------------------------------------------- softmax
+    const int row = threadIdx.x;
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    // scores in units of log2 e; a scale of zero becomes one that still takes
+    // the masked scores' infinity to infinity
+    const float sc = a.scale == 0.f ? 1e-30f : a.scale * 1.4426950408889634f;
+    float m = -CUDART_INF_F, l = 0.f;
+    bool first = true, opens = w.local == 0;
+    int r = 0, lo = 0, hi = -1, tok = 0;
+    auto begin = [&]() {
+      r = w.t * kRows + row;
+      tok = r / p.group;
+      const int pos = tok < w.s.n ? w.s.pos0 + tok : -1;
+      lo = kv_first(pos, a.window);
+      hi = min(pos, w.x.end - 1);
+      m = -CUDART_INF_F, l = 0.f;
+      first = true;
+    };
+    if (n_steps > 0) begin();
+    for (int j = 0; j < n_steps; ++j) {
+      const int k0 = w.x.base + w.local * kKeys;
+      const bool same = j + 1 < n_steps && w.local + 1 < w.x.steps;
+      const uint32_t s_tmem = tmem + lane_off + (j & 1) * 128;
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(sfull0 + 8 * (j & 1), (j >> 1) & 1, p.wait_limit, abort_flag, p.dev_err))) break;
+      tc::fence_after();
+      float s[128];
+      {
+        float t[64];
+        tc::tmem_ld64(s_tmem, t);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[i] = t[i];
+        tc::tmem_ld64(s_tmem + 64, t);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[64 + i] = t[i];
+      }
+      const uint32_t bad = bad_sh[j % kBadRing];
+      if (bad || k0 < lo || k0 + kKeys - 1 > hi) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          const int c = k0 + i;
+          if (c < lo || c > hi || ((bad >> (i / p.box)) & 1)) s[i] = sc < 0.f ? CUDART_INF_F : -CUDART_INF_F;
+        }
+      }
+      // the maximum of scale * score: of the scores for a positive scale, of the
+      // negated ones for a negative
+      float mx;
+      {
+        float v[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+        if (sc >= 0.f) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) v[i & 3] = fmaxf(v[i & 3], s[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) v[i & 3] = fmaxf(v[i & 3], -s[i]);
+        }
+        mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        mx = mx == -CUDART_INF_F ? mx : mx * fabsf(sc);
+      }
+      const bool move = mx > m + 8.f;
+      if (__any_sync(0xffffffffu, move)) {
+        const float m2 = fmaxf(m, mx), f = m2 == -CUDART_INF_F ? 1.f : ex2(m - m2);
+        m = m2;
+        l *= f;
+        if (!first) {   // O holds the steps before: let the last one finish
+          if (!__all_sync(0xffffffffu, tc::mbar_wait(odone, (j - 1) & 1, p.wait_limit, abort_flag, p.dev_err))) break;
+          tc::fence_after();
+#pragma unroll
+          for (int c = 0; c < S::kDV; c += 32) {
+            float t[16];
+            uint32_t u[32];
+            tc::tmem_ld16(o_tmem + lane_off + c, t);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(t[i] * f);
+            tc::tmem_ld16(o_tmem + lane_off + c + 16, t);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[16 + i] = __float_as_uint(t[i] * f);
+            tc::tmem_st32(o_tmem + lane_off + c, u);
+          }
+        }
+      }
+      const float mb = m == -CUDART_INF_F ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t u[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float x = s[64 * g + 2 * i], y = s[64 * g + 2 * i + 1];
+          const float e0 = ex2(fmaf(x, sc, -mb)), e1 = ex2(fmaf(y, sc, -mb));
+          sum[(2 * i) & 3] += e0;
+          sum[(2 * i + 1) & 3] += e1;
+          u[i] = Half16<T>::pack(e0, e1);
+        }
+        tc::tmem_st32(s_tmem + 32 * g, u);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      // values that no row of the tile sees may be anything, and 0 times
+      // infinity is no zero: they are cleared in shared memory
+      if (k0 < w.x.lo || k0 + kKeys > w.x.end) {
+        // slot number of the step's first V slot
+        const int vq = S::kNK * (j + 1 + (same ? 1 : 0)) + S::kNV * j;
+        bool landed = true;
+        for (int h = 0; h < S::kNV; ++h)
+          landed = landed && tc::mbar_wait(full0 + 8 * ((vq + h) % NS), ((vq + h) / NS) & 1, p.wait_limit, abort_flag, p.dev_err);
+        if (!__all_sync(0xffffffffu, landed)) break;
+        for (int h = 0; h < S::kNV; ++h) {
+          const uint32_t vb = ring0 + ((vq + h) % NS) * S::kSlot;
+          // a thread clears one 16-byte piece of a row of every slab
+          for (int i = threadIdx.x; i < S::kVK * 8; i += 128) {
+            const int c = k0 + h * S::kVK + (i >> 3);
+            if (c < w.x.lo || c >= w.x.end) {
+#pragma unroll
+              for (int sl = 0; sl < S::kDV / 64; ++sl)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + sl * (S::kVK * 128) + i * 16), "r"(0) : "memory");
+            }
+          }
+        }
+        tc::fence_proxy_async();
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(pready0 + 8 * (j & 1));
+      first = false;
+      if (same) {
+        ++w.local;
+        continue;
+      }
+      // ---- the item's part is complete.  The barrier's parity tells two
+      // neighbouring phases apart, so the step before is waited for first (the
+      // one before that is complete: this step's scores were issued after it).
+      if (j > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(odone, (j - 1) & 1, p.wait_limit, abort_flag, p.dev_err))) break;
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(odone, j & 1, p.wait_limit, abort_flag, p.dev_err))) break;
+      tc::fence_after();
+      const bool closes = w.local + 1 == w.x.steps;
+      const bool in = tok < w.s.n;
+      if (opens && closes) {
+        const long long orow = (long long)(w.s.cu + tok) * a.n_q + w.head * p.group + r - tok * p.group;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        T* out = static_cast<T*>(a.out) + orow * D + w.part * S::kDV;
+#pragma unroll
+        for (int c = 0; c < S::kDV; c += 64) {
+          float t[64];
+          tc::tmem_ld64(o_tmem + lane_off + c, t);
+          if (in) {
+#pragma unroll
+            for (int i = 0; i < 64; i += 8)
+              *reinterpret_cast<uint4*>(out + c + i) =
+                  make_uint4(Half16<T>::pack(t[i] * inv, t[i + 1] * inv), Half16<T>::pack(t[i + 2] * inv, t[i + 3] * inv),
+                             Half16<T>::pack(t[i + 4] * inv, t[i + 5] * inv), Half16<T>::pack(t[i + 6] * inv, t[i + 7] * inv));
+          }
+        }
+        if (in && w.part == 0 && a.lse) a.lse[orow] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+      } else {
+        const long long slot = 2ll * blockIdx.x + (opens ? 1 : 0);
+        float* po = p.split.part_o + (slot * kRows + row) * S::kDV;
+#pragma unroll
+        for (int c = 0; c < S::kDV; c += 64) {
+          float t[64];
+          tc::tmem_ld64(o_tmem + lane_off + c, t);
+          if (in) {
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) *reinterpret_cast<float4*>(po + c + i) = make_float4(t[i], t[i + 1], t[i + 2], t[i + 3]);
+          }
+        }
+        p.split.part_ml[slot * kRows + row] = make_float2(m, l);
+        if (opens && threadIdx.x == 0)
+          p.split.recs[blockIdx.x] = {w.seq, w.head, w.t * PARTS + w.part,
+                                      (int)((first_step + j - w.local + w.x.steps - 1) / share)};
+      }
+      tc::fence_before();
+      if (j + 1 < n_steps) {
+        walk_next<PARTS>(w, p);
+        opens = true;
+        begin();
+      }
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D>
+static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
+  using S = Shape<D>;
+  static PerDevice attr;
+  if (!attr.get(dev.ordinal)) {
+    const cudaError_t e = cudaFuncSetAttribute(tile_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "tile attention smem attribute");
+    attr.set(dev.ordinal);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(kThr);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, p);
+  if (e != cudaSuccess) return cuda_fail(e, "tile attention launch");
+  return launch_attn_join(p.a, p.split, p.group, kRows, D, S::kDV, p.box, std::is_same<T, __nv_bfloat16>::value, p.grid, s);
+}
+
+template <typename T>
+static int launch_t(Params& p, int D, const DeviceInfo& dev, cudaStream_t s) {
+  switch (D) {
+    case 64: return launch<T, 64>(p, dev, s);
+    case 128: return launch<T, 128>(p, dev, s);
+    case 256: return launch<T, 256>(p, dev, s);
+    default: return launch<T, 512>(p, dev, s);
+  }
+}
+
+}  // namespace tile
+
+size_t attn_tile_ws_bytes(int D, const DeviceInfo& dev) { return attn_split_bytes(dev.sms, tile::kRows, D < 256 ? D : 256); }
+
+int launch_attn_tile(const AttnParams& a, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s) {
+  tile::Params p = {};
+  const bool bf16 = c.dtype == Q4_BF16;
+  const uint64_t rows = (uint64_t)c.n_pages * c.n_kv * c.page_size;
+  p.box = c.page_size % 64 == 0 ? 64 : c.page_size % 32 == 0 ? 32 : 16;
+  int st = encode_cache_rows(&p.tm_k, c.k, bf16, c.head_dim, rows, p.box, 1, "the K cache");
+  if (st == Q4_OK) st = encode_cache_rows(&p.tm_v, c.v, bf16, c.head_dim, rows, p.box, 1, "the V cache");
+  if (st != Q4_OK) return st;
+  p.a = a;
+  p.group = a.n_q / c.n_kv;
+  p.grid = dev.sms;
+  p.total_rows = (int)rows;
+  p.wait_limit = wait_limit();
+  p.dev_err = device_error_word();
+  p.split = attn_split(ws, p.grid, tile::kRows, c.head_dim < 256 ? c.head_dim : 256);
+  return bf16 ? tile::launch_t<__nv_bfloat16>(p, c.head_dim, dev, s) : tile::launch_t<__half>(p, c.head_dim, dev, s);
+}
+
+}  // namespace q4w

@@ -1,0 +1,75 @@
+// What the attention kernels share: the part of a sequence's work that its
+// lengths determine, and the joining of parts that several CTAs had.
+#pragma once
+
+#include <math_constants.h>
+
+#include "q4w_internal.cuh"
+#include "q4w_kv.cuh"
+
+namespace q4w {
+
+struct Seq {
+  int n, pos0;           // new tokens taken, position of the first
+  int base, end;         // keys [base, end) that any of them sees, base a multiple of `align`
+  int cu;                // the first one's index
+};
+
+// align: a power of two that divides the page size.
+__device__ __forceinline__ Seq seq_of(const AttnParams& a, int seq, int align) {
+  Seq s;
+  s.cu = a.kv.cu_tokens[seq];
+  const int n = a.kv.cu_tokens[seq + 1] - s.cu, len = max(a.kv.kv_lens[seq], 0);
+  s.n = s.cu >= 0 ? min(min(max(n, 0), a.max_q), max(a.T - s.cu, 0)) : 0;
+  s.pos0 = len - n;
+  s.base = kv_first(s.pos0, a.window) & ~(align - 1);
+  s.end = s.n > 0 ? min(s.pos0 + s.n, a.kv.max_pages * a.kv.page_size) : 0;
+  return s;
+}
+// More tokens than max_q, or a length that the block table does not hold.
+__device__ __forceinline__ bool seq_bad(const AttnParams& a, int seq) {
+  const int n = a.kv.cu_tokens[seq + 1] - a.kv.cu_tokens[seq];
+  return n > a.max_q || (n > 0 && a.kv.kv_lens[seq] > a.kv.max_pages * a.kv.page_size);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The parts of work that is cut.  The steps of all items form one line that is
+// cut into equal shares; CTA c leaves the part of an item that began before it
+// in slot 2 c, and the part of one that it begins and does not end in slot
+// 2 c + 1, with a record of how far that item goes.
+struct SplitRec {
+  int seq, head, tile;   // tile: of `rows` query rows, times the column parts of D, plus the part
+  int last;              // CTA that ends the item; -1: this CTA begins none that it does not end
+};
+struct AttnSplit {
+  float* part_o;         // [2 grid][rows][dv]: sums of the values
+  float2* part_ml;       // [2 grid][rows]: maximum (in units of log2 e) and sum
+  SplitRec* recs;        // [grid]
+};
+
+inline size_t attn_up256(size_t n) { return (n + 255) & ~(size_t)255; }
+inline size_t attn_split_bytes(int grid, int rows, int dv) {
+  return attn_up256(grid * sizeof(SplitRec)) + attn_up256(2 * (size_t)grid * rows * sizeof(float2)) +
+         attn_up256(2 * (size_t)grid * rows * dv * 4);
+}
+inline AttnSplit attn_split(void* ws, int grid, int rows, int dv) {
+  AttnSplit s;
+  char* w = static_cast<char*>(ws);
+  s.recs = reinterpret_cast<SplitRec*>(w);
+  w += attn_up256(grid * sizeof(SplitRec));
+  s.part_ml = reinterpret_cast<float2*>(w);
+  w += attn_up256(2 * (size_t)grid * rows * sizeof(float2));
+  s.part_o = reinterpret_cast<float*>(w);
+  return s;
+}
+
+// Joins what the recorded items left in their slots, in the order of the keys.
+int launch_attn_join(const AttnParams& a, const AttnSplit& split, int group, int rows, int D, int dv, int align,
+                     bool bf16, int grid, cudaStream_t s);
+
+}  // namespace q4w

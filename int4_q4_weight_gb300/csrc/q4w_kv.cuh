@@ -58,6 +58,9 @@ size_t attn_ws_bytes(int max_rows, int D, int n_seqs, const DeviceInfo& dev);
 bool attn_decode_fits(int max_rows, int D);
 size_t attn_decode_ws_bytes(int max_rows, int D, const DeviceInfo& dev);
 int launch_attn_decode(const AttnParams& a, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s);
+// Tiles of 128 query rows (k_attn_tile.cu).
+size_t attn_tile_ws_bytes(int D, const DeviceInfo& dev);
+int launch_attn_tile(const AttnParams& a, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s);
 int launch_kv_attention(const AttnParams& p, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s);
 
 int launch_logits_sample(const void* z, long long stride, int dtype, int rows, int V, const float* u,

@@ -229,6 +229,13 @@ def test_attention_long_and_split(cuda_lib, D, hq, new):
     check_attention(cuda_lib, c)
 
 
+@pytest.mark.parametrize("D,n,kv", [(256, [400, 3], [2000, 900]), (512, [100], [4000]), (512, [200, 3], [700, 900]),
+                                    (128, [900], [2500]), (64, [1000, 70], [1500, 3000])])
+def test_attention_several_steps_and_items_per_cta(cuda_lib, D, n, kv):
+    """More steps than SMs: shares of several steps that end and begin inside items."""
+    check_attention(cuda_lib, Case(n, kv, 8, 1, D, 64, F16, seed=D))
+
+
 @pytest.mark.parametrize("D,hq,hkv,new", [(256, 8, 1, 1), (512, 8, 1, 1), (64, 3, 1, 1), (256, 8, 1, 64), (512, 4, 1, 50), (128, 4, 2, 90)])
 def test_attention_rows_that_see_nothing(cuda_lib, D, hq, hkv, new):
     """A length of zero, and lengths shorter than the new tokens."""
