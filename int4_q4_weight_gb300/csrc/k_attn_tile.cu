@@ -4,18 +4,21 @@
 // A tile's rows are (token, query head of the group) pairs, so all heads of a
 // group share the keys that are read.  One pass over the keys, 128 a step:
 //   S[128 rows][128 keys] = Q K^T     A = Q, B = K, both in shared memory
-//   P = 2^(S scale log2(e) - m)       one thread per row, S read from TMEM,
-//                                     P (16 bits) written over it
+//   P = 2^(S scale log2(e) - m)       two threads per row, half of the keys
+//                                     each, S read from TMEM, P (16 bits)
+//                                     written over it
 //   O[128 rows][DV]      += P V       A = P in TMEM, B = V in shared memory
-// with the running maximum m and sum of each row in its thread.  m is moved
+// with the running maximum m and sum of each row in its threads.  m is moved
 // only when a score passes it by 2^8, so O (in TMEM) is rarely rescaled.
 // Two S tiles alternate: the scores of step j + 1 are formed while the softmax
 // of step j runs.  TMEM: S 2 x 128 columns, O 256 = all 512.  Head size 512 does
 // not fit: its two column halves of O are items of their own, which form the
 // scores twice (1.5 times the products).
 //
-// Warps: 0-3 softmax (warp w the rows 32 w ..), 4 issues the MMAs, 5 the TMA
-// loads, 6-7 load the query rows of the next item.  K and V go through one ring
+// Warps: 0-7 softmax (warp w the rows 32 (w mod 4) .., keys 64 (w div 4) ..), 8
+// issues the MMAs, 9 the TMA loads, 10-11 load the query rows of the next item.
+// The softmax is written to be short: a path that is taken once per item and
+// unrolled to hundreds of instructions cost 20000 cycles of instruction fetches.  K and V go through one ring
 // of slots in the order in which the MMAs take them: K slots of [128 keys][<=
 // 128 dims], V slots of [64 or 128 keys][DV], loaded in boxes of 16 to 64 rows
 // (the page size's share), 128-byte swizzle.
@@ -34,8 +37,9 @@ namespace q4w {
 namespace tile {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kThr = 256;
-constexpr int kMmaWarp = 4, kTmaWarp = 5, kQWarp = 6;
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kMmaWarp + 1, kQWarp = kTmaWarp + 1, kQWarps = 2;
+constexpr int kThr = (kQWarp + kQWarps) * 32;
 constexpr long long kDrainCycles = 2000000000LL;
 constexpr int kBadRing = 16;
 
@@ -50,7 +54,7 @@ struct Shape {
   static constexpr int kNV = kKeys / kVK;                    // V slots per step
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kSlots = (229376 - kQBytes) / kSlot < 12 ? (229376 - kQBytes) / kSlot : 12;   // 3, 5, 6, 12
-  static constexpr size_t kSmem = 1024 + kQBytes + (size_t)kSlots * kSlot;
+  static constexpr size_t kSmem = kQBytes + (size_t)kSlots * kSlot;   // with the static part, all 227 KB
 };
 
 struct Params {
@@ -147,7 +151,11 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
   constexpr int NS = S::kSlots, PARTS = S::kParts;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* smem = smem_raw;
+  if (tc::smem_u32(smem) & 1023) {   // the swizzle needs it; there is no room to move the buffers
+    if (threadIdx.x == 0) atomicOr(p.dev_err, 1u);
+    return;
+  }
   uint8_t* ring = smem + S::kQBytes;
   __shared__ uint64_t bars[2 * NS + 8];
   __shared__ uint32_t tmem_sh;
@@ -155,6 +163,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
   __shared__ int start_sh[6];
   __shared__ long long scan_sh[kThr / 32];
   __shared__ uint32_t bad_sh[kBadRing];   // per step: boxes whose page is none of the cache
+  __shared__ float row_sh[2][2][kRows];   // per half of the keys: the rows' maxima of a step, their sums of an item
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AttnParams& a = p.a;
   const uint32_t full0 = tc::smem_u32(bars), empty0 = full0 + 8 * NS;
@@ -166,8 +175,8 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     if (lane == 0) abort_sh = 0, start_sh[0] = -1;
     if (lane < 2 * NS + 8) {
       unsigned count = 1;
-      if (lane == 2 * NS) count = 64;                                // qfull: the loading threads
-      else if (lane == 2 * NS + 4 || lane == 2 * NS + 5) count = 4;  // pready: the softmax warps
+      if (lane == 2 * NS) count = kQWarps * 32;                               // qfull: the loading threads
+      else if (lane == 2 * NS + 4 || lane == 2 * NS + 5) count = kSoftWarps;  // pready
       tc::mbar_init(tc::smem_u32(bars + lane), count);
     }
     tc::mbar_fence_init();
@@ -272,23 +281,32 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     const int nb = kKeys / p.box;
     uint32_t q = 0;   // slots filled
     bool ok = true;
-    // cache rows of a step's boxes, lane b the box b
-    auto rows_of = [&](const Walk& y, int j) {
-      int row = p.total_rows;   // out of the cache: zeros
-      bool bad = false;
+    // A step's boxes, lane b the box b: the block-table entry is fetched a step
+    // before it is needed (the load takes longer than a slot's products).
+    struct Boxes {
+      int entry, off, head;   // entry -2: nothing to load
+    };
+    auto fetch = [&](const Walk& y) {
+      Boxes x = {-2, 0, y.head};
       const int pos = y.x.base + y.local * kKeys + lane * p.box;
       if (lane < nb && pos < y.x.end && pos + p.box > y.x.lo) {
-        const int page = kv_page(a.kv, y.seq, pos);
-        bad = page < 0;
-        if (!bad) row = (int)kv_row(a.kv, page, y.head) + pos % a.kv.page_size;
+        const int at = pos / a.kv.page_size;
+        x.off = pos - at * a.kv.page_size;
+        x.entry = at < a.kv.max_pages ? a.kv.block_table[(long long)y.seq * a.kv.max_pages + at] : -1;
+        if (x.entry < 0) x.entry = -1;
       }
+      return x;
+    };
+    // their rows of the cache; total_rows, out of the cache, gives zeros
+    auto rows_of = [&](const Boxes& x, int j) {
+      const bool bad = x.entry == -1 || x.entry >= a.kv.n_pages;
       const uint32_t mask = __ballot_sync(0xffffffffu, bad);
       if (lane == 0) {
         bad_sh[j % kBadRing] = mask;
         if (mask && a.err) *a.err = 1;
       }
       __syncwarp();
-      return row;
+      return bad || x.entry < 0 ? p.total_rows : (int)kv_row(a.kv, x.entry, x.head) + x.off;
     };
     auto acquire = [&]() {
       const uint32_t slot = q % NS;
@@ -322,21 +340,38 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       }
     };
     if (n_steps > 0) {
-      int row = rows_of(w, 0);
+      // w: the step whose boxes are fetched, two ahead of the values
+      bool same1 = false;             // whether step j + 1 belongs to step j's item
+      auto advance = [&]() {
+        same1 = w.local + 1 < w.x.steps;
+        if (same1) ++w.local; else walk_next<PARTS>(w, p);
+      };
+      Boxes nb1 = fetch(w);
+      int part = w.part;
+      int row = rows_of(nb1, 0);
       load_k(row);
+      int part1 = 0;
+      if (1 < n_steps) {
+        advance();
+        nb1 = fetch(w);
+        part1 = w.part;
+      }
       for (int j = 0; j < n_steps && ok; ++j) {
-        const int part = w.part;
-        bool same = false;
-        int next_row = 0;
-        if (j + 1 < n_steps) {
-          same = w.local + 1 < w.x.steps;
-          if (same) ++w.local; else walk_next<PARTS>(w, p);
-          next_row = rows_of(w, j + 1);
+        const bool same = same1;
+        const Boxes cur = nb1;
+        const int part_next = part1;
+        if (j + 2 < n_steps) {
+          advance();
+          nb1 = fetch(w);
+          part1 = w.part;
         }
-        if (same) load_k(next_row);
+        int next_row = 0;
+        if (j + 1 < n_steps) next_row = rows_of(cur, j + 1);
+        if (same && j + 1 < n_steps) load_k(next_row);
         load_v(row, part);
         if (!same && j + 1 < n_steps) load_k(next_row);
         row = next_row;
+        part = part_next;
       }
       // what was issued lands before the CTA leaves
       for (uint32_t i = q > (uint32_t)NS ? q - NS : 0u; i < q; ++i)
@@ -425,19 +460,22 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     __syncwarp();
   } else if (warp >= kQWarp) {
     // ------------------------------------------------------- query rows
-    const int th = threadIdx.x - kQWarp * 32;
     int item = 0;
     for (int j = 0; j < n_steps;) {
       if (!tc::mbar_wait(qempty, (item & 1) ^ 1, p.wait_limit, abort_flag, p.dev_err)) break;
       const int R = w.s.n * p.group;
+      // a warp takes whole rows (several, when a row is shorter than 512 bytes)
       constexpr int per_row = D / 8;   // 16-byte pieces
-      for (int i = th; i < kRows * per_row; i += 64) {
-        const int row = i / per_row, c = i % per_row, r = w.t * kRows + row;
+      constexpr int rows_at_once = per_row < 32 ? 32 / per_row : 1;
+#pragma unroll 4
+      for (int i = (warp - kQWarp) * rows_at_once; i < kRows; i += kQWarps * rows_at_once) {
+        const int row = i + (per_row < 32 ? lane / per_row : 0), r = w.t * kRows + row;
         const bool in = r < R;
         const int tok = in ? r / p.group : 0, h = in ? r - tok * p.group : 0;
-        const T* src = static_cast<const T*>(a.q) + (long long)(w.s.cu + tok) * a.q_stride +
-                       (long long)(w.head * p.group + h) * D + c * 8;
-        cp_async16(q_addr + (c >> 3) * (kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), src, in);
+        const T* src = static_cast<const T*>(a.q) + (long long)(w.s.cu + tok) * a.q_stride + (long long)(w.head * p.group + h) * D;
+#pragma unroll
+        for (int c = per_row < 32 ? lane % per_row : lane; c < per_row; c += 32)
+          cp_async16(q_addr + (c >> 3) * (kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), src + c * 8, in);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       tc::fence_proxy_async();
@@ -448,14 +486,24 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     }
   } else {
     // ----------------------------------------------------------- softmax
-    const int row = threadIdx.x;
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const int row = threadIdx.x & (kRows - 1), half = warp >> 2;   // half of the step's keys, of O's columns
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     // scores in units of log2 e; a scale of zero becomes one that still takes
     // the masked scores' infinity to infinity
     const float sc = a.scale == 0.f ? 1e-30f : a.scale * 1.4426950408889634f;
     float m = -CUDART_INF_F, l = 0.f;
-    bool first = true, opens = w.local == 0;
+    bool first = true, opens = w.local == 0, dead = false;
     int r = 0, lo = 0, hi = -1, tok = 0;
+    // the two warps of the same rows meet; a dead one too, so that none is left waiting
+    auto meet = [&]() {
+      tc::fence_before();
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+      tc::fence_after();
+    };
+    auto wait = [&](uint32_t bar, uint32_t par) {
+      if (!dead) dead = !__all_sync(0xffffffffu, tc::mbar_wait(bar, par, p.wait_limit, abort_flag, p.dev_err));
+      tc::fence_after();
+    };
     auto begin = [&]() {
       r = w.t * kRows + row;
       tok = r / p.group;
@@ -466,96 +514,91 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       first = true;
     };
     if (n_steps > 0) begin();
+    constexpr int kHalfO = S::kDV / 2;
+    const uint32_t o_half = o_tmem + lane_off + half * kHalfO;
     for (int j = 0; j < n_steps; ++j) {
-      const int k0 = w.x.base + w.local * kKeys;
+      const int k0 = w.x.base + w.local * kKeys, kh = k0 + 64 * half;   // the step's keys, this thread's
       const bool same = j + 1 < n_steps && w.local + 1 < w.x.steps;
       const uint32_t s_tmem = tmem + lane_off + (j & 1) * 128;
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(sfull0 + 8 * (j & 1), (j >> 1) & 1, p.wait_limit, abort_flag, p.dev_err))) break;
-      tc::fence_after();
-      float s[128];
-      {
-        float t[64];
-        tc::tmem_ld64(s_tmem, t);
-#pragma unroll
-        for (int i = 0; i < 64; ++i) s[i] = t[i];
-        tc::tmem_ld64(s_tmem + 64, t);
-#pragma unroll
-        for (int i = 0; i < 64; ++i) s[64 + i] = t[i];
-      }
+      wait(sfull0 + 8 * (j & 1), (j >> 1) & 1);
+      float s[64];
+      tc::tmem_ld64(s_tmem + 64 * half, s);
       const uint32_t bad = bad_sh[j % kBadRing];
-      if (bad || k0 < lo || k0 + kKeys - 1 > hi) {
+      if (bad || kh < lo || kh + 63 > hi) {
+        // bit i: the row sees key kh + i
+        auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+        unsigned long long see = below(hi + 1 - kh) & ~below(lo - kh);
+        if (bad) {
+          for (int i = 0; i < 64; i += 16)
+            if ((bad >> ((64 * half + i) / p.box)) & 1) see &= ~(0xffffull << i);
+        }
+        const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
+        const float none = sc < 0.f ? CUDART_INF_F : -CUDART_INF_F;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) {
-          const int c = k0 + i;
-          if (c < lo || c > hi || ((bad >> (i / p.box)) & 1)) s[i] = sc < 0.f ? CUDART_INF_F : -CUDART_INF_F;
+        for (int i = 0; i < 32; ++i) {
+          s[i] = (see0 >> i) & 1 ? s[i] : none;
+          s[32 + i] = (see1 >> i) & 1 ? s[32 + i] : none;
         }
       }
       // the maximum of scale * score: of the scores for a positive scale, of the
       // negated ones for a negative
-      float mx;
       {
         float v[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
         if (sc >= 0.f) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) v[i & 3] = fmaxf(v[i & 3], s[i]);
+          for (int i = 0; i < 64; ++i) v[i & 3] = fmaxf(v[i & 3], s[i]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) v[i & 3] = fmaxf(v[i & 3], -s[i]);
+          for (int i = 0; i < 64; ++i) v[i & 3] = fmaxf(v[i & 3], -s[i]);
         }
-        mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-        mx = mx == -CUDART_INF_F ? mx : mx * fabsf(sc);
+        float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        row_sh[half][j & 1][row] = mx == -CUDART_INF_F ? mx : mx * fabsf(sc);
       }
-      const bool move = mx > m + 8.f;
-      if (__any_sync(0xffffffffu, move)) {
+      meet();
+      const float mx = fmaxf(row_sh[0][j & 1][row], row_sh[1][j & 1][row]);
+      if (__any_sync(0xffffffffu, mx > m + 8.f)) {
         const float m2 = fmaxf(m, mx), f = m2 == -CUDART_INF_F ? 1.f : ex2(m - m2);
         m = m2;
         l *= f;
         if (!first) {   // O holds the steps before: let the last one finish
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(odone, (j - 1) & 1, p.wait_limit, abort_flag, p.dev_err))) break;
-          tc::fence_after();
-#pragma unroll
-          for (int c = 0; c < S::kDV; c += 32) {
-            float t[16];
+          wait(odone, (j - 1) & 1);
+#pragma unroll 1
+          for (int c = 0; c < kHalfO; c += 32) {
+            float t[32];
             uint32_t u[32];
-            tc::tmem_ld16(o_tmem + lane_off + c, t);
+            tc::tmem_ld32(o_half + c, t);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(t[i] * f);
-            tc::tmem_ld16(o_tmem + lane_off + c + 16, t);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) u[16 + i] = __float_as_uint(t[i] * f);
-            tc::tmem_st32(o_tmem + lane_off + c, u);
+            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(t[i] * f);
+            tc::tmem_st32(o_half + c, u);
           }
         }
       }
       const float mb = m == -CUDART_INF_F ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      {
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t u[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float x = s[64 * g + 2 * i], y = s[64 * g + 2 * i + 1];
-          const float e0 = ex2(fmaf(x, sc, -mb)), e1 = ex2(fmaf(y, sc, -mb));
+          const float e0 = ex2(fmaf(s[2 * i], sc, -mb)), e1 = ex2(fmaf(s[2 * i + 1], sc, -mb));
           sum[(2 * i) & 3] += e0;
           sum[(2 * i + 1) & 3] += e1;
           u[i] = Half16<T>::pack(e0, e1);
         }
-        tc::tmem_st32(s_tmem + 32 * g, u);
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // P of the other half lies where this half's scores are: both have read
+        // theirs (meet())
+        tc::tmem_st32(s_tmem + 32 * half, u);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       // values that no row of the tile sees may be anything, and 0 times
       // infinity is no zero: they are cleared in shared memory
       if (k0 < w.x.lo || k0 + kKeys > w.x.end) {
         // slot number of the step's first V slot
         const int vq = S::kNK * (j + 1 + (same ? 1 : 0)) + S::kNV * j;
-        bool landed = true;
-        for (int h = 0; h < S::kNV; ++h)
-          landed = landed && tc::mbar_wait(full0 + 8 * ((vq + h) % NS), ((vq + h) / NS) & 1, p.wait_limit, abort_flag, p.dev_err);
-        if (!__all_sync(0xffffffffu, landed)) break;
+        for (int h = 0; h < S::kNV; ++h) wait(full0 + 8 * ((vq + h) % NS), ((vq + h) / NS) & 1);
         for (int h = 0; h < S::kNV; ++h) {
           const uint32_t vb = ring0 + ((vq + h) % NS) * S::kSlot;
           // a thread clears one 16-byte piece of a row of every slab
-          for (int i = threadIdx.x; i < S::kVK * 8; i += 128) {
+          for (int i = threadIdx.x; i < S::kVK * 8; i += kSoftWarps * 32) {
             const int c = k0 + h * S::kVK + (i >> 3);
             if (c < w.x.lo || c >= w.x.end) {
 #pragma unroll
@@ -577,42 +620,39 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       // ---- the item's part is complete.  The barrier's parity tells two
       // neighbouring phases apart, so the step before is waited for first (the
       // one before that is complete: this step's scores were issued after it).
-      if (j > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(odone, (j - 1) & 1, p.wait_limit, abort_flag, p.dev_err))) break;
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(odone, j & 1, p.wait_limit, abort_flag, p.dev_err))) break;
-      tc::fence_after();
-      const bool closes = w.local + 1 == w.x.steps;
-      const bool in = tok < w.s.n;
-      if (opens && closes) {
-        const long long orow = (long long)(w.s.cu + tok) * a.n_q + w.head * p.group + r - tok * p.group;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        T* out = static_cast<T*>(a.out) + orow * D + w.part * S::kDV;
+      if (j > 0) wait(odone, (j - 1) & 1);
+      wait(odone, j & 1);
+      const bool closes = w.local + 1 == w.x.steps, whole = opens && closes;
+      const bool in = tok < w.s.n && !dead;
+      // the row's sum: of both halves
+      row_sh[half][j & 1][row] = l;   // every maximum in it has been read: the step's products are complete
+      meet();
+      l = row_sh[0][j & 1][row] + row_sh[1][j & 1][row];
+      const long long orow = (long long)(w.s.cu + tok) * a.n_q + w.head * p.group + r - tok * p.group;
+      const long long slot = 2ll * blockIdx.x + (opens ? 1 : 0);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      T* out = static_cast<T*>(a.out) + orow * D + w.part * S::kDV + half * kHalfO;
+      float* po = p.split.part_o + (slot * kRows + row) * S::kDV + half * kHalfO;
+#pragma unroll 1
+      for (int c = 0; c < kHalfO; c += 32) {
+        float t[32];
+        tc::tmem_ld32(o_half + c, t);
+        if (!in) continue;
+        if (whole) {
 #pragma unroll
-        for (int c = 0; c < S::kDV; c += 64) {
-          float t[64];
-          tc::tmem_ld64(o_tmem + lane_off + c, t);
-          if (in) {
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(out + c + i) =
+                make_uint4(Half16<T>::pack(t[i] * inv, t[i + 1] * inv), Half16<T>::pack(t[i + 2] * inv, t[i + 3] * inv),
+                           Half16<T>::pack(t[i + 4] * inv, t[i + 5] * inv), Half16<T>::pack(t[i + 6] * inv, t[i + 7] * inv));
+        } else {
 #pragma unroll
-            for (int i = 0; i < 64; i += 8)
-              *reinterpret_cast<uint4*>(out + c + i) =
-                  make_uint4(Half16<T>::pack(t[i] * inv, t[i + 1] * inv), Half16<T>::pack(t[i + 2] * inv, t[i + 3] * inv),
-                             Half16<T>::pack(t[i + 4] * inv, t[i + 5] * inv), Half16<T>::pack(t[i + 6] * inv, t[i + 7] * inv));
-          }
+          for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(po + c + i) = make_float4(t[i], t[i + 1], t[i + 2], t[i + 3]);
         }
-        if (in && w.part == 0 && a.lse) a.lse[orow] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
-      } else {
-        const long long slot = 2ll * blockIdx.x + (opens ? 1 : 0);
-        float* po = p.split.part_o + (slot * kRows + row) * S::kDV;
-#pragma unroll
-        for (int c = 0; c < S::kDV; c += 64) {
-          float t[64];
-          tc::tmem_ld64(o_tmem + lane_off + c, t);
-          if (in) {
-#pragma unroll
-            for (int i = 0; i < 64; i += 4) *reinterpret_cast<float4*>(po + c + i) = make_float4(t[i], t[i + 1], t[i + 2], t[i + 3]);
-          }
-        }
-        p.split.part_ml[slot * kRows + row] = make_float2(m, l);
-        if (opens && threadIdx.x == 0)
+      }
+      if (half == 0) {
+        if (!whole) p.split.part_ml[slot * kRows + row] = make_float2(m, l);
+        else if (in && w.part == 0 && a.lse) a.lse[orow] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+        if (opens && !closes && row == 0)
           p.split.recs[blockIdx.x] = {w.seq, w.head, w.t * PARTS + w.part,
                                       (int)((first_step + j - w.local + w.x.steps - 1) / share)};
       }
