@@ -5,8 +5,8 @@
 namespace q4w {
 namespace attn {
 
-// Block: 64 elements of 8 rows of one item; four groups of threads take every
-// fourth part.
+// Block: 64 elements of 8 rows of one item at a time; four groups of threads
+// take every fourth part.  The blocks of an item take its row groups in turn.
 constexpr int kJoinThr = 512;
 
 template <typename T>
@@ -19,47 +19,50 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const __grid_constant__ 
   const SplitRec rec = p.recs[c0];
   if (rec.last < 0) return;
   const Seq s = seq_of(a, rec.seq, align);
-  const int cols = D / dv, tile = rec.tile / cols;
+  const int cols = D / dv, tile = rec.tile / cols, tokens = rows / group;   // a tile has whole tokens
+  const int used = min(tokens, s.n - tile * tokens) * group;                // its rows
   const int part = threadIdx.x >> 7, rr = (threadIdx.x >> 4) & 7, d = blockIdx.y * 64 + 4 * (threadIdx.x & 15);
-  const int lr = blockIdx.z * 8 + rr, r = tile * rows + lr;   // row of the tile, of the sequence
-  if (tile * rows + (int)blockIdx.z * 8 >= s.n * group) return;
-  const bool in = r < s.n * group;
   const int np = rec.last - c0 + 1;
-  auto slot = [&](int i) { return (i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i)) * rows + lr; };
-  float mm = -CUDART_INF_F;
-  if (in) {
-    for (int i = threadIdx.x & 15; i < np; i += 16) mm = fmaxf(mm, p.part_ml[slot(i)].x);
-  }
+  for (int r0 = blockIdx.z * 8; r0 < used; r0 += gridDim.z * 8) {
+    const int lr = r0 + rr;
+    const bool in = lr < used;
+    auto slot = [&](int i) { return (i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i)) * rows + lr; };
+    float mm = -CUDART_INF_F;
+    if (in) {
+      for (int i = threadIdx.x & 15; i < np; i += 16) mm = fmaxf(mm, p.part_ml[slot(i)].x);
+    }
 #pragma unroll
-  for (int x = 8; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  if (in) {
+    for (int x = 8; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (in) {
 #pragma unroll 4
-    for (int i = part; i < np; i += 4) {
-      const float2 ml = p.part_ml[slot(i)];
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * dv + d);
-      const float f = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - mm);
-      l = fmaf(ml.y, f, l);
-      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+      for (int i = part; i < np; i += 4) {
+        const float2 ml = p.part_ml[slot(i)];
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * dv + d);
+        const float f = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - mm);
+        l = fmaf(ml.y, f, l);
+        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+      }
     }
-  }
-  sum_sh[threadIdx.x] = o;
-  if ((threadIdx.x & 15) == 0) l_sh[part][rr] = l;
-  __syncthreads();
-  if (part == 0 && in) {
-    l = (l_sh[0][rr] + l_sh[1][rr]) + (l_sh[2][rr] + l_sh[3][rr]);
+    __syncthreads();
+    sum_sh[threadIdx.x] = o;
+    if ((threadIdx.x & 15) == 0) l_sh[part][rr] = l;
+    __syncthreads();
+    if (part == 0 && in) {
+      l = (l_sh[0][rr] + l_sh[1][rr]) + (l_sh[2][rr] + l_sh[3][rr]);
 #pragma unroll
-    for (int i = 1; i < 4; ++i) {
-      const float4 v = sum_sh[threadIdx.x + 128 * i];
-      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+      for (int i = 1; i < 4; ++i) {
+        const float4 v = sum_sh[threadIdx.x + 128 * i];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+      }
+      const int tok = tile * tokens + lr / group, col = rec.tile % cols;
+      const long long row = (long long)(s.cu + tok) * a.n_q + rec.head * group + lr % group;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + col * dv + d) =
+          make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
+      if (d == 0 && col == 0 && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
     }
-    const int tok = r / group, col = rec.tile % cols;
-    const long long row = (long long)(s.cu + tok) * a.n_q + rec.head * group + r - tok * group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + col * dv + d) =
-        make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
-    if (d == 0 && col == 0 && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -68,7 +71,7 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const __grid_constant__ 
 int launch_attn_join(const AttnParams& a, const AttnSplit& split, int group, int rows, int D, int dv, int align,
                      bool bf16, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, dv / 64, rows / 8);
+  cfg.gridDim = dim3(grid, dv / 64, rows / 8 < 4 ? rows / 8 : 4);
   cfg.blockDim = dim3(attn::kJoinThr);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

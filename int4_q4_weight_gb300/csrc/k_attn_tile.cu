@@ -16,12 +16,14 @@
 // scores twice (1.5 times the products).
 //
 // Warps: 0-7 softmax (warp w the rows 32 (w mod 4) .., keys 64 (w div 4) ..), 8
-// issues the MMAs, 9 the TMA loads, 10-11 load the query rows of the next item.
+// issues the MMAs, 9 the loads of K and V, 10 those of the next item's query rows
+// (a box of whole tokens: a tile has floor(128 / group) of them).
 // The softmax is written to be short: a path that is taken once per item and
 // unrolled to hundreds of instructions cost 20000 cycles of instruction fetches.  K and V go through one ring
-// of slots in the order in which the MMAs take them: K slots of [128 keys][<=
-// 128 dims], V slots of [64 or 128 keys][DV], loaded in boxes of 16 to 64 rows
-// (the page size's share), 128-byte swizzle.
+// of 32 KB slots in the order in which the MMAs take them: K slots of [128
+// keys][128 dims], V slots of [64 or 128 keys][DV], loaded in boxes of 16 to 64
+// rows (the page size's share), 128-byte swizzle (16 KB slots: half as many
+// bytes per box, and a third slower).
 //
 // Split: the steps of all items (sequence, KV head, tile) form one line that is
 // cut into equal shares, one CTA per SM; causal tiles of any length and ragged
@@ -38,7 +40,7 @@ namespace tile {
 
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kMmaWarp + 1, kQWarp = kTmaWarp + 1, kQWarps = 2;
+constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kMmaWarp + 1, kQWarp = kTmaWarp + 1, kQWarps = 1;
 constexpr int kThr = (kQWarp + kQWarps) * 32;
 constexpr long long kDrainCycles = 2000000000LL;
 constexpr int kBadRing = 16;
@@ -50,7 +52,7 @@ struct Shape {
   static constexpr int kKD = D < 128 ? D : 128;              // dims of a K slot
   static constexpr int kNK = D / kKD;                        // K slots per step
   static constexpr int kSlot = kKeys * kKD * 2;              // bytes: 32 KB, 16 KB for D = 64
-  static constexpr int kVK = kSlot / (kDV * 2);              // keys of a V slot
+  static constexpr int kVK = kSlot / (kDV * 2);              // keys of a V slot: 64, 128
   static constexpr int kNV = kKeys / kVK;                    // V slots per step
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kSlots = (229376 - kQBytes) / kSlot < 12 ? (229376 - kQBytes) / kSlot : 12;   // 3, 5, 6, 12
@@ -58,12 +60,13 @@ struct Shape {
 };
 
 struct Params {
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_k, tm_v, tm_q;
   AttnParams a;
   AttnSplit split;
   unsigned* dev_err;
   long long wait_limit;
-  int group, total_rows, grid;
+  int group, tokens;     // query heads per KV head, tokens of a tile
+  int total_rows, grid;
   int box;               // rows of a TMA box: 16, 32 or 64, a divisor of the page size
 };
 
@@ -71,16 +74,16 @@ struct Params {
 struct Span {
   int lo, base, end, steps;   // lo: the first key that its first token sees
 };
-__device__ __forceinline__ Span span_of(const AttnParams& a, const Seq& s, int group, int t, int box) {
+__device__ __forceinline__ Span span_of(const AttnParams& a, const Seq& s, int tokens, int t, int box) {
   Span x;
-  const int j0 = t * kRows / group, j1 = min((t * kRows + kRows - 1) / group, s.n - 1);
+  const int j0 = t * tokens, j1 = min(j0 + tokens, s.n) - 1;
   x.lo = kv_first(s.pos0 + j0, a.window);
   x.base = x.lo & ~(box - 1);
   x.end = min(s.end, s.pos0 + j1 + 1);
   x.steps = x.end > x.base ? (x.end - x.base + kKeys - 1) / kKeys : 1;
   return x;
 }
-__device__ __forceinline__ int tiles_of(const Seq& s, int group) { return (s.n * group + kRows - 1) / kRows; }
+__device__ __forceinline__ int tiles_of(const Seq& s, int tokens) { return (s.n + tokens - 1) / tokens; }
 
 // A walk over the items of a CTA's share: for each sequence its heads, their
 // column parts, their tiles.
@@ -91,7 +94,7 @@ struct Walk {
   Span x;
 };
 template <int PARTS>
-__device__ __forceinline__ void walk_item(Walk& w, const Params& p) { w.x = span_of(p.a, w.s, p.group, w.t, p.box); }
+__device__ __forceinline__ void walk_item(Walk& w, const Params& p) { w.x = span_of(p.a, w.s, p.tokens, w.t, p.box); }
 // To the next item (the caller knows that there is one).
 template <int PARTS>
 __device__ __forceinline__ void walk_next(Walk& w, const Params& p) {
@@ -106,7 +109,7 @@ __device__ __forceinline__ void walk_next(Walk& w, const Params& p) {
           ++w.seq;
           if (w.seq >= p.a.kv.n_seqs) return;
           w.s = seq_of(p.a, w.seq, p.box);
-          w.n_tiles = tiles_of(w.s, p.group);
+          w.n_tiles = tiles_of(w.s, p.tokens);
         } while (w.n_tiles == 0);
       }
     }
@@ -141,10 +144,6 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t lbo) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ Params p) {
   using S = Shape<D>;
@@ -175,8 +174,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     if (lane == 0) abort_sh = 0, start_sh[0] = -1;
     if (lane < 2 * NS + 8) {
       unsigned count = 1;
-      if (lane == 2 * NS) count = kQWarps * 32;                               // qfull: the loading threads
-      else if (lane == 2 * NS + 4 || lane == 2 * NS + 5) count = kSoftWarps;  // pready
+      if (lane == 2 * NS + 4 || lane == 2 * NS + 5) count = kSoftWarps;  // pready
       tc::mbar_init(tc::smem_u32(bars + lane), count);
     }
     tc::mbar_fence_init();
@@ -192,9 +190,9 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     int* steps_sh = reinterpret_cast<int*>(ring);   // steps of one head and part of each sequence
     for (int q = warp; q < a.kv.n_seqs; q += kThr / 32) {
       const Seq s = seq_of(a, q, p.box);
-      const int nt = tiles_of(s, p.group);
+      const int nt = tiles_of(s, p.tokens);
       int sum = 0;
-      for (int t = lane; t < nt; t += 32) sum += span_of(a, s, p.group, t, p.box).steps;
+      for (int t = lane; t < nt; t += 32) sum += span_of(a, s, p.tokens, t, p.box).steps;
       sum = __reduce_add_sync(0xffffffffu, sum);
       if (lane == 0) {
         steps_sh[q] = sum;
@@ -245,10 +243,10 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     // the tile: every warp scans the sequence's tiles, 32 at a time
     w.seq = start_sh[0], w.head = start_sh[1], w.part = start_sh[2];
     w.s = seq_of(a, w.seq, p.box);
-    w.n_tiles = tiles_of(w.s, p.group);
+    w.n_tiles = tiles_of(w.s, p.tokens);
     int left = start_sh[3];
     for (int t0 = 0;; t0 += 32) {
-      const int n = t0 + lane < w.n_tiles ? span_of(a, w.s, p.group, t0 + lane, p.box).steps : 0;
+      const int n = t0 + lane < w.n_tiles ? span_of(a, w.s, p.tokens, t0 + lane, p.box).steps : 0;
       int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -461,29 +459,20 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
   } else if (warp >= kQWarp) {
     // ------------------------------------------------------- query rows
     int item = 0;
-    for (int j = 0; j < n_steps;) {
-      if (!tc::mbar_wait(qempty, (item & 1) ^ 1, p.wait_limit, abort_flag, p.dev_err)) break;
-      const int R = w.s.n * p.group;
-      // a warp takes whole rows (several, when a row is shorter than 512 bytes)
-      constexpr int per_row = D / 8;   // 16-byte pieces
-      constexpr int rows_at_once = per_row < 32 ? 32 / per_row : 1;
-#pragma unroll 4
-      for (int i = (warp - kQWarp) * rows_at_once; i < kRows; i += kQWarps * rows_at_once) {
-        const int row = i + (per_row < 32 ? lane / per_row : 0), r = w.t * kRows + row;
-        const bool in = r < R;
-        const int tok = in ? r / p.group : 0, h = in ? r - tok * p.group : 0;
-        const T* src = static_cast<const T*>(a.q) + (long long)(w.s.cu + tok) * a.q_stride + (long long)(w.head * p.group + h) * D;
-#pragma unroll
-        for (int c = per_row < 32 ? lane % per_row : lane; c < per_row; c += 32)
-          cp_async16(q_addr + (c >> 3) * (kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), src + c * 8, in);
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      tc::fence_proxy_async();
-      tc::mbar_arrive(qfull);
-      ++item;
+    for (int j = 0; j < n_steps; ++item) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(qempty, (item & 1) ^ 1, p.wait_limit, abort_flag, p.dev_err))) break;
+      if (lane == 0) tc::mbar_expect_tx(qfull, (D / 64) * p.tokens * p.group * 128);
+      __syncwarp();
+      // tokens behind the sequence's are another's or, behind the last, zeros:
+      // their rows are masked and not written
+      if (lane < D / 64)
+        tc::tma_load_4d(q_addr + lane * (kRows * 128), &p.tm_q, 0, w.head * p.group, w.s.cu + w.t * p.tokens, lane, qfull);
       j += w.x.steps - w.local;
       if (j < n_steps) walk_next<PARTS>(w, p);
     }
+    // the loads land before the CTA leaves
+    if (item > 0) tc::mbar_drain(qfull, (item - 1) & 1, kDrainCycles, p.dev_err);
+    __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax
     const int row = threadIdx.x & (kRows - 1), half = warp >> 2;   // half of the step's keys, of O's columns
@@ -493,7 +482,8 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     const float sc = a.scale == 0.f ? 1e-30f : a.scale * 1.4426950408889634f;
     float m = -CUDART_INF_F, l = 0.f;
     bool first = true, opens = w.local == 0, dead = false;
-    int r = 0, lo = 0, hi = -1, tok = 0;
+    const int row_tok = row < p.tokens * p.group ? row / p.group : 1 << 28, row_head = row % p.group;
+    int lo = 0, hi = -1, tok = 0;
     // the two warps of the same rows meet; a dead one too, so that none is left waiting
     auto meet = [&]() {
       tc::fence_before();
@@ -505,8 +495,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       tc::fence_after();
     };
     auto begin = [&]() {
-      r = w.t * kRows + row;
-      tok = r / p.group;
+      tok = w.t * p.tokens + row_tok;
       const int pos = tok < w.s.n ? w.s.pos0 + tok : -1;
       lo = kv_first(pos, a.window);
       hi = min(pos, w.x.end - 1);
@@ -628,7 +617,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       row_sh[half][j & 1][row] = l;   // every maximum in it has been read: the step's products are complete
       meet();
       l = row_sh[0][j & 1][row] + row_sh[1][j & 1][row];
-      const long long orow = (long long)(w.s.cu + tok) * a.n_q + w.head * p.group + r - tok * p.group;
+      const long long orow = (long long)(w.s.cu + tok) * a.n_q + w.head * p.group + row_head;
       const long long slot = 2ll * blockIdx.x + (opens ? 1 : 0);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       T* out = static_cast<T*>(a.out) + orow * D + w.part * S::kDV + half * kHalfO;
@@ -718,9 +707,11 @@ int launch_attn_tile(const AttnParams& a, const q4_kv_cache& c, void* ws, const 
   p.box = c.page_size % 64 == 0 ? 64 : c.page_size % 32 == 0 ? 32 : 16;
   int st = encode_cache_rows(&p.tm_k, c.k, bf16, c.head_dim, rows, p.box, 1, "the K cache");
   if (st == Q4_OK) st = encode_cache_rows(&p.tm_v, c.v, bf16, c.head_dim, rows, p.box, 1, "the V cache");
+  p.group = a.n_q / c.n_kv;
+  p.tokens = tile::kRows / p.group;
+  if (st == Q4_OK) st = encode_query_rows(&p.tm_q, a.q, bf16, c.head_dim, a.n_q, a.T, a.q_stride, p.group, p.tokens);
   if (st != Q4_OK) return st;
   p.a = a;
-  p.group = a.n_q / c.n_kv;
   p.grid = dev.sms;
   p.total_rows = (int)rows;
   p.wait_limit = wait_limit();

@@ -816,6 +816,22 @@ int encode_cache_rows(CUtensorMap* tm, const void* base, bool bf16, int D, uint6
   return Q4_OK;
 }
 
+int encode_query_rows(CUtensorMap* tm, const void* base, bool bf16, int D, int n_q, int T, long long stride,
+                      uint32_t heads, uint32_t tokens) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(Q4_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[4] = {64, (cuuint64_t)n_q, (cuuint64_t)T, (cuuint64_t)D / 64};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2, 128};
+  const cuuint32_t box[4] = {64, heads, tokens, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(Q4_ERR_CUDA, "tensor map for the queries: driver error %d", (int)r);
+  return Q4_OK;
+}
+
 size_t gemm_ws_bytes(int K) { return ((size_t)gemm::kTok * K * 2 + 255) & ~(size_t)255; }
 size_t mma16_ws_bytes(int K) { return ((size_t)16 * K * 2 + 255) & ~(size_t)255; }
 
