@@ -5,73 +5,112 @@
 namespace q4w {
 namespace attn {
 
-// Block: 64 elements of 8 rows of one item at a time; four groups of threads
-// take every fourth part.  The blocks of an item take its row groups in turn.
+// Task: 64 elements of 8 rows of one recorded item; four groups of threads take
+// every fourth part.  Every block reads all the records, so the tasks of the
+// few items that were split spread over the device whatever CTA recorded them.
 constexpr int kJoinThr = 512;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThr) join_kernel(const __grid_constant__ AttnParams a, const AttnSplit p,
-                                                        int group, int rows, int D, int dv, int align) {
+__global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n_recs, int n_q, int rows, int D, int dv,
+                                                        void* out_, float* lse) {
   __shared__ float4 sum_sh[kJoinThr];
-  __shared__ float l_sh[4][8];
+  __shared__ float2 ml_sh[4][8];
+  __shared__ int first_sh[kJoinThr + 1];   // tasks before a record's
+  __shared__ SplitRec rec_sh[kJoinThr];
+  __shared__ int warp_sh[kJoinThr / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  const int c0 = blockIdx.x;
-  const SplitRec rec = p.recs[c0];
-  if (rec.last < 0) return;
-  const Seq s = seq_of(a, rec.seq, align);
-  const int cols = D / dv, tile = rec.tile / cols, tokens = rows / group;   // a tile has whole tokens
-  const int used = min(tokens, s.n - tile * tokens) * group;                // its rows
-  const int part = threadIdx.x >> 7, rr = (threadIdx.x >> 4) & 7, d = blockIdx.y * 64 + 4 * (threadIdx.x & 15);
-  const int np = rec.last - c0 + 1;
-  for (int r0 = blockIdx.z * 8; r0 < used; r0 += gridDim.z * 8) {
-    const int lr = r0 + rr;
-    const bool in = lr < used;
-    auto slot = [&](int i) { return (i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i)) * rows + lr; };
-    float mm = -CUDART_INF_F;
-    if (in) {
-      for (int i = threadIdx.x & 15; i < np; i += 16) mm = fmaxf(mm, p.part_ml[slot(i)].x);
+  {
+    int n = 0;
+    if (threadIdx.x < n_recs) {
+      const SplitRec r = p.recs[threadIdx.x];
+      rec_sh[threadIdx.x] = r;
+      n = r.last < 0 ? 0 : (r.used + 7) / 8 * (dv / 64);
     }
+    int incl = n;
 #pragma unroll
-    for (int x = 8; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) warp_sh[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sh[w];
+    first_sh[threadIdx.x + 1] = before + incl;
+    if (threadIdx.x == 0) first_sh[0] = 0;
+    __syncthreads();
+  }
+  const int part = threadIdx.x >> 7, rr = (threadIdx.x >> 4) & 7;
+  const int total = first_sh[kJoinThr];
+  for (int task = blockIdx.x; task < total; task += gridDim.x) {
+    int lo = 0, hi = n_recs;   // the record: the last one that begins at or before the task
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first_sh[mid] <= task) lo = mid; else hi = mid;
+    }
+    const SplitRec rec = rec_sh[lo];
+    const int c0 = lo, sub = task - first_sh[lo], d = sub % (dv / 64) * 64 + 4 * (threadIdx.x & 15);
+    const int lr = sub / (dv / 64) * 8 + rr, np = rec.last - c0 + 1;
+    const bool in = lr < rec.used;
+    auto slot = [&](int i) { return (i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i)) * rows + lr; };
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
+    float l = 0.f, m = -CUDART_INF_F;
     if (in) {
-#pragma unroll 4
-      for (int i = part; i < np; i += 4) {
-        const float2 ml = p.part_ml[slot(i)];
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * dv + d);
-        const float f = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - mm);
-        l = fmaf(ml.y, f, l);
-        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+      for (int i = part; i < np; i += 16) {   // four parts at a time
+        float2 ml[4];
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int at = i + 4 * k;
+          ml[k] = at < np ? p.part_ml[slot(at)] : make_float2(-CUDART_INF_F, 0.f);
+          v[k] = at < np ? *reinterpret_cast<const float4*>(p.part_o + slot(at) * dv + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const float m2 = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+        const float mb = m2 == -CUDART_INF_F ? 0.f : m2, f0 = ex2(m - mb);
+        m = m2;
+        l *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float f = ex2(ml[k].x - mb);
+          l = fmaf(ml[k].y, f, l);
+          o.x = fmaf(v[k].x, f, o.x), o.y = fmaf(v[k].y, f, o.y), o.z = fmaf(v[k].z, f, o.z), o.w = fmaf(v[k].w, f, o.w);
+        }
       }
     }
     __syncthreads();
     sum_sh[threadIdx.x] = o;
-    if ((threadIdx.x & 15) == 0) l_sh[part][rr] = l;
+    if ((threadIdx.x & 15) == 0) ml_sh[part][rr] = make_float2(m, l);
     __syncthreads();
     if (part == 0 && in) {
-      l = (l_sh[0][rr] + l_sh[1][rr]) + (l_sh[2][rr] + l_sh[3][rr]);
+      float mm = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 1; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) mm = fmaxf(mm, ml_sh[i][rr].x);
+      const float mb = mm == -CUDART_INF_F ? 0.f : mm;
+      l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = ex2(ml_sh[i][rr].x - mb);
         const float4 v = sum_sh[threadIdx.x + 128 * i];
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        l = fmaf(ml_sh[i][rr].y, f, l);
+        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
       }
-      const int tok = tile * tokens + lr / group, col = rec.tile % cols;
-      const long long row = (long long)(s.cu + tok) * a.n_q + rec.head * group + lr % group;
+      const long long row = (long long)(rec.token + lr / rec.group) * n_q + rec.head0 + lr % rec.group;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + col * dv + d) =
+      *reinterpret_cast<uint2*>(static_cast<T*>(out_) + row * D + rec.col * dv + d) =
           make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
-      if (d == 0 && col == 0 && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
+      if (d == 0 && rec.col == 0 && lse) lse[row] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
     }
   }
 }
 
 }  // namespace attn
 
-int launch_attn_join(const AttnParams& a, const AttnSplit& split, int group, int rows, int D, int dv, int align,
-                     bool bf16, int grid, cudaStream_t s) {
+int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int D, int dv, bool bf16, int grid,
+                     cudaStream_t s) {
+  if (grid > attn::kJoinThr) return fail(Q4_ERR_SHAPE, "attention: %d SMs are more than the join handles", grid);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, dv / 64, rows / 8 < 4 ? rows / 8 : 4);
+  cfg.gridDim = dim3(2 * grid);
   cfg.blockDim = dim3(attn::kJoinThr);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -80,8 +119,8 @@ int launch_attn_join(const AttnParams& a, const AttnSplit& split, int group, int
   cfg.attrs = at;
   cfg.numAttrs = 1;
   const cudaError_t e =
-      bf16 ? cudaLaunchKernelEx(&cfg, attn::join_kernel<__nv_bfloat16>, a, split, group, rows, D, dv, align)
-           : cudaLaunchKernelEx(&cfg, attn::join_kernel<__half>, a, split, group, rows, D, dv, align);
+      bf16 ? cudaLaunchKernelEx(&cfg, attn::join_kernel<__nv_bfloat16>, split, grid, a.n_q, rows, D, dv, a.out, a.lse)
+           : cudaLaunchKernelEx(&cfg, attn::join_kernel<__half>, split, grid, a.n_q, rows, D, dv, a.out, a.lse);
   return e == cudaSuccess ? Q4_OK : cuda_fail(e, "attention join launch");
 }
 

@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
       const bool whole = opens && closes;
       const long long slot = 2ll * blockIdx.x + (opens ? 1 : 0);
       if (opens && !closes && threadIdx.x == 0)   // goes on in the next CTAs
-        p.split.recs[blockIdx.x] = {cw.seq, cw.head, 0, (int)((first_step + step - cw.local + cw.n_local - 1) / share)};
+        p.split.recs[blockIdx.x] = {(int)((first_step + step - cw.local + cw.n_local - 1) / share), cw.s.cu, R,
+                                    cw.head * p.group, p.group, 0};
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         // every warp to the common maximum
@@ -509,7 +510,7 @@ static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, D, NT>, p);
   if (e != cudaSuccess) return cuda_fail(e, "decode attention launch");
-  return launch_attn_join(p.a, p.split, p.group, 8 * NT, D, D, kUnit, std::is_same<T, __nv_bfloat16>::value, p.grid, s);
+  return launch_attn_join(p.a, p.split, 8 * NT, D, D, std::is_same<T, __nv_bfloat16>::value, p.grid, s);
 }
 
 // The largest NT: registers hold NT (D/8 + D/4) values of Q and O.

@@ -642,8 +642,8 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
         if (!whole) p.split.part_ml[slot * kRows + row] = make_float2(m, l);
         else if (in && w.part == 0 && a.lse) a.lse[orow] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
         if (opens && !closes && row == 0)
-          p.split.recs[blockIdx.x] = {w.seq, w.head, w.t * PARTS + w.part,
-                                      (int)((first_step + j - w.local + w.x.steps - 1) / share)};
+          p.split.recs[blockIdx.x] = {(int)((first_step + j - w.local + w.x.steps - 1) / share), w.s.cu + w.t * p.tokens,
+                                      min(p.tokens, w.s.n - w.t * p.tokens) * p.group, w.head * p.group, p.group, w.part};
       }
       tc::fence_before();
       if (j + 1 < n_steps) {
@@ -683,7 +683,7 @@ static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, p);
   if (e != cudaSuccess) return cuda_fail(e, "tile attention launch");
-  return launch_attn_join(p.a, p.split, p.group, kRows, D, S::kDV, p.box, std::is_same<T, __nv_bfloat16>::value, p.grid, s);
+  return launch_attn_join(p.a, p.split, kRows, D, S::kDV, std::is_same<T, __nv_bfloat16>::value, p.grid, s);
 }
 
 template <typename T>

@@ -43,8 +43,10 @@ __device__ __forceinline__ float ex2(float x) {
 // in slot 2 c, and the part of one that it begins and does not end in slot
 // 2 c + 1, with a record of how far that item goes.
 struct SplitRec {
-  int seq, head, tile;   // tile: of `rows` query rows, times the column parts of D, plus the part
   int last;              // CTA that ends the item; -1: this CTA begins none that it does not end
+  int token, used;       // first token of the item's tile, its rows
+  int head0, group;      // first query head, heads per token: row r is token r / group, head r % group
+  int col;               // column part of D
 };
 struct AttnSplit {
   float* part_o;         // [2 grid][rows][dv]: sums of the values
@@ -69,7 +71,7 @@ inline AttnSplit attn_split(void* ws, int grid, int rows, int dv) {
 }
 
 // Joins what the recorded items left in their slots, in the order of the keys.
-int launch_attn_join(const AttnParams& a, const AttnSplit& split, int group, int rows, int D, int dv, int align,
-                     bool bf16, int grid, cudaStream_t s);
+int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int D, int dv, bool bf16, int grid,
+                     cudaStream_t s);
 
 }  // namespace q4w
