@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
     if (threadIdx.x == 0) first_sh[0] = 0;
     __syncthreads();
   }
-  const int part = threadIdx.x >> 7, rr = (threadIdx.x >> 4) & 7;
+  const int part = threadIdx.x >> 7, rr = threadIdx.x & 7, dl = (threadIdx.x >> 3) & 15;   // rows lie side by side in a part
   const int total = first_sh[kJoinThr];
   for (int task = blockIdx.x; task < total; task += gridDim.x) {
     int lo = 0, hi = n_recs;   // the record: the last one that begins at or before the task
@@ -50,10 +50,10 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
       if (first_sh[mid] <= task) lo = mid; else hi = mid;
     }
     const SplitRec rec = rec_sh[lo];
-    const int c0 = lo, sub = task - first_sh[lo], d = sub % (dv / 64) * 64 + 4 * (threadIdx.x & 15);
+    const int c0 = lo, sub = task - first_sh[lo], d = sub % (dv / 64) * 64 + 4 * dl;
     const int lr = sub / (dv / 64) * 8 + rr, np = rec.last - c0 + 1;
     const bool in = lr < rec.used;
-    auto slot = [&](int i) { return (i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i)) * rows + lr; };
+    auto slot = [&](int i) { return i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i); };
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f, m = -CUDART_INF_F;
     if (in) {
@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int at = i + 4 * k;
-          ml[k] = at < np ? p.part_ml[slot(at)] : make_float2(-CUDART_INF_F, 0.f);
-          v[k] = at < np ? *reinterpret_cast<const float4*>(p.part_o + slot(at) * dv + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+          ml[k] = at < np ? p.part_ml[slot(at) * rows + lr] : make_float2(-CUDART_INF_F, 0.f);
+          v[k] = at < np ? *reinterpret_cast<const float4*>(p.part_o + (slot(at) * dv + d) * rows + 4 * lr) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         const float m2 = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
         const float mb = m2 == -CUDART_INF_F ? 0.f : m2, f0 = ex2(m - mb);
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
     }
     __syncthreads();
     sum_sh[threadIdx.x] = o;
-    if ((threadIdx.x & 15) == 0) ml_sh[part][rr] = make_float2(m, l);
+    if (dl == 0) ml_sh[part][rr] = make_float2(m, l);
     __syncthreads();
     if (part == 0 && in) {
       float mm = -CUDART_INF_F;

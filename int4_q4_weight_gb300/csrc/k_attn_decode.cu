@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
         }
         __syncthreads();
         for (int i = threadIdx.x; i < 8 * (D / 4); i += S::kThr) {
-          const int rr = i / (D / 4), r = 8 * t + rr, d = 4 * (i % (D / 4));
+          const int rr = i & 7, r = 8 * t + rr, d = 4 * (i >> 3);
           if (r >= R) continue;
           float mm = -CUDART_INF_F, ll = 0.f;
 #pragma unroll
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
                 make_uint2(Half16<T>::pack(v.x * inv, v.y * inv), Half16<T>::pack(v.z * inv, v.w * inv));
             if (d == 0 && a.lse) a.lse[row] = ll == 0.f ? -CUDART_INF_F : (mm + log2f(ll)) * 0.6931471805599453f;
           } else {
-            *reinterpret_cast<float4*>(p.split.part_o + (slot * (8 * NT) + r) * D + d) = v;
+            *reinterpret_cast<float4*>(p.split.part_o + (slot * D + d) * (8 * NT) + 4 * r) = v;
             if (d == 0) p.split.part_ml[slot * (8 * NT) + r] = make_float2(mm, ll);
           }
         }

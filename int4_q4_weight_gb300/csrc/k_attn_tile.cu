@@ -16,14 +16,14 @@
 // scores twice (1.5 times the products).
 //
 // Warps: 0-7 softmax (warp w the rows 32 (w mod 4) .., keys 64 (w div 4) ..), 8
-// issues the MMAs, 9 the loads of K and V, 10 those of the next item's query rows
-// (a box of whole tokens: a tile has floor(128 / group) of them).
+// issues the MMAs, 9 and 10 the loads of K and of V, 11 those of the next item's
+// query rows (a box of whole tokens: a tile has floor(128 / group) of them).
 // The softmax is written to be short: a path that is taken once per item and
-// unrolled to hundreds of instructions cost 20000 cycles of instruction fetches.  K and V go through one ring
-// of 32 KB slots in the order in which the MMAs take them: K slots of [128
-// keys][128 dims], V slots of [64 or 128 keys][DV], loaded in boxes of 16 to 64
-// rows (the page size's share), 128-byte swizzle (16 KB slots: half as many
-// bytes per box, and a third slower).
+// unrolled to hundreds of instructions cost 20000 cycles of instruction fetches.
+// K and V have a ring of slots each, so that the next keys load while the values
+// wait for P: K slots of [128 keys][64 or 128 dims], V slots of [64 or 128
+// keys][DV], loaded in boxes of 16 to 64 rows (the page size's share), 128-byte
+// swizzle.
 //
 // Split: the steps of all items (sequence, KV head, tile) form one line that is
 // cut into equal shares, one CTA per SM; causal tiles of any length and ragged
@@ -40,8 +40,8 @@ namespace tile {
 
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kMmaWarp + 1, kQWarp = kTmaWarp + 1, kQWarps = 1;
-constexpr int kThr = (kQWarp + kQWarps) * 32;
+constexpr int kMmaWarp = kSoftWarps, kKWarp = kMmaWarp + 1, kVWarp = kKWarp + 1, kQWarp = kVWarp + 1;
+constexpr int kThr = (kQWarp + 1) * 32;
 constexpr long long kDrainCycles = 2000000000LL;
 constexpr int kBadRing = 16;
 
@@ -49,14 +49,19 @@ template <int D>
 struct Shape {
   static constexpr int kDV = D < 256 ? D : 256;              // columns of O of an item
   static constexpr int kParts = D / kDV;                     // items per tile
-  static constexpr int kKD = D < 128 ? D : 128;              // dims of a K slot
+  static constexpr int kKD = D == 128 || D == 256 ? 128 : 64;   // dims of a K slot
   static constexpr int kNK = D / kKD;                        // K slots per step
-  static constexpr int kSlot = kKeys * kKD * 2;              // bytes: 32 KB, 16 KB for D = 64
-  static constexpr int kVK = kSlot / (kDV * 2);              // keys of a V slot: 64, 128
+  static constexpr int kKSlot = kKeys * kKD * 2;             // bytes: 32 KB, 16 KB for D = 64 and 512
+  static constexpr int kVSlot = D == 64 ? 16384 : 32768;
+  static constexpr int kVK = kVSlot / (kDV * 2);             // keys of a V slot: 128, 128, 64, 64
   static constexpr int kNV = kKeys / kVK;                    // V slots per step
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kSlots = (229376 - kQBytes) / kSlot < 12 ? (229376 - kQBytes) / kSlot : 12;   // 3, 5, 6, 12
-  static constexpr size_t kSmem = kQBytes + (size_t)kSlots * kSlot;   // with the static part, all 227 KB
+  static constexpr int kKSlots = D == 64 ? 6 : D == 128 ? 3 : 2;   // rings of K and of V
+  static constexpr int kVSlots = D == 64 ? 6 : D <= 256 ? 3 : 2;   // all of a step's: its rows are cleared together
+  static_assert(kVSlots >= kNV, "the softmax waits for a whole step of V");
+  static constexpr int kRing = kKSlots * kKSlot + kVSlots * kVSlot;
+  static_assert(kVK >= 64, "a slot of V holds the largest box");
+  static constexpr size_t kSmem = kQBytes + kRing;   // with the static part, all 227 KB
 };
 
 struct Params {
@@ -147,7 +152,7 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t lbo) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ Params p) {
   using S = Shape<D>;
-  constexpr int NS = S::kSlots, PARTS = S::kParts;
+  constexpr int NKS = S::kKSlots, NVS = S::kVSlots, NS = NKS + NVS, PARTS = S::kParts;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -269,23 +274,27 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
   tc::fence_after();
   const uint32_t tmem = tmem_sh;
   const uint32_t q_addr = tc::smem_u32(smem), ring0 = tc::smem_u32(ring);
+  const uint32_t v_ring0 = ring0 + NKS * S::kKSlot;
   const uint32_t o_tmem = tmem + 256;
 
-  // Whether step j + 1 of the share belongs to the same item as step j: then its
-  // scores are formed before the values of step j, else after them.
-  if (warp == kTmaWarp) {
+  // slots: those of K, then those of V
+  if (warp == kKWarp || warp == kVWarp) {
     // ---------------------------------------------------------- TMA loads
+    const bool is_k = warp == kKWarp;
     const uint64_t policy = tc::policy_evict_last();
     const int nb = kKeys / p.box;
-    uint32_t q = 0;   // slots filled
+    const int slots = is_k ? NKS : NVS, slot0 = is_k ? 0 : NKS, bytes = is_k ? S::kKSlot : S::kVSlot;
+    const uint32_t base = is_k ? ring0 : v_ring0;
+    int slot = 0;
+    uint32_t round = 0;
     bool ok = true;
     // A step's boxes, lane b the box b: the block-table entry is fetched a step
     // before it is needed (the load takes longer than a slot's products).
     struct Boxes {
-      int entry, off, head;   // entry -2: nothing to load
+      int entry, off, head, part;   // entry -2: nothing to load
     };
     auto fetch = [&](const Walk& y) {
-      Boxes x = {-2, 0, y.head};
+      Boxes x = {-2, 0, y.head, y.part};
       const int pos = y.x.base + y.local * kKeys + lane * p.box;
       if (lane < nb && pos < y.x.end && pos + p.box > y.x.lo) {
         const int at = pos / a.kv.page_size;
@@ -295,91 +304,60 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       }
       return x;
     };
-    // their rows of the cache; total_rows, out of the cache, gives zeros
-    auto rows_of = [&](const Boxes& x, int j) {
-      const bool bad = x.entry == -1 || x.entry >= a.kv.n_pages;
+    Boxes next = {};
+    if (n_steps > 0) next = fetch(w);
+    for (int j = 0; j < n_steps && ok; ++j) {
+      const Boxes cur = next;
+      if (j + 1 < n_steps) {
+        if (w.local + 1 < w.x.steps) ++w.local; else walk_next<PARTS>(w, p);
+        next = fetch(w);
+      }
+      // the boxes' rows of the cache; total_rows, out of the cache, gives zeros
+      const bool bad = cur.entry == -1 || cur.entry >= a.kv.n_pages;
+      const int row = bad || cur.entry < 0 ? p.total_rows : (int)kv_row(a.kv, cur.entry, cur.head) + cur.off;
       const uint32_t mask = __ballot_sync(0xffffffffu, bad);
-      if (lane == 0) {
+      if (is_k && lane == 0) {
         bad_sh[j % kBadRing] = mask;
         if (mask && a.err) *a.err = 1;
       }
       __syncwarp();
-      return bad || x.entry < 0 ? p.total_rows : (int)kv_row(a.kv, x.entry, x.head) + x.off;
-    };
-    auto acquire = [&]() {
-      const uint32_t slot = q % NS;
-      const bool f = tc::mbar_wait(empty0 + 8 * slot, ((q / NS) & 1) ^ 1, p.wait_limit, abort_flag, p.dev_err);
-      if (!__all_sync(0xffffffffu, f)) return ok = false;
-      if (lane == 0) tc::mbar_expect_tx(full0 + 8 * slot, S::kSlot);
-      __syncwarp();
-      return true;
-    };
-    auto load_k = [&](int row) {
-      for (int h = 0; h < S::kNK && ok; ++h) {
-        if (!acquire()) return;
-        const uint32_t slot = q % NS, dst = ring0 + slot * S::kSlot;
-        constexpr int slabs = S::kKD / 64;
-        const int b = lane % nb, sl = lane / nb, r = __shfl_sync(0xffffffffu, row, b);
-        if (sl < slabs)
-          tc::tma_load_3d(dst + sl * (kKeys * 128) + b * p.box * 128, &p.tm_k, 0, r, h * slabs + sl, full0 + 8 * slot, policy);
-        ++q;
-      }
-    };
-    auto load_v = [&](int row, int part) {
-      for (int h = 0; h < S::kNV && ok; ++h) {
-        if (!acquire()) return;
-        const uint32_t slot = q % NS, dst = ring0 + slot * S::kSlot;
-        constexpr int slabs = S::kDV / 64;
-        const int vb = S::kVK / p.box;   // boxes of the slot's keys
-        const int b = lane % vb, sl = lane / vb, r = __shfl_sync(0xffffffffu, row, h * vb + b);
-        if (sl < slabs)
-          tc::tma_load_3d(dst + sl * (S::kVK * 128) + b * p.box * 128, &p.tm_v, 0, r, part * slabs + sl, full0 + 8 * slot, policy);
-        ++q;
-      }
-    };
-    if (n_steps > 0) {
-      // w: the step whose boxes are fetched, two ahead of the values
-      bool same1 = false;             // whether step j + 1 belongs to step j's item
-      auto advance = [&]() {
-        same1 = w.local + 1 < w.x.steps;
-        if (same1) ++w.local; else walk_next<PARTS>(w, p);
-      };
-      Boxes nb1 = fetch(w);
-      int part = w.part;
-      int row = rows_of(nb1, 0);
-      load_k(row);
-      int part1 = 0;
-      if (1 < n_steps) {
-        advance();
-        nb1 = fetch(w);
-        part1 = w.part;
-      }
-      for (int j = 0; j < n_steps && ok; ++j) {
-        const bool same = same1;
-        const Boxes cur = nb1;
-        const int part_next = part1;
-        if (j + 2 < n_steps) {
-          advance();
-          nb1 = fetch(w);
-          part1 = w.part;
+      const int n_slots = is_k ? S::kNK : S::kNV;
+      for (int h = 0; h < n_slots; ++h) {
+        const uint32_t full = full0 + 8 * (slot0 + slot), dst = base + slot * bytes;
+        const bool f = tc::mbar_wait(empty0 + 8 * (slot0 + slot), (round & 1) ^ 1, p.wait_limit, abort_flag, p.dev_err);
+        if (!__all_sync(0xffffffffu, f)) {
+          ok = false;
+          break;
         }
-        int next_row = 0;
-        if (j + 1 < n_steps) next_row = rows_of(cur, j + 1);
-        if (same && j + 1 < n_steps) load_k(next_row);
-        load_v(row, part);
-        if (!same && j + 1 < n_steps) load_k(next_row);
-        row = next_row;
-        part = part_next;
+        if (lane == 0) tc::mbar_expect_tx(full, bytes);
+        __syncwarp();
+        if (is_k) {
+          constexpr int slabs = S::kKD / 64;
+          const int b = lane % nb, sl = lane / nb, r = __shfl_sync(0xffffffffu, row, b);
+          if (sl < slabs) tc::tma_load_3d(dst + sl * (kKeys * 128) + b * p.box * 128, &p.tm_k, 0, r, h * slabs + sl, full, policy);
+        } else {
+          constexpr int slabs = S::kDV / 64;
+          const int vb = S::kVK / p.box;   // boxes of the slot's keys
+          const int b = lane % vb, sl = lane / vb, r = __shfl_sync(0xffffffffu, row, h * vb + b);
+          if (sl < slabs)
+            tc::tma_load_3d(dst + sl * (S::kVK * 128) + b * p.box * 128, &p.tm_v, 0, r, cur.part * slabs + sl, full, policy);
+        }
+        if (++slot == slots) slot = 0, ++round;
       }
-      // what was issued lands before the CTA leaves
-      for (uint32_t i = q > (uint32_t)NS ? q - NS : 0u; i < q; ++i)
-        tc::mbar_drain(full0 + 8 * (i % NS), (i / NS) & 1, kDrainCycles, p.dev_err);
+    }
+    // what was issued lands before the CTA leaves: the slots of this round, and
+    // of the one before those not yet filled again
+    for (int i = 0; i < slots; ++i) {
+      const bool again = i < slot;
+      if (again || round > 0)
+        tc::mbar_drain(full0 + 8 * (slot0 + i), (again ? round : round - 1) & 1, kDrainCycles, p.dev_err);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------- MMA issuer
     constexpr uint32_t id_s = idesc(kKeys, BF16, false), id_o = idesc(S::kDV, BF16, true);
-    uint32_t q = 0;
+    int ks = 0, vs = 0;                // slots
+    uint32_t kround = 0, vround = 0;
     int item = 0;
     bool ok = n_steps > 0;
     auto wait_all = [&](uint32_t bar, uint32_t par) {
@@ -390,11 +368,11 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     auto scores = [&](int j, bool first, bool last) {
       if (first && !wait_all(qfull, item & 1)) return;
       for (int h = 0; h < S::kNK; ++h) {
-        const uint32_t slot = q % NS;
-        if (!wait_all(full0 + 8 * slot, (q / NS) & 1)) return;
+        const uint32_t slot = ks;
+        if (!wait_all(full0 + 8 * slot, kround & 1)) return;
         tc::fence_after();
         if (tc::elect_one()) {
-          const uint32_t kb = ring0 + slot * S::kSlot, qb = q_addr + h * (S::kKD / 64) * (kRows * 128);
+          const uint32_t kb = ring0 + slot * S::kKSlot, qb = q_addr + h * (S::kKD / 64) * (kRows * 128);
 #pragma unroll
           for (int k = 0; k < S::kKD / 16; ++k) {
             const uint32_t off = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
@@ -403,7 +381,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
           tc::commit(empty0 + 8 * slot);
         }
         __syncwarp();
-        ++q;
+        if (++ks == NKS) ks = 0, ++kround;
       }
       if (tc::elect_one()) {
         tc::commit(sfull0 + 8 * (j & 1));
@@ -415,18 +393,18 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     auto values = [&](int j, bool first) {
       if (!wait_all(pready0 + 8 * (j & 1), (j >> 1) & 1)) return;
       for (int h = 0; h < S::kNV; ++h) {
-        const uint32_t slot = q % NS;
-        if (!wait_all(full0 + 8 * slot, (q / NS) & 1)) return;
+        const uint32_t slot = NKS + vs;
+        if (!wait_all(full0 + 8 * slot, vround & 1)) return;
         tc::fence_after();
         if (tc::elect_one()) {
-          const uint32_t vb = ring0 + slot * S::kSlot, pa = tmem + (j & 1) * 128 + h * (S::kVK / 2);
+          const uint32_t vb = v_ring0 + vs * S::kVSlot, pa = tmem + (j & 1) * 128 + h * (S::kVK / 2);
 #pragma unroll
           for (int k = 0; k < S::kVK / 16; ++k)
             mma_ts(o_tmem, pa + 8 * k, desc_mn_sw128(vb + k * 2048, S::kVK * 128), id_o, (first && h == 0 && k == 0) ? 0u : 1u);
           tc::commit(empty0 + 8 * slot);
         }
         __syncwarp();
-        ++q;
+        if (++vs == NVS) vs = 0, ++vround;
       }
       if (tc::elect_one()) tc::commit(odone);
       __syncwarp();
@@ -581,11 +559,10 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       // values that no row of the tile sees may be anything, and 0 times
       // infinity is no zero: they are cleared in shared memory
       if (k0 < w.x.lo || k0 + kKeys > w.x.end) {
-        // slot number of the step's first V slot
-        const int vq = S::kNK * (j + 1 + (same ? 1 : 0)) + S::kNV * j;
-        for (int h = 0; h < S::kNV; ++h) wait(full0 + 8 * ((vq + h) % NS), ((vq + h) / NS) & 1);
+        const int vq = S::kNV * j;   // V slots before the step's
+        for (int h = 0; h < S::kNV; ++h) wait(full0 + 8 * (NKS + (vq + h) % NVS), ((vq + h) / NVS) & 1);
         for (int h = 0; h < S::kNV; ++h) {
-          const uint32_t vb = ring0 + ((vq + h) % NS) * S::kSlot;
+          const uint32_t vb = v_ring0 + (vq + h) % NVS * S::kVSlot;
           // a thread clears one 16-byte piece of a row of every slab
           for (int i = threadIdx.x; i < S::kVK * 8; i += kSoftWarps * 32) {
             const int c = k0 + h * S::kVK + (i >> 3);
@@ -621,7 +598,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       const long long slot = 2ll * blockIdx.x + (opens ? 1 : 0);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       T* out = static_cast<T*>(a.out) + orow * D + w.part * S::kDV + half * kHalfO;
-      float* po = p.split.part_o + (slot * kRows + row) * S::kDV + half * kHalfO;
+      float* po = p.split.part_o + (slot * S::kDV + half * kHalfO) * kRows + row * 4;
 #pragma unroll 1
       for (int c = 0; c < kHalfO; c += 32) {
         float t[32];
@@ -635,7 +612,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
                            Half16<T>::pack(t[i + 4] * inv, t[i + 5] * inv), Half16<T>::pack(t[i + 6] * inv, t[i + 7] * inv));
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(po + c + i) = make_float4(t[i], t[i + 1], t[i + 2], t[i + 3]);
+          for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(po + (c + i) * kRows) = make_float4(t[i], t[i + 1], t[i + 2], t[i + 3]);
         }
       }
       if (half == 0) {

@@ -49,7 +49,7 @@ struct SplitRec {
   int col;               // column part of D
 };
 struct AttnSplit {
-  float* part_o;         // [2 grid][rows][dv]: sums of the values
+  float* part_o;         // [2 grid][dv / 4][rows][4]: sums of the values
   float2* part_ml;       // [2 grid][rows]: maximum (in units of log2 e) and sum
   SplitRec* recs;        // [grid]
 };
