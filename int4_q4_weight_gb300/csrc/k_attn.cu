@@ -5,16 +5,24 @@
 namespace q4w {
 namespace attn {
 
-// Task: 64 elements of 8 rows of one recorded item; four groups of threads take
-// every fourth part.  Every block reads all the records, so the tasks of the
-// few items that were split spread over the device whatever CTA recorded them.
+// Task: 8 rows of one recorded item and 256 / P of their elements; P groups of
+// threads take every P-th part (P = 1, 4 or 16: two parts of a tile are read by
+// as many threads as there are elements; the 152 parts of the few rows of a
+// single long sequence by 16 groups side by side, as there are no other tasks:
+// 16 us with 4 groups, 8 with 16; tiles have tasks enough, 17 us against 23).  Every block reads all the
+// records, so the tasks of the few items that were split spread over the device
+// whatever CTA recorded them.
 constexpr int kJoinThr = 512;
+
+__device__ __forceinline__ int join_groups(int parts, int used, int dv) {
+  return max(parts <= 4 ? 1 : parts > 16 && used <= 16 ? 16 : 4, 256 / dv);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n_recs, int n_q, int rows, int D, int dv,
                                                         void* out_, float* lse) {
   __shared__ float4 sum_sh[kJoinThr];
-  __shared__ float2 ml_sh[4][8];
+  __shared__ float2 ml_sh[16][8];
   __shared__ int first_sh[kJoinThr + 1];   // tasks before a record's
   __shared__ SplitRec rec_sh[kJoinThr];
   __shared__ int warp_sh[kJoinThr / 32];
@@ -25,7 +33,7 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
     if (threadIdx.x < n_recs) {
       const SplitRec r = p.recs[threadIdx.x];
       rec_sh[threadIdx.x] = r;
-      n = r.last < 0 ? 0 : (r.used + 7) / 8 * (dv / 64);
+      n = r.last < 0 ? 0 : (r.used + 7) / 8 * (dv * join_groups(r.last - (int)threadIdx.x + 1, r.used, dv) / 256);
     }
     int incl = n;
 #pragma unroll
@@ -41,7 +49,7 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
     if (threadIdx.x == 0) first_sh[0] = 0;
     __syncthreads();
   }
-  const int part = threadIdx.x >> 7, rr = threadIdx.x & 7, dl = (threadIdx.x >> 3) & 15;   // rows lie side by side in a part
+  const int rr = threadIdx.x & 7;   // rows lie side by side in a part
   const int total = first_sh[kJoinThr];
   for (int task = blockIdx.x; task < total; task += gridDim.x) {
     int lo = 0, hi = n_recs;   // the record: the last one that begins at or before the task
@@ -50,19 +58,21 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
       if (first_sh[mid] <= task) lo = mid; else hi = mid;
     }
     const SplitRec rec = rec_sh[lo];
-    const int c0 = lo, sub = task - first_sh[lo], d = sub % (dv / 64) * 64 + 4 * dl;
-    const int lr = sub / (dv / 64) * 8 + rr, np = rec.last - c0 + 1;
+    const int c0 = lo, sub = task - first_sh[lo], np = rec.last - c0 + 1;
+    const int groups = join_groups(np, rec.used, dv), quads = 64 / groups, col_tasks = dv * groups / 256;
+    const int part = (threadIdx.x >> 3) / quads, dl = (threadIdx.x >> 3) % quads, d = (sub % col_tasks * quads + dl) * 4;
+    const int lr = sub / col_tasks * 8 + rr;
     const bool in = lr < rec.used;
     auto slot = [&](int i) { return i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i); };
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f, m = -CUDART_INF_F;
     if (in) {
-      for (int i = part; i < np; i += 16) {   // four parts at a time
+      for (int i = part; i < np; i += 4 * groups) {   // four parts at a time
         float2 ml[4];
         float4 v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int at = i + 4 * k;
+          const int at = i + groups * k;
           ml[k] = at < np ? p.part_ml[slot(at) * rows + lr] : make_float2(-CUDART_INF_F, 0.f);
           v[k] = at < np ? *reinterpret_cast<const float4*>(p.part_o + (slot(at) * dv + d) * rows + 4 * lr) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -84,14 +94,12 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
     __syncthreads();
     if (part == 0 && in) {
       float mm = -CUDART_INF_F;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mm = fmaxf(mm, ml_sh[i][rr].x);
+      for (int i = 0; i < groups; ++i) mm = fmaxf(mm, ml_sh[i][rr].x);
       const float mb = mm == -CUDART_INF_F ? 0.f : mm;
       l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < groups; ++i) {
         const float f = ex2(ml_sh[i][rr].x - mb);
-        const float4 v = sum_sh[threadIdx.x + 128 * i];
+        const float4 v = sum_sh[threadIdx.x + 8 * quads * i];
         l = fmaf(ml_sh[i][rr].y, f, l);
         o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
       }
@@ -110,7 +118,7 @@ int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int 
                      cudaStream_t s) {
   if (grid > attn::kJoinThr) return fail(Q4_ERR_SHAPE, "attention: %d SMs are more than the join handles", grid);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * grid);
+  cfg.gridDim = dim3(4 * grid);
   cfg.blockDim = dim3(attn::kJoinThr);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

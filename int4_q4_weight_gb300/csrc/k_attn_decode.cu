@@ -198,27 +198,30 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
   lw.enter(a);
   Walk<S::kStep> cw = lw;
 
-  // pages of the next 32 units of this warp in the walk's sequence, one per lane
+  // cache rows of the next 32 units of this warp in the walk's sequence, one per
+  // lane (-1: a page that is none of the cache, -2: behind the end)
   int l_step = 0, l_half = 0;        // next load: step of the share, 0 = K, 1 = V
-  int pg_base = -32, pg = -1;
-  int l_row = 0;                     // cache row of the unit, total_rows: out of the cache (zero fill)
+  int row_base = -32, rows = -2;
+  int l_row = 0;                     // the unit's row; total_rows, out of the cache, gives zeros
   uint32_t l_slot = 0;               // loads issued
+  uint32_t skip = 0;                 // per slot of K: nothing in it counts
   auto issue = [&]() {
     if (l_step >= n_steps || dead) return;
     const int slot = (int)(l_slot % SLOTS);
     if (l_half == 0) {
-      if (lw.local < pg_base || lw.local >= pg_base + 32) {
-        pg_base = lw.local;
-        const int pos = lw.s.base + ((pg_base + lane) * W + warp) * kUnit;
-        pg = -1;
+      if (lw.local < row_base || lw.local >= row_base + 32) {
+        row_base = lw.local;
+        const int pos = lw.s.base + ((row_base + lane) * W + warp) * kUnit;
+        rows = -2;
         if (pos < lw.s.end) {
-          pg = kv_page(a.kv, lw.seq, pos);
-          if (pg < 0 && a.err) *a.err = 1;
+          const int page = kv_page(a.kv, lw.seq, pos);
+          rows = page < 0 ? -1 : (int)kv_row(a.kv, page, lw.head) + pos % a.kv.page_size;
+          if (page < 0 && a.err) *a.err = 1;
         }
       }
-      const int pos = lw.s.base + (lw.local * W + warp) * kUnit;
-      const int page = __shfl_sync(0xffffffffu, pg, lw.local - pg_base);
-      l_row = page < 0 ? p.total_rows : (int)kv_row(a.kv, page, lw.head) + pos % a.kv.page_size;
+      const int row = __shfl_sync(0xffffffffu, rows, lw.local - row_base);
+      l_row = row < 0 ? p.total_rows : row;
+      skip = row < 0 ? skip | (1u << slot) : skip & ~(1u << slot);
     }
     if (lane == 0) {
       const uint32_t bar = bar0 + 8 * slot;
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
     if (l_half) {
       l_half = 0;
       ++l_step;
-      if (l_step < n_steps && lw.next(a)) pg_base = -32;
+      if (l_step < n_steps && lw.next(a)) row_base = -32;
     } else {
       l_half = 1;
     }
@@ -270,14 +273,14 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
   for (int step = 0; step < n_steps; ++step) {
     // ------------------------------------------------ one unit of 16 keys
     const int k0 = cw.s.base + (cw.local * W + warp) * kUnit;
-    const uint32_t ks = ring0 + (c_slot % SLOTS) * S::kSlotBytes, kb = bar0 + 8 * (c_slot % SLOTS);
+    const uint32_t k_slot = c_slot % SLOTS;
+    const uint32_t ks = ring0 + k_slot * S::kSlotBytes, kb = bar0 + 8 * k_slot;
     const uint32_t kpar = (c_slot / SLOTS) & 1;
     ++c_slot;
     const uint32_t vs = ring0 + (c_slot % SLOTS) * S::kSlotBytes, vb = bar0 + 8 * (c_slot % SLOTS);
     const uint32_t vpar = (c_slot / SLOTS) & 1;
     ++c_slot;
-    const bool any = k0 < cw.s.end;
-    const bool valid = any && kv_page(a.kv, cw.seq, k0) >= 0;
+    const bool valid = !((skip >> k_slot) & 1);
     if (!dead) dead = !__all_sync(0xffffffffu, tc::mbar_wait(kb, kpar, p.wait_limit, &abort_sh, p.dev_err));
     float s[NT][4];
     if (valid && !dead) {
