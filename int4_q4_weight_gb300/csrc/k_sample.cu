@@ -14,25 +14,28 @@
 //
 // Arithmetic.  A token that lies next to a border has to fall on the side
 // that the definition says, and a border is a sum of up to 2^20 weights, so
-// fp32 sums of expf would be too coarse: masses are integers.  t is formed as
-// an fp32 pair (the difference exactly, log2(e)/T in two pieces), cut into
-// eighths of an octave, n = floor(8 t), and the rest f in [0, 1/8] goes
-// through a degree-6 polynomial of 2^-f to a 28-bit mantissa; the weight is
+// fp32 sums of expf would be too coarse: masses are integers.  8 t is formed as
+// an fp32 pair (the difference exactly, 8 log2(e)/T in two pieces), cut into
+// n = floor(8 t), an eighth of an octave, and the rest f in [0, 1], which goes
+// through a degree-6 polynomial of 2^(-f/8) to a 28-bit mantissa; the weight is
 // mantissa * 2^(-(n mod 8)/8) * 2^-(n div 8) rounded to units of 2^-42.
 // Integer sums have no order, so atomics and cluster reductions give the same
 // bits on every run.  A weight is off by about 2^-29 of itself, unbiased.
+// Products of a mass with top_p or u are formed exactly in 128 bits (fp64 runs
+// at a sixtieth of the fp32 rate: one logarithm per row is all of it).
 //
 // Work.  A cluster of CTAs takes a row, each an index range of it:
-//   A  the maximum (and its lowest index, the answer of greedy rows);
+//   A  the maximum (greedy rows: then its lowest index);
 //   B  a histogram of n over the row (1024 bins: 128 octaves), which bounds
 //      the last bin that S can reach;
 //   C  few candidates (<= 1024) up to that bin: they are gathered into the
-//      leader CTA, sorted, cut and sampled there;
+//      leader CTA, ranked, cut and sampled there;
 //   D  many: the bin that holds a border is refined by histograms of the
 //      order-preserving integer key (1024 sub-bins a level) until the
 //      threshold is a single key; then masses of 128-index segments, a scan of
 //      them, and the one segment that holds the target.
-// The row is read from HBM once; the later passes find it in L2.
+// The row is read from HBM once; the later passes find it in L2, with 16-byte
+// loads, four in flight a thread.
 #include <math_constants.h>
 
 #include "q4w_device.cuh"
@@ -46,10 +49,11 @@ namespace sample {
 constexpr int kThr = 512;
 constexpr int kWarpsS = kThr / 32;
 constexpr int kBins = 1024;
+static_assert(kBins == 2 * kThr, "a thread has two bins of a merged histogram");
 constexpr int kCap = 1024;          // candidates that the leader takes
+constexpr int kCount = 256;         // up to here they are ranked by counting, else sorted
 constexpr int kSeg = 128;           // indices per segment of the final pass
 constexpr int kMaxSegs = 1024;      // segments of a CTA: 2^17 indices, so a 32-bit bin never overflows
-constexpr int kMaxCluster = 8;
 typedef unsigned long long u64;
 
 struct Params {
@@ -66,9 +70,9 @@ struct Params {
   int range;                   // indices per CTA of the cluster, a multiple of kSeg
 };
 
-// Order-preserving integer of a logit: larger logit, larger key.
+// Order-preserving integer of a logit: larger logit, larger key; 0 and -0 tie.
 __device__ __forceinline__ uint32_t key_of(float z) {
-  const uint32_t b = __float_as_uint(z);
+  const uint32_t b = __float_as_uint(z + 0.f);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float logit_of(uint32_t k) {
@@ -77,43 +81,50 @@ __device__ __forceinline__ float logit_of(uint32_t k) {
 
 // What turns a logit of this row into a weight.
 struct Scale {
-  float top;       // M
-  float ch, cl;    // log2(e) / T in two pieces
-  float mh, ml;    // log2(1 / min_p) in two pieces: kept while t <= it
+  float top;       // M, the largest finite number for an infinite maximum
+  float ch, cl;    // 8 log2(e) / T in two pieces
+  u64 minp;        // min_p in units of 2^-59, 0: off
 };
 
-// t = (M - z) log2(e) / T as p + e, |e| small against p.  Zero at z = M
-// whatever T is; +inf for z = -inf.
-__device__ __forceinline__ void octaves(const Scale& s, float z, float& p, float& e) {
-  const float d = s.top - z;
-  if (z == s.top) {
-    p = e = 0.f;
-    return;
-  }
-  p = d * s.ch;
-  if (!(p < 128.f)) {
-    e = 0.f;
-    return;
-  }
-  // the exact difference is d + dl
-  const float bb = d - s.top;
-  const float dl = (s.top - (d - bb)) - (z + bb);
-  e = fmaf(d, s.ch, -p) + fmaf(d, s.cl, dl * s.ch);
+__device__ __forceinline__ Scale make_scale(float top, float temp, float min_p) {
+  Scale s;
+  s.top = fminf(top, CUDART_MAX_NORMAL_F);
+  // 8 log2(e) = h + l; the quotient's remainder is exact
+  const float h = 11.541560173034668f, l = 1.540770427e-07f;
+  const float t = fmaxf(temp, 1e-36f);
+  s.ch = h / t;
+  const float r = fmaf(-s.ch, t, h) + l;
+  s.cl = r / t;
+  if (!(s.ch < 1e38f) || temp == CUDART_INF_F) s.cl = 0.f;
+  const float m = fminf(min_p, 1.f);
+  s.minp = min_p > 0.f ? max((u64)(m * 576460752303423488.f), 1ull) : 0ull;   // a power of two times m: exact
+  return s;
 }
 
-// Bin of a logit, kBins when its weight is below 2^-128 (it never counts).
-__device__ __forceinline__ int bin_of(float p) { return p < 128.f ? (int)(p * 8.f) : kBins; }
+// A logit as the passes see it: +inf becomes the largest finite number, a NaN
+// stays one and fails every comparison.
+__device__ __forceinline__ float capped(const Scale& s, float z) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(s.top));
+  return r;
+}
+// 8 t, rounded: it only cuts the weights into bins, the same way everywhere.
+// Not below kBins (or NaN): the weight is below 2^-128 and never counts.
+__device__ __forceinline__ float eighths(const Scale& s, float z) { return (s.top - z) * s.ch; }
 
 // 28-bit mantissa of the weight inside its bin: 2^-(t - n/8), in (0.9, 1] * 2^28.
-__device__ __forceinline__ uint32_t mantissa(float p, float e, int n) {
-  const float f = fmaf((float)n, -0.125f, p) + e;
-  // 2^-f - 1 on [0, 1/8]: the series of exp(-f ln 2), whose next term is below 2^-37
-  float g = 1.5403530393381608e-4f;
-  g = fmaf(g, f, -1.3333558146428443e-3f);
-  g = fmaf(g, f, 9.618129107628477e-3f);
-  g = fmaf(g, f, -5.550410866482158e-2f);
-  g = fmaf(g, f, 2.402265069591007e-1f);
-  g = fmaf(g, f, -6.931471805599453e-1f);
+__device__ __forceinline__ uint32_t mantissa(const Scale& s, float z, float q, int n) {
+  const float d = s.top - z, bb = d - s.top;
+  const float dl = (s.top - (d - bb)) - (z + bb);           // the exact difference is d + dl
+  const float e = fmaf(d, s.ch, -q) + fmaf(d, s.cl, dl * s.ch);
+  const float f = (q - (float)n) + e;
+  // 2^(-f/8) - 1 on [0, 1]: the series of exp(-f ln 2 / 8); the next term is below 2^-37
+  float g = 5.875980527e-10f;
+  g = fmaf(g, f, -4.069079024e-08f);
+  g = fmaf(g, f, 2.348176052e-06f);
+  g = fmaf(g, f, -1.084064622e-04f);
+  g = fmaf(g, f, 3.753539171e-03f);
+  g = fmaf(g, f, -8.664339757e-02f);
   g = g * f;
   return (uint32_t)((1 << 28) + __float2int_rn(g * 268435456.f));
 }
@@ -129,32 +140,71 @@ __device__ __forceinline__ u64 weight_of(uint32_t mant, int n) {
   return sh > 60 ? 0ull : (w + (1ull << (sh - 1))) >> sh;
 }
 __device__ __forceinline__ u64 weight(const Scale& s, float z) {
-  float p, e;
-  octaves(s, z, p, e);
-  const int n = bin_of(p);
-  return n < kBins ? weight_of(mantissa(p, e, n), n) : 0ull;
+  const float q = eighths(s, z);
+  if (!(q < (float)kBins)) return 0ull;
+  const int n = (int)q;
+  return weight_of(mantissa(s, z, q, n), n);
 }
 __device__ __forceinline__ bool passes_minp(const Scale& s, float z) {
-  float p, e;
-  octaves(s, z, p, e);
-  return z == s.top || (p - s.mh) + (e - s.ml) <= 0.f;
+  const float q = eighths(s, z);
+  if (!(q < (float)kBins)) return false;
+  const int n = (int)q;
+  return ((u64)mantissa(s, z, q, n) * kEighth[n & 7]) >> (n >> 3) >= s.minp;
+}
+
+// floor (or ceiling) of m * f for 0 <= f < 1, exactly.
+__device__ __forceinline__ u64 times(u64 m, float f, bool up) {
+  const uint32_t b = __float_as_uint(f);
+  const int ex = (int)(b >> 23);
+  const u64 mant = ex ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
+  const int sh = 150 - max(ex, 1);                 // f = mant * 2^-sh, sh >= 24
+  const u64 lo = m * mant, hi = __umul64hi(m, mant);
+  u64 q, rest;
+  if (sh < 64) q = (lo >> sh) | (hi << (64 - sh)), rest = lo << (64 - sh);
+  else if (sh == 64) q = hi, rest = lo;
+  else if (sh < 128) q = hi >> (sh - 64), rest = lo | (hi << (128 - sh));
+  else q = 0, rest = lo | hi;
+  return q + (up && rest ? 1 : 0);
 }
 
 template <typename T>
-__device__ __forceinline__ float load_logit(const T* p) {
-  float z;
-  if constexpr (sizeof(T) == 4) z = *p;
-  else if constexpr (std::is_same<T, __half>::value) z = __half2float(*p);
-  else z = __bfloat162float(*p);
-  return z != z ? -CUDART_INF_F : z + 0.f;   // a NaN is never chosen; -0 and 0 tie
+__device__ __forceinline__ float as_float(T v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else if constexpr (std::is_same<T, __half>::value) return __half2float(v);
+  else return __bfloat162float(v);
 }
 
-// Calls f(z, index) for every index of [i0, i1) of the row, a warp taking
-// consecutive indices.
+// Calls f(logit, index) for every index of [i0, i1) of the row, in no order; i0
+// is a multiple of kSeg, vec: the row begins on a 16-byte boundary.
 template <typename T, typename F>
-__device__ __forceinline__ void for_range(const T* row, int i0, int i1, F f) {
+__device__ __forceinline__ void sweep(const T* row, int i0, int i1, bool vec, F f) {
+  constexpr int E = 16 / sizeof(T), U = sizeof(T) == 4 ? 4 : 2;
+  if (vec) {
+    const int full = i0 + (i1 - i0) / E * E, step = E * kThr;
+    int i = i0 + E * (int)threadIdx.x;
+    for (; i + (U - 1) * step < full; i += U * step) {
+      uint4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const uint4*>(row + i + u * step);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const T* e = reinterpret_cast<const T*>(&v[u]);
+#pragma unroll
+        for (int k = 0; k < E; ++k) f(as_float(e[k]), i + u * step + k);
+      }
+    }
+    for (; i < full; i += step) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + i);
+      const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int k = 0; k < E; ++k) f(as_float(e[k]), i + k);
+    }
+    i = full + (int)threadIdx.x;
+    if (i < i1) f(as_float(row[i]), i);
+  } else {
 #pragma unroll 4
-  for (int i = i0 + (int)threadIdx.x; i < i1; i += kThr) f(load_logit(row + i), i);
+    for (int i = i0 + (int)threadIdx.x; i < i1; i += kThr) f(as_float(row[i]), i);
+  }
 }
 
 __device__ __forceinline__ u64 ld_cluster_u64(uint32_t a) {
@@ -180,14 +230,14 @@ struct Shared {
   };
   uint32_t tie[kMaxSegs];                      // elements equal to the threshold, per segment
   u64 total;                                   // this CTA's mass (phase B), then of S
-  u64 best;                                    // this CTA's maximum: key, inverted index
+  float top;                                   // this CTA's maximum
+  int first;                                   // its first index that holds the row's
   u64 mine;                                    // this CTA's mass of S
   uint32_t ties;                               // this CTA's elements equal to the threshold
   uint32_t n_list;
   u64 red[kWarpsS];
   uint32_t red32[kWarpsS];
   u64 scan_total;
-  Scale scale;
   u64 goal;
   // the crossing bin of a scan
   int cross_bin;
@@ -242,6 +292,7 @@ __device__ __forceinline__ void bitonic(u64* v, int n) {
 // Adds every CTA's histogram, in every CTA: bins 2 threadIdx.x and + 1.
 __device__ __forceinline__ void merge_bins(Shared& sh, uint32_t ctas, bool masses, u64 (&cnt)[2], u64 (&mant)[2]) {
   cnt[0] = cnt[1] = mant[0] = mant[1] = 0;
+#pragma unroll 4
   for (uint32_t r = 0; r < ctas; ++r) {
     const u64 c = ld_cluster_u64(tc::cluster_addr(&sh.cnt[2 * threadIdx.x], r));
     cnt[0] += (uint32_t)c, cnt[1] += c >> 32;
@@ -275,17 +326,18 @@ __device__ __forceinline__ u64 bin_mass(u64 m, int n) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__ Params p) {
   __shared__ Shared sh;
   uint32_t rank, ctas;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   const int row = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) sh.n_list = 0;
+  if (threadIdx.x == 0) sh.n_list = 0, sh.first = 0x7fffffff;
   clear_bins(sh);
   pdl_wait();
   const T* z = static_cast<const T*>(p.z) + row * p.stride;
+  const bool vec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
   const int i0 = min((int)rank * p.range, p.V), i1 = min(i0 + p.range, p.V);
 
   const float temp = p.temperature ? p.temperature[row] : 1.f;
@@ -297,98 +349,88 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
   const bool has_p = top_p < 1.f;
   const bool has_m = min_p > 0.f;
 
-  // ---- A: the maximum and its lowest index
-  u64 best = 0;
+  // ---- A: the maximum (fmaxf passes over a NaN)
+  float top = -CUDART_INF_F;
   {
-    for_range(z, i0, i1, [&](float v, int i) {
-      const u64 c = ((u64)key_of(v) << 32) | (uint32_t)~i;
-      best = c > best ? c : best;
-    });
+    sweep(z, i0, i1, vec, [&](float v, int) { top = fmaxf(top, v); });
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const u64 t = __shfl_xor_sync(0xffffffffu, best, o);
-      best = t > best ? t : best;
-    }
-    if (lane == 0) sh.red[warp] = best;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sh.red32[warp] = __float_as_uint(top);
     __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 0; w < kWarpsS; ++w) best = sh.red[w] > best ? sh.red[w] : best;
-      sh.best = best;
+    if (warp == 0) {
+      top = lane < kWarpsS ? __uint_as_float(sh.red32[lane]) : -CUDART_INF_F;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) sh.top = top;
     }
     cluster_sync();
-    best = 0;
-    for (uint32_t r = 0; r < ctas; ++r) {
-      const u64 t = ld_cluster_u64(tc::cluster_addr(&sh.best, r));
-      best = t > best ? t : best;
-    }
+    top = -CUDART_INF_F;
+    for (uint32_t r = 0; r < ctas; ++r) top = fmaxf(top, __uint_as_float(ld_cluster_u32(tc::cluster_addr(&sh.top, r))));
   }
-  Scale s;
-  s.top = logit_of((uint32_t)(best >> 32));
-  const bool nothing = s.top == -CUDART_INF_F;
+  const bool nothing = top == -CUDART_INF_F;
   const bool greedy = !(temp > 0.f) || k_in == 1 || top_p <= 0.f;
   if (nothing || greedy) {   // the same in every CTA of the cluster
+    if (!nothing) {
+      int first = 0x7fffffff;
+      sweep(z, i0, i1, vec, [&](float v, int i) { first = v == top ? min(first, i) : first; });
+      first = __reduce_min_sync(0xffffffffu, first);
+      if (lane == 0 && first != 0x7fffffff) atomicMin(&sh.first, first);
+    }
+    cluster_sync();
     if (rank == 0 && threadIdx.x == 0) {
-      p.token[row] = nothing ? -1 : (int)~(uint32_t)best;
+      int first = 0x7fffffff;
+      for (uint32_t r = 0; r < ctas; ++r) first = min(first, (int)ld_cluster_u32(tc::cluster_addr(&sh.first, r)));
+      p.token[row] = nothing ? -1 : first;
       if (p.logprob) p.logprob[row] = nothing ? -CUDART_INF_F : 0.f;
     }
     cluster_sync();   // no CTA leaves while another reads its shared memory
     return;
   }
-  // fp64 runs at a small fraction of the fp32 rate: one thread's work
-  if (threadIdx.x == 0) {
-    const double c = fmin(1.4426950408889634 / (double)temp, 1e30);
-    s.ch = (float)c;
-    s.cl = (float)(c - (double)s.ch);
-    const double l = has_m ? fmax(-log2((double)min_p), 0.0) : 0.0;
-    s.mh = (float)l;
-    s.ml = (float)(l - (double)s.mh);
-    sh.scale = s;
-  }
-  __syncthreads();
-  s = sh.scale;
+  const Scale s = make_scale(top, temp, min_p);
 
-  // ---- B: histogram over the row; its mass when the row has no top-k
-  const bool need_total = has_p && !has_k;
-  {
-    u64 sum = 0;
-    for_range(z, i0, i1, [&](float v, int) {
-      float pp, e;
-      octaves(s, v, pp, e);
-      const int n = bin_of(pp);
-      if (n < kBins) {
-        atomicAdd(&sh.cnt[n], 1u);
-        if (need_total) sum += weight_of(mantissa(pp, e, n), n);
-      }
-    });
-    u64 tot;
-    block_incl(sum, sh.red, &tot);
-    if (threadIdx.x == 0) sh.total = tot;
-  }
-  cluster_sync();
-  u64 total = 0;
-  for (uint32_t r = 0; r < ctas; ++r) total += ld_cluster_u64(tc::cluster_addr(&sh.total, r));
-  int last;            // last bin that S can reach
-  uint32_t n_cand;     // elements up to it
-  {
+  int last = kBins - 1;          // last bin that S can reach
+  uint32_t n_cand = 0xffffffffu;   // elements up to it
+  u64 total = 0;                 // mass of the row (top-p without top-k)
+  if (has_k || has_p || has_m) {
+    // ---- B: histogram over the row; its mass when the row has no top-k
+    if (has_p && !has_k) {
+      u64 sum = 0;
+      sweep(z, i0, i1, vec, [&](float v, int) {
+        v = capped(s, v);
+        const float q = eighths(s, v);
+        if (q < (float)kBins) {
+          const int n = (int)q;
+          atomicAdd(&sh.cnt[n], 1u);
+          sum += weight_of(mantissa(s, v, q, n), n);
+        }
+      });
+      u64 tot;
+      block_incl(sum, sh.red, &tot);
+      if (threadIdx.x == 0) sh.total = tot;
+      cluster_sync();
+      for (uint32_t r = 0; r < ctas; ++r) total += ld_cluster_u64(tc::cluster_addr(&sh.total, r));
+    } else {
+      sweep(z, i0, i1, vec, [&](float v, int) {
+        const float q = eighths(s, capped(s, v));
+        if (q < (float)kBins) atomicAdd(&sh.cnt[(int)q], 1u);
+      });
+      cluster_sync();
+    }
     u64 cnt[2], mant[2];
     merge_bins(sh, ctas, false, cnt, mant);
     u64 all;
     const u64 incl = block_incl(cnt[0] + cnt[1], sh.red, &all);
     const u64 c0 = incl - cnt[1], c1 = incl;   // elements up to bin 2 tid and 2 tid + 1
-    // bounds on the mass of the bins: 2^-((n + 1)/8) .. 2^-(n/8) per element
+    // a lower bound on the mass up to a bin: 2^-((n + 1)/8) per element
     const int b0 = 2 * threadIdx.x;
     const float h0 = exp2f(-0.125f * b0), q = 0.91700404f;   // 2^(-1/8)
-    float mass = 0.f, mtot;
-    {
-      const float lower = ((float)cnt[0] + (float)cnt[1] * q) * h0 * q * 0.9999f;
-      const float li = block_incl(lower, reinterpret_cast<float*>(sh.red32), &mtot);
-      mass = li;
-    }
+    float mtot;
+    const float mass = block_incl(((float)cnt[0] + (float)cnt[1] * q) * h0 * q * 0.9999f, reinterpret_cast<float*>(sh.red32), &mtot);
     const float m0 = mass - (float)cnt[1] * q * q * h0;   // up to bin b0 (a little less)
     // The first bin where one of the sets must have ended.  With both top-k and
     // top-p the mass of all of S_k is wanted, so only top-k ends it.
     const float target = has_p ? top_p * ((float)total * 2.2737368e-13f) * 1.0002f : CUDART_INF_F;
-    const float mbin = has_m ? s.mh * 8.f + 1.f : 2000.f;
+    const float mbin = has_m ? -8.f * log2f(fminf(min_p, 1.f)) + 1.f : 2000.f;
     const bool k_only = has_k && has_p;
     const bool e0 = (has_k && c0 >= (u64)k_in) || c0 == all || (!k_only && (m0 >= target || (float)b0 >= mbin));
     const bool e1 = (has_k && c1 >= (u64)k_in) || c1 == all || (!k_only && (mass >= target || (float)(b0 + 1) >= mbin));
@@ -397,7 +439,6 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
     __syncthreads();
     if (lane == 0) sh.red32[warp] = (uint32_t)mine;
     __syncthreads();
-    last = kBins - 1;
     for (int w = 0; w < kWarpsS; ++w) last = min(last, (int)sh.red32[w]);
     if (b0 == (last & ~1)) sh.scan_total = (last & 1) ? c1 : c0;
     __syncthreads();
@@ -407,10 +448,10 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
   if (n_cand <= (uint32_t)kCap) {
     // ---- C: the candidates into the leader
     const uint32_t list0 = tc::cluster_addr(sh.list, 0), count0 = tc::cluster_addr(&sh.n_list, 0);
-    for_range(z, i0, i1, [&](float v, int i) {
-      float pp, e;
-      octaves(s, v, pp, e);
-      if (bin_of(pp) <= last) {
+    const float lim = (float)(last + 1);
+    sweep(z, i0, i1, vec, [&](float v, int i) {
+      v = capped(s, v);
+      if (eighths(s, v) < lim) {
         uint32_t at;
         asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(count0) : "memory");
         const u64 c = ((u64)~key_of(v) << 32) | (uint32_t)i;
@@ -420,10 +461,21 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
     cluster_sync();
     if (rank != 0) return;   // only the leader's own memory is used from here
     const int n = (int)min(n_cand, (uint32_t)kCap);
-    int n2 = 32;
-    while (n2 < n) n2 <<= 1;
-    for (int i = n + threadIdx.x; i < n2; i += kThr) sh.list[i] = ~0ull;
-    bitonic(sh.list, n2);
+    if (n <= kCount) {
+      // each element's place: how many come before it (two threads count)
+      const u64 c = (int)(threadIdx.x >> 1) < n ? sh.list[threadIdx.x >> 1] : ~0ull;
+      int place = 0;
+      for (int j = threadIdx.x & 1; j < n; j += 2) place += sh.list[j] < c;
+      place += __shfl_xor_sync(0xffffffffu, place, 1);
+      __syncthreads();
+      if ((threadIdx.x & 1) == 0 && (int)(threadIdx.x >> 1) < n) sh.list[place] = c;
+      __syncthreads();
+    } else {
+      int n2 = 2 * kCount;
+      while (n2 < n) n2 <<= 1;
+      for (int i = n + threadIdx.x; i < n2; i += kThr) sh.list[i] = ~0ull;
+      bitonic(sh.list, n2);
+    }
     // cut: thread i holds elements 2 i and 2 i + 1
     constexpr int kPer = kCap / kThr;
     u64 w[kPer], mass_k = 0, sum = 0;
@@ -435,11 +487,9 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
       sum += w[j];
     }
     const u64 incl = block_incl(sum, sh.red, &mass_k);
-    if (threadIdx.x == 0)   // kept while the mass before it is below this
-      sh.goal = has_p ? (u64)ceil((double)top_p * (double)(has_k ? mass_k : total)) : ~0ull;
-    __syncthreads();
-    const u64 limit = sh.goal;
-    u64 before = incl - sum;
+    // kept while the mass before it is below this
+    const u64 limit = has_p ? times(has_k ? mass_k : total, top_p, true) : ~0ull;
+    u64 before = incl - sum, kept = 0;
     int keep = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -447,41 +497,56 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
       const bool k = i < nk && (i == 0 || (before < limit && (!has_m || passes_minp(s, logit_of(~(uint32_t)(sh.list[i] >> 32))))));
       before += w[j];
       keep += k;
+      kept += k ? w[j] : 0ull;
     }
+    u64 mass;
+    block_incl(kept, sh.red, &mass);
     keep = (int)__reduce_add_sync(0xffffffffu, (unsigned)keep);
     __syncthreads();
     if (lane == 0) sh.red32[warp] = (uint32_t)keep;
+    // the weights, beside the elements
+    u64* wt = reinterpret_cast<u64*>(sh.cnt);
+    static_assert(sizeof(sh.cnt) + sizeof(sh.lo) >= kCap * 8, "the weights take the place of the bins");
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) wt[kPer * threadIdx.x + j] = w[j];
     __syncthreads();
     keep = 0;
     for (int x = 0; x < kWarpsS; ++x) keep += (int)sh.red32[x];
-    // back in vocabulary order: index in the upper half
-    n2 = 32;
-    while (n2 < keep) n2 <<= 1;
-    for (int i = threadIdx.x; i < n2; i += kThr) {
-      const u64 c = sh.list[i];
-      sh.list[i] = i < keep ? (c << 32) | (c >> 32) : ~0ull;
-    }
-    bitonic(sh.list, n2);
-    sum = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = kPer * threadIdx.x + j;
-      w[j] = i < keep ? weight(s, logit_of(~(uint32_t)sh.list[i])) : 0ull;
-      sum += w[j];
-    }
-    u64 mass;
-    u64 run = block_incl(sum, sh.red, &mass) - sum;
-    if (threadIdx.x == 0) sh.goal = min((u64)floor((double)u * (double)mass), mass - 1);
-    __syncthreads();
-    const u64 goal = sh.goal;   // the token's running mass is the first above it
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = kPer * threadIdx.x + j;
-      if (i < keep && run <= goal && run + w[j] > goal) {
-        p.token[row] = (int)(sh.list[i] >> 32);
-        if (p.logprob) p.logprob[row] = (float)log((double)w[j] / (double)mass);
+    // the first running mass, in vocabulary order, above the goal
+    const u64 goal = min(times(mass, u, false), mass - 1);
+    auto pick = [&](int index, u64 wi) {
+      p.token[row] = index;
+      if (p.logprob) p.logprob[row] = (float)log((double)wi / (double)mass);
+    };
+    if (keep <= kCount) {
+      const int i = threadIdx.x >> 1;
+      const uint32_t at = i < keep ? (uint32_t)sh.list[i] : 0u;
+      u64 run = 0;
+      for (int j = threadIdx.x & 1; j < keep; j += 2) run += (uint32_t)sh.list[j] < at ? wt[j] : 0ull;
+      run += __shfl_xor_sync(0xffffffffu, run, 1);
+      if ((threadIdx.x & 1) == 0 && i < keep && run <= goal && run + wt[i] > goal) pick((int)at, wt[i]);
+    } else {
+      int n2 = 2 * kCount;
+      while (n2 < keep) n2 <<= 1;
+      for (int i = threadIdx.x; i < n2; i += kThr) {
+        const u64 c = sh.list[i];
+        sh.list[i] = i < keep ? (c << 32) | (c >> 32) : ~0ull;
       }
-      run += w[j];
+      bitonic(sh.list, n2);
+      sum = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = kPer * threadIdx.x + j;
+        w[j] = i < keep ? weight(s, logit_of(~(uint32_t)sh.list[i])) : 0ull;
+        sum += w[j];
+      }
+      u64 run = block_incl(sum, sh.red, &mass) - sum;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = kPer * threadIdx.x + j;
+        if (i < keep && run <= goal && run + w[j] > goal) pick((int)(sh.list[i] >> 32), w[j]);
+        run += w[j];
+      }
     }
     return;
   }
@@ -491,15 +556,18 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
   uint32_t thr_key = 0;
   u64 thr_ties = ~0ull;
   if (has_k || has_p) {
-    // histogram with masses
+    // histogram with masses, up to the last bin that matters
     cluster_sync();   // every CTA has read the counts
     clear_bins(sh);
     __syncthreads();
-    for_range(z, i0, i1, [&](float v, int) {
-      float pp, e;
-      octaves(s, v, pp, e);
-      const int n = bin_of(pp);
-      if (n < kBins) add_to_bin(sh, n, mantissa(pp, e, n));
+    const float lim = (float)(last + 1);
+    sweep(z, i0, i1, vec, [&](float v, int) {
+      v = capped(s, v);
+      const float q = eighths(s, v);
+      if (q < lim) {
+        const int n = (int)q;
+        add_to_bin(sh, n, mantissa(s, v, q, n));
+      }
     });
     cluster_sync();
     u64 cnt[2], mant[2];
@@ -531,28 +599,28 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
         return;
       }
       u64 c_before = sh.cross_cnt, m_before = sh.cross_mass;
-      // the keys of the bin: from the smallest z with p*8 >= bin .. ; the range
-      // is found by bisection on the key, as bin_of is monotone in z
+      // the keys of the bin: eighths() is monotone in the logit, so they are a
+      // range; each warp finds its ends by a 32-way search
       uint32_t k_lo, k_hi;   // keys of the bin: [k_lo, k_hi]
       {
         const uint32_t top_key = key_of(s.top), inf_key = key_of(-CUDART_INF_F);
-        auto bin_at = [&](uint32_t k) {
-          float pp, e;
-          octaves(s, logit_of(k), pp, e);
-          return bin_of(pp);
+        // the smallest key in [inf_key, top_key] whose logit lies below `edge` eighths
+        auto first_key = [&](float edge) {
+          uint32_t a = inf_key, b = top_key;   // b qualifies
+          while (a < b) {
+            const uint32_t span = b - a, part = span / 32 + 1;
+            const uint32_t k = min(a + part * lane, b);
+            const float q = eighths(s, logit_of(k));
+            const uint32_t yes = __ballot_sync(0xffffffffu, q < edge || k == b);
+            const int f = yes ? __ffs(yes) - 1 : 32;   // the first that qualifies
+            const uint32_t below = __shfl_sync(0xffffffffu, k, f > 0 ? f - 1 : 0), at = __shfl_sync(0xffffffffu, k, f & 31);
+            if (yes) b = at;
+            if (f > 0) a = below + 1;
+          }
+          return b;
         };
-        uint32_t a = inf_key, b = top_key;   // smallest key with bin_at <= bin
-        while (a < b) {
-          const uint32_t mid = a + ((b - a) >> 1);
-          if (bin_at(mid) <= bin) b = mid; else a = mid + 1;
-        }
-        k_lo = a;
-        a = k_lo, b = top_key;               // largest key with bin_at >= bin
-        while (a < b) {
-          const uint32_t mid = b - ((b - a) >> 1);
-          if (bin_at(mid) >= bin) a = mid; else b = mid - 1;
-        }
-        k_hi = a;
+        k_lo = first_key((float)(bin + 1));
+        k_hi = bin == 0 ? top_key : first_key((float)bin) - 1;
       }
       for (;;) {
         const uint32_t width = k_hi - k_lo;   // keys - 1
@@ -561,13 +629,10 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
         cluster_sync();   // every CTA has read the last histogram
         clear_bins(sh);
         __syncthreads();
-        for_range(z, i0, i1, [&](float v, int) {
+        sweep(z, i0, i1, vec, [&](float v, int) {
+          v = capped(s, v);
           const uint32_t k = key_of(v);
-          if (k >= k_lo && k <= k_hi) {
-            float pp, e;
-            octaves(s, v, pp, e);
-            add_to_bin(sh, (int)((k_hi - k) >> shift), mantissa(pp, e, bin));
-          }
+          if (k - k_lo <= width) add_to_bin(sh, (int)((k_hi - k) >> shift), mantissa(s, v, eighths(s, v), bin));
         });
         cluster_sync();
         u64 c[2], m[2];
@@ -609,9 +674,8 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
         k_hi = hi;
         if (shift == 0) {
           thr_key = k_hi;
-          float pp, e;
-          octaves(s, logit_of(k_hi), pp, e);
-          const u64 w = weight_of(mantissa(pp, e, bin), bin);
+          const float v = logit_of(k_hi);
+          const u64 w = weight_of(mantissa(s, v, eighths(s, v), bin), bin);
           const u64 rest = goal > (by_mass ? m_before : c_before) ? goal - (by_mass ? m_before : c_before) : 1ull;
           thr_ties = by_mass ? (w ? (rest + w - 1) / w : ~0ull) : rest;
           *mass_out = m_before + w * (by_mass ? 0ull : thr_ties);
@@ -625,10 +689,7 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
       const uint32_t kk = thr_key;
       const u64 kt = thr_ties;
       u64 unused;
-      __syncthreads();
-      if (threadIdx.x == 0) sh.goal = max((u64)ceil((double)top_p * (double)(has_k ? mass_k : total)), 1ull);
-      __syncthreads();
-      descend(true, sh.goal, &unused);
+      descend(true, max(times(has_k ? mass_k : total, top_p, true), 1ull), &unused);
       if (has_k && (thr_key < kk || (thr_key == kk && thr_ties > kt))) thr_key = kk, thr_ties = kt;
     }
   }
@@ -638,22 +699,47 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
   const int n_seg = (i1 - i0 + kSeg - 1) / kSeg;
   auto kept = [&](float v) { return key_of(v) > thr_key && (!has_m || passes_minp(s, v)); };
   auto tied = [&](float v) { return key_of(v) == thr_key && thr_key != 0 && (!has_m || passes_minp(s, v)); };
-  for (int g = warp; g < n_seg; g += kWarpsS) {
-    u64 sum = 0;
-    uint32_t ties = 0;
+  // four consecutive indices of a segment per lane; past the end: -inf
+  auto load4 = [&](int i, float (&v)[4]) {
+    if (vec && i + 4 <= i1) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(z + i);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(z + i);
+        const T* e = reinterpret_cast<const T*>(&x);
 #pragma unroll
-    for (int j = 0; j < kSeg / 32; ++j) {
-      const int i = i0 + g * kSeg + j * 32 + lane;
-      if (i < i1) {
-        const float v = load_logit(z + i);
-        if (kept(v)) sum += weight(s, v);
-        ties += tied(v);
+        for (int k = 0; k < 4; ++k) v[k] = as_float(e[k]);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = i + k < i1 ? as_float(z[i + k]) : -CUDART_INF_F;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    ties = __reduce_add_sync(0xffffffffu, ties);
-    if (lane == 0) sh.seg[g] = sum, sh.tie[g] = ties;
+    for (int k = 0; k < 4; ++k) v[k] = capped(s, v[k]);
+  };
+  constexpr int kAtOnce = 4;   // segments of a warp at once: their loads overlap
+  for (int g0 = warp * kAtOnce; g0 < n_seg; g0 += kWarpsS * kAtOnce) {
+    float v[kAtOnce][4];
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x)
+      if (g0 + x < n_seg) load4(i0 + (g0 + x) * kSeg + 4 * lane, v[x]);
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      if (g0 + x >= n_seg) break;
+      u64 sum = 0;
+      uint32_t ties = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (kept(v[x][k])) sum += weight(s, v[x][k]);
+        ties += tied(v[x][k]);
+      }
+      // the lanes' sums are below 2^45: two pieces of 23 bits
+      const u64 lo = __reduce_add_sync(0xffffffffu, (uint32_t)sum & 0x7fffffu);
+      const u64 hi = __reduce_add_sync(0xffffffffu, (uint32_t)(sum >> 23));
+      ties = __reduce_add_sync(0xffffffffu, ties);
+      if (lane == 0) sh.seg[g0 + x] = lo + (hi << 23), sh.tie[g0 + x] = ties;
+    }
   }
   __syncthreads();
   // prefix of the ties: how many of a segment's are kept
@@ -689,13 +775,11 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
     if (r < rank) before += t;
     mass += t;
   }
-  __syncthreads();
-  if (threadIdx.x == 0) sh.goal = min((u64)floor((double)u * (double)mass), mass - 1);
+  const u64 goal = min(times(mass, u, false), mass - 1);
   m_run += before;
   t_run = t_first;
   if (threadIdx.x == 0) sh.cross_bin = -1;
   __syncthreads();
-  const u64 goal = sh.goal;
   for (int j = 0; j < kPerS; ++j) {
     const int g = threadIdx.x * kPerS + j;
     if (g < n_seg) {
@@ -710,27 +794,28 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const __grid_constant__ Pa
   }
   __syncthreads();
   if (warp == 0 && sh.cross_bin >= 0) {
-    u64 run = sh.cross_mass, ties = sh.scan_total;
-    bool done = false;
-    for (int j = 0; j < kSeg / 32 && !done; ++j) {
-      const int i = i0 + sh.cross_bin * kSeg + j * 32 + lane;
-      u64 w = 0;
-      bool tie = false;
-      if (i < i1) {
-        const float v = load_logit(z + i);
-        if (kept(v)) w = weight(s, v);
-        tie = tied(v);
+    const int i = i0 + sh.cross_bin * kSeg + 4 * lane;
+    float v[4];
+    load4(i, v);
+    u64 w[4], sum = 0;
+    uint32_t ties = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) ties += tied(v[k]);
+    u64 t_at = sh.scan_total + warp_incl(ties) - ties;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[k] = kept(v[k]) ? weight(s, v[k]) : 0ull;
+      if (tied(v[k])) w[k] = t_at++ < thr_ties ? w_tie : 0ull;
+      sum += w[k];
+    }
+    u64 run = sh.cross_mass + warp_incl(sum) - sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (run <= goal && run + w[k] > goal) {
+        p.token[row] = i + k;
+        if (p.logprob) p.logprob[row] = (float)log((double)w[k] / (double)mass);
       }
-      const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie);
-      if (tie && ties + __popc(tie_mask & ((1u << lane) - 1u)) < thr_ties) w = w_tie;
-      ties += __popc(tie_mask);
-      const u64 incl = warp_incl(w) + run;
-      if (incl > goal && incl - w <= goal) {
-        p.token[row] = i;
-        if (p.logprob) p.logprob[row] = (float)log((double)w / (double)mass);
-      }
-      run = __shfl_sync(0xffffffffu, incl, 31);
-      done = run > goal;
+      run += w[k];
     }
   }
   cluster_sync();   // no CTA leaves while another reads its shared memory
