@@ -18,7 +18,7 @@
 // an fp32 pair (the difference exactly, 8 log2(e)/T in two pieces), cut into
 // n = floor(8 t), an eighth of an octave, and the rest f in [0, 1], which goes
 // through a degree-6 polynomial of 2^(-f/8) to a 28-bit mantissa; the weight is
-// mantissa * 2^(-(n mod 8)/8) * 2^-(n div 8) rounded to units of 2^-42.
+// mantissa * 2^(-(n mod 8)/8) * 2^-(n div 8), cut off to units of 2^-42.
 // Integer sums have no order, so atomics and cluster reductions give the same
 // bits on every run.  A weight is off by about 2^-29 of itself, unbiased.
 // Products of a mass with top_p or u are formed exactly in 128 bits (fp64 runs
@@ -28,7 +28,7 @@
 //   A  the maximum (greedy rows: then its lowest index);
 //   B  a histogram of n over the row (1024 bins: 128 octaves), which bounds
 //      the last bin that S can reach;
-//   C  few candidates (<= 1024) up to that bin: they are gathered into the
+//   C  few candidates (<= 2048) up to that bin: they are gathered into the
 //      leader CTA, ranked, cut and sampled there;
 //   D  many: the bin that holds a border is refined by histograms of the
 //      order-preserving integer key (1024 sub-bins a level) until the
@@ -50,10 +50,11 @@ constexpr int kThr = 512;
 constexpr int kWarpsS = kThr / 32;
 constexpr int kBins = 1024;
 static_assert(kBins == 2 * kThr, "a thread has two bins of a merged histogram");
-constexpr int kCap = 1024;          // candidates that the leader takes
+constexpr int kCap = 2048;          // candidates that the leader takes
 constexpr int kCount = 256;         // up to here they are ranked by counting, else sorted
 constexpr int kSeg = 128;           // indices per segment of the final pass
 constexpr int kMaxSegs = 1024;      // segments of a CTA: 2^17 indices, so a 32-bit bin never overflows
+constexpr int kKeep = 64;           // indices a thread may keep in registers
 typedef unsigned long long u64;
 
 struct Params {
@@ -112,48 +113,61 @@ __device__ __forceinline__ float capped(const Scale& s, float z) {
 // Not below kBins (or NaN): the weight is below 2^-128 and never counts.
 __device__ __forceinline__ float eighths(const Scale& s, float z) { return (s.top - z) * s.ch; }
 
-// 28-bit mantissa of the weight inside its bin: 2^-(t - n/8), in (0.9, 1] * 2^28.
-__device__ __forceinline__ uint32_t mantissa(const Scale& s, float z, float q, int n) {
+// floor(q) for 0 <= q < 2^22, as a number and as an integer, without the
+// conversion unit (a quarter of the rate of an addition or less).
+__device__ __forceinline__ int whole(float q, float* n) {
+  const float t = __fadd_rd(q, 8388608.f);
+  *n = t - 8388608.f;
+  return __float_as_int(t) & 0x7fffff;
+}
+
+// 28-bit mantissa of the weight inside its bin n: 2^-(t - n/8), in (0.9, 1] * 2^28.
+__device__ __forceinline__ uint32_t mantissa(const Scale& s, float z, float q, float n) {
   const float d = s.top - z, bb = d - s.top;
   const float dl = (s.top - (d - bb)) - (z + bb);           // the exact difference is d + dl
   const float e = fmaf(d, s.ch, -q) + fmaf(d, s.cl, dl * s.ch);
-  const float f = (q - (float)n) + e;
-  // 2^(-f/8) - 1 on [0, 1]: the series of exp(-f ln 2 / 8); the next term is below 2^-37
-  float g = 5.875980527e-10f;
-  g = fmaf(g, f, -4.069079024e-08f);
-  g = fmaf(g, f, 2.348176052e-06f);
-  g = fmaf(g, f, -1.084064622e-04f);
-  g = fmaf(g, f, 3.753539171e-03f);
-  g = fmaf(g, f, -8.664339757e-02f);
-  g = g * f;
-  return (uint32_t)((1 << 28) + __float2int_rn(g * 268435456.f));
+  const float f = (q - n) + e;
+  // (2^(-f/8) - 1) 2^28 on [0, 1]: the series of exp(-f ln 2 / 8); the next term is below 2^-9
+  float g = 1.577321512e-01f;
+  g = fmaf(g, f, -1.092285083e+01f);
+  g = fmaf(g, f, 6.303337092e+02f);
+  g = fmaf(g, f, -2.910013812e+04f);
+  g = fmaf(g, f, 1.007582999e+06f);
+  g = fmaf(g, f, -2.325815994e+07f);
+  return (uint32_t)((1 << 28) + __float2int_rn(g * f));
 }
 
-// 2^(-j/8) * 2^31, rounded
+// 2^(-j/8) * 2^31, rounded; the kernel keeps a copy in shared memory (lanes that
+// ask for different entries of constant memory wait for one another).
 __device__ __constant__ uint32_t kEighth[8] = {2147483648u, 1969251188u, 1805811301u, 1655936265u,
                                                1518500250u, 1392470869u, 1276901417u, 1170923762u};
 
-// The weight in units of 2^-42.
-__device__ __forceinline__ u64 weight_of(uint32_t mant, int n) {
-  const u64 w = (u64)mant * kEighth[n & 7];        // 2^59 scale
-  const int sh = 17 + (n >> 3);
-  return sh > 60 ? 0ull : (w + (1ull << (sh - 1))) >> sh;
+__device__ __forceinline__ u64 shift_right(u64 x, int by) {   // 0 from 64 on
+  u64 r;
+  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(x), "r"(by));
+  return r;
 }
-__device__ __forceinline__ u64 weight(const Scale& s, float z) {
-  const float q = eighths(s, z);
-  if (!(q < (float)kBins)) return 0ull;
-  const int n = (int)q;
-  return weight_of(mantissa(s, z, q, n), n);
+// The weight in units of 2^-42 (2^-59 before the shift), cut off.
+__device__ __forceinline__ u64 weight_of(const uint32_t* eighth, uint32_t mant, int n) {
+  return shift_right((u64)mant * eighth[n & 7], 17 + (n >> 3));
 }
-__device__ __forceinline__ bool passes_minp(const Scale& s, float z) {
-  const float q = eighths(s, z);
-  if (!(q < (float)kBins)) return false;
-  const int n = (int)q;
-  return ((u64)mantissa(s, z, q, n) * kEighth[n & 7]) >> (n >> 3) >= s.minp;
+// Of any logit, a NaN among them, without a branch: the elements of a thread are
+// computed side by side.  Beyond the bins the shift leaves nothing.
+__device__ __forceinline__ u64 weight(const uint32_t* eighth, const Scale& s, float z) {
+  const float q = fminf(eighths(s, z), (float)kBins - 1.f);
+  float nf;
+  const int n = whole(q, &nf);
+  return weight_of(eighth, mantissa(s, z, q, nf), n);
+}
+__device__ __forceinline__ bool passes_minp(const uint32_t* eighth, const Scale& s, float z) {
+  const float q = fminf(eighths(s, z), (float)kBins - 1.f);
+  float nf;
+  const int n = whole(q, &nf);
+  return shift_right((u64)mantissa(s, z, q, nf) * eighth[n & 7], n >> 3) >= s.minp;
 }
 
 // floor (or ceiling) of m * f for 0 <= f < 1, exactly.
-__device__ __forceinline__ u64 times(u64 m, float f, bool up) {
+__device__ __noinline__ u64 times(u64 m, float f, bool up) {
   const uint32_t b = __float_as_uint(f);
   const int ex = (int)(b >> 23);
   const u64 mant = ex ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
@@ -167,6 +181,8 @@ __device__ __forceinline__ u64 times(u64 m, float f, bool up) {
   return q + (up && rest ? 1 : 0);
 }
 
+__device__ __noinline__ float ln_ratio(u64 w, u64 mass) { return (float)log((double)w / (double)mass); }
+
 template <typename T>
 __device__ __forceinline__ float as_float(T v) {
   if constexpr (sizeof(T) == 4) return v;
@@ -174,38 +190,94 @@ __device__ __forceinline__ float as_float(T v) {
   else return __bfloat162float(v);
 }
 
-// Calls f(logit, index) for every index of [i0, i1) of the row, in no order; i0
-// is a multiple of kSeg, vec: the row begins on a 16-byte boundary.
-template <typename T, typename F>
-__device__ __forceinline__ void sweep(const T* row, int i0, int i1, bool vec, F f) {
-  constexpr int E = 16 / sizeof(T), U = sizeof(T) == 4 ? 4 : 2;
-  if (vec) {
-    const int full = i0 + (i1 - i0) / E * E, step = E * kThr;
-    int i = i0 + E * (int)threadIdx.x;
-    for (; i + (U - 1) * step < full; i += U * step) {
-      uint4 v[U];
+// E consecutive logits from index i on, a multiple of E; NaN behind i1 (a NaN is
+// neither a maximum nor below any bound).  vec: the row begins on a 16-byte
+// boundary.
+template <typename T, int E>
+__device__ __forceinline__ void load_logits(const T* row, int i, int i1, bool vec, float (&v)[E]) {
+  if (vec && i + E <= i1) {
+    T e[E];
+    if constexpr (sizeof(e) == 16) *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(row + i);
+    else *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(row + i);
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const uint4*>(row + i + u * step);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const T* e = reinterpret_cast<const T*>(&v[u]);
-#pragma unroll
-        for (int k = 0; k < E; ++k) f(as_float(e[k]), i + u * step + k);
-      }
-    }
-    for (; i < full; i += step) {
-      const uint4 v = *reinterpret_cast<const uint4*>(row + i);
-      const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-      for (int k = 0; k < E; ++k) f(as_float(e[k]), i + k);
-    }
-    i = full + (int)threadIdx.x;
-    if (i < i1) f(as_float(row[i]), i);
+    for (int k = 0; k < E; ++k) v[k] = as_float(e[k]);
   } else {
-#pragma unroll 4
-    for (int i = i0 + (int)threadIdx.x; i < i1; i += kThr) f(as_float(row[i]), i);
+#pragma unroll
+    for (int k = 0; k < E; ++k) v[k] = i + k < i1 ? as_float(row[i + k]) : CUDART_NAN_F;
   }
 }
+
+// A CTA's part [i0, i1) of the row, i0 a multiple of kSeg.  KEEP: the part has at
+// most kKeep indices a thread, which stay in registers from the first pass on.
+template <typename T, bool KEEP>
+struct Part {
+  static constexpr int E = 16 / sizeof(T), kVecs = kKeep / E, step = E * kThr;
+  const T* row;
+  int i0, i1;
+  bool vec;
+  float v[KEEP ? kKeep : 1];
+
+  __device__ __forceinline__ void load() {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int x = 0; x < kVecs; ++x) {
+        float t[E];
+        load_logits<T, E>(row, i0 + E * (int)threadIdx.x + x * step, i1, vec, t);
+#pragma unroll
+        for (int k = 0; k < E; ++k) v[x * E + k] = t[k];
+      }
+    }
+  }
+  // Calls f(logit, index) for every index, and with NaNs behind them, in no
+  // order: short bodies.
+  template <typename F>
+  __device__ __forceinline__ void light(F f) const {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int x = 0; x < kVecs; ++x)
+#pragma unroll
+        for (int k = 0; k < E; ++k) f(v[x * E + k], i0 + E * (int)threadIdx.x + x * step + k);
+    } else {
+      constexpr int U = sizeof(T) == 4 ? 4 : 2;   // loads in flight
+      int i = i0 + E * (int)threadIdx.x;
+      if (vec) {
+#pragma unroll 1
+        for (; i + (U - 1) * step + E <= i1; i += U * step) {
+          float t[U][E];
+#pragma unroll
+          for (int x = 0; x < U; ++x) load_logits<T, E>(row, i + x * step, 0x7fffffff, true, t[x]);
+#pragma unroll
+          for (int x = 0; x < U; ++x)
+#pragma unroll
+            for (int k = 0; k < E; ++k) f(t[x][k], i + x * step + k);
+        }
+      }
+#pragma unroll 1
+      for (; i < i1; i += step) {
+        float t[E];
+        load_logits<T, E>(row, i, i1, vec, t);
+#pragma unroll
+        for (int k = 0; k < E; ++k) f(t[k], i + k);
+      }
+    }
+  }
+  // The same for long bodies, expanded for one load only, the next one in flight
+  // meanwhile.
+  template <typename F>
+  __device__ __forceinline__ void heavy(F f) const {
+    float next[E];
+    load_logits<T, E>(row, i0 + E * (int)threadIdx.x, i1, vec, next);
+#pragma unroll 1
+    for (int i = i0 + E * (int)threadIdx.x; i < i1; i += step) {
+      float t[E];
+#pragma unroll
+      for (int k = 0; k < E; ++k) t[k] = next[k];
+      load_logits<T, E>(row, i + step, i1, vec, next);
+#pragma unroll
+      for (int k = 0; k < E; ++k) f(t[k], i + k);
+    }
+  }
+};
 
 __device__ __forceinline__ u64 ld_cluster_u64(uint32_t a) {
   u64 v;
@@ -222,6 +294,20 @@ __device__ __forceinline__ void cluster_sync() {
   tc::cluster_wait();
 }
 
+// Sum of a 64-bit value that every CTA has at `v`, and of those of the CTAs
+// before this one: lane r asks CTA r.
+__device__ __forceinline__ u64 cluster_sum(const u64* v, uint32_t rank, uint32_t ctas, u64* before) {
+  const uint32_t lane = threadIdx.x & 31;
+  u64 x = lane < ctas ? ld_cluster_u64(tc::cluster_addr(v, lane)) : 0ull, y = lane < rank ? x : 0ull;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  *before = __shfl_sync(0xffffffffu, y, 0);
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
 struct Shared {
   uint32_t cnt[kBins], lo[kBins], hi[kBins];   // per bin: elements, sums of the mantissa's low 14 and high bits
   union {
@@ -229,16 +315,15 @@ struct Shared {
     u64 seg[kMaxSegs];                         // masses of the segments
   };
   uint32_t tie[kMaxSegs];                      // elements equal to the threshold, per segment
-  u64 total;                                   // this CTA's mass (phase B), then of S
   float top;                                   // this CTA's maximum
   int first;                                   // its first index that holds the row's
   u64 mine;                                    // this CTA's mass of S
-  uint32_t ties;                               // this CTA's elements equal to the threshold
+  u64 ties;                                    // this CTA's elements equal to the threshold
   uint32_t n_list;
   u64 red[kWarpsS];
   uint32_t red32[kWarpsS];
   u64 scan_total;
-  u64 goal;
+  uint32_t eighth[8];
   // the crossing bin of a scan
   int cross_bin;
   uint32_t cross_cnt;
@@ -273,18 +358,19 @@ __device__ __forceinline__ V block_incl(V v, V* red, V* total) {
   return v + before;
 }
 
-// Ascending bitonic sort of n values in shared memory, n a power of two.
-__device__ __forceinline__ void bitonic(u64* v, int n) {
+// Ascending bitonic sort of n values in shared memory, n a power of two.  A
+// warp's 32 pairs of a step lie in 64 neighbouring values when they are at most
+// 32 apart, so only the wider steps need the whole CTA.
+__device__ __noinline__ void bitonic(u64* v, int n) {
+  __syncthreads();
   for (int k = 2; k <= n; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < n; i += kThr) {
-        const int x = i ^ j;
-        if (x > i) {
-          const u64 a = v[i], b = v[x];
-          if ((a > b) == ((i & k) == 0)) v[i] = b, v[x] = a;
-        }
+      for (int p = threadIdx.x; p < n / 2; p += kThr) {
+        const int i = p + (p & ~(j - 1)), x = i + j;
+        const u64 a = v[i], b = v[x];
+        if ((a > b) == ((i & k) == 0)) v[i] = b, v[x] = a;
       }
+      if (j > 32 || (j == 1 && k >= 64)) __syncthreads(); else __syncwarp();
     }
   __syncthreads();
 }
@@ -292,7 +378,7 @@ __device__ __forceinline__ void bitonic(u64* v, int n) {
 // Adds every CTA's histogram, in every CTA: bins 2 threadIdx.x and + 1.
 __device__ __forceinline__ void merge_bins(Shared& sh, uint32_t ctas, bool masses, u64 (&cnt)[2], u64 (&mant)[2]) {
   cnt[0] = cnt[1] = mant[0] = mant[1] = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (uint32_t r = 0; r < ctas; ++r) {
     const u64 c = ld_cluster_u64(tc::cluster_addr(&sh.cnt[2 * threadIdx.x], r));
     cnt[0] += (uint32_t)c, cnt[1] += c >> 32;
@@ -316,17 +402,17 @@ __device__ __forceinline__ void add_to_bin(Shared& sh, int b, uint32_t mant) {
 }
 
 // Mass of a bin whose elements' mantissas sum to m, in units of 2^-42.
-__device__ __forceinline__ u64 bin_mass(u64 m, int n) {
+__device__ __forceinline__ u64 bin_mass(const uint32_t* eighth, u64 m, int n) {
   // m < 2^49: in two pieces so that the product with the 32-bit factor fits
-  const u64 e = kEighth[n & 7];
+  const u64 e = eighth[n & 7];
   const u64 a = (m >> 24) * e, b = (m & 0xffffffu) * e;   // 2^59 scale: a << 24 + b
   const int sh = 17 + (n >> 3);
   if (sh > 80) return 0ull;
   return (sh >= 24 ? a >> (sh - 24) : a << (24 - sh)) + (sh < 60 ? b >> sh : 0ull);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__ Params p) {
+template <typename T, bool KEEP>
+__global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid_constant__ Params p) {
   __shared__ Shared sh;
   uint32_t rank, ctas;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -334,11 +420,15 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
   const int row = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) sh.n_list = 0, sh.first = 0x7fffffff;
+  if (threadIdx.x < 8) sh.eighth[threadIdx.x] = kEighth[threadIdx.x];
   clear_bins(sh);
   pdl_wait();
   const T* z = static_cast<const T*>(p.z) + row * p.stride;
   const bool vec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
   const int i0 = min((int)rank * p.range, p.V), i1 = min(i0 + p.range, p.V);
+  Part<T, KEEP> part;
+  part.row = z, part.i0 = i0, part.i1 = i1, part.vec = vec;
+  part.load();
 
   const float temp = p.temperature ? p.temperature[row] : 1.f;
   const int k_in = p.top_k ? p.top_k[row] : 0;
@@ -352,7 +442,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
   // ---- A: the maximum (fmaxf passes over a NaN)
   float top = -CUDART_INF_F;
   {
-    sweep(z, i0, i1, vec, [&](float v, int) { top = fmaxf(top, v); });
+    part.light([&](float v, int) { top = fmaxf(top, v); });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) sh.red32[warp] = __float_as_uint(top);
@@ -364,15 +454,16 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
       if (lane == 0) sh.top = top;
     }
     cluster_sync();
-    top = -CUDART_INF_F;
-    for (uint32_t r = 0; r < ctas; ++r) top = fmaxf(top, __uint_as_float(ld_cluster_u32(tc::cluster_addr(&sh.top, r))));
+    top = lane < (int)ctas ? __uint_as_float(ld_cluster_u32(tc::cluster_addr(&sh.top, lane))) : -CUDART_INF_F;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
   const bool nothing = top == -CUDART_INF_F;
   const bool greedy = !(temp > 0.f) || k_in == 1 || top_p <= 0.f;
   if (nothing || greedy) {   // the same in every CTA of the cluster
     if (!nothing) {
       int first = 0x7fffffff;
-      sweep(z, i0, i1, vec, [&](float v, int i) { first = v == top ? min(first, i) : first; });
+      part.light([&](float v, int i) { first = v == top ? min(first, i) : first; });
       first = __reduce_min_sync(0xffffffffu, first);
       if (lane == 0 && first != 0x7fffffff) atomicMin(&sh.first, first);
     }
@@ -391,33 +482,31 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
   int last = kBins - 1;          // last bin that S can reach
   uint32_t n_cand = 0xffffffffu;   // elements up to it
   u64 total = 0;                 // mass of the row (top-p without top-k)
+  u64 cnt[2] = {0, 0}, mant[2] = {0, 0};   // this thread's two bins of the row's histogram
+  const bool row_mass = has_p && !has_k;
   if (has_k || has_p || has_m) {
-    // ---- B: histogram over the row; its mass when the row has no top-k
-    if (has_p && !has_k) {
-      u64 sum = 0;
-      sweep(z, i0, i1, vec, [&](float v, int) {
+    // ---- B: histogram over the row, with masses for top-p without top-k
+    // (which goes by the mass of the whole row)
+    if (row_mass) {
+      part.heavy([&](float v, int) {
         v = capped(s, v);
         const float q = eighths(s, v);
         if (q < (float)kBins) {
-          const int n = (int)q;
-          atomicAdd(&sh.cnt[n], 1u);
-          sum += weight_of(mantissa(s, v, q, n), n);
+          float nf;
+          const int n = whole(q, &nf);
+          add_to_bin(sh, n, mantissa(s, v, q, nf));
         }
       });
-      u64 tot;
-      block_incl(sum, sh.red, &tot);
-      if (threadIdx.x == 0) sh.total = tot;
-      cluster_sync();
-      for (uint32_t r = 0; r < ctas; ++r) total += ld_cluster_u64(tc::cluster_addr(&sh.total, r));
     } else {
-      sweep(z, i0, i1, vec, [&](float v, int) {
+      part.light([&](float v, int) {
         const float q = eighths(s, capped(s, v));
         if (q < (float)kBins) atomicAdd(&sh.cnt[(int)q], 1u);
       });
-      cluster_sync();
     }
-    u64 cnt[2], mant[2];
-    merge_bins(sh, ctas, false, cnt, mant);
+    cluster_sync();
+    merge_bins(sh, ctas, row_mass, cnt, mant);
+    if (row_mass)
+      block_incl(bin_mass(sh.eighth, mant[0], 2 * threadIdx.x) + bin_mass(sh.eighth, mant[1], 2 * threadIdx.x + 1), sh.red, &total);
     u64 all;
     const u64 incl = block_incl(cnt[0] + cnt[1], sh.red, &all);
     const u64 c0 = incl - cnt[1], c1 = incl;   // elements up to bin 2 tid and 2 tid + 1
@@ -449,7 +538,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
     // ---- C: the candidates into the leader
     const uint32_t list0 = tc::cluster_addr(sh.list, 0), count0 = tc::cluster_addr(&sh.n_list, 0);
     const float lim = (float)(last + 1);
-    sweep(z, i0, i1, vec, [&](float v, int i) {
+    part.light([&](float v, int i) {
       v = capped(s, v);
       if (eighths(s, v) < lim) {
         uint32_t at;
@@ -483,7 +572,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = kPer * threadIdx.x + j;
-      w[j] = i < nk ? weight(s, logit_of(~(uint32_t)(sh.list[i] >> 32))) : 0ull;
+      w[j] = i < nk ? weight(sh.eighth, s, logit_of(~(uint32_t)(sh.list[i] >> 32))) : 0ull;
       sum += w[j];
     }
     const u64 incl = block_incl(sum, sh.red, &mass_k);
@@ -494,7 +583,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = kPer * threadIdx.x + j;
-      const bool k = i < nk && (i == 0 || (before < limit && (!has_m || passes_minp(s, logit_of(~(uint32_t)(sh.list[i] >> 32))))));
+      const bool k = i < nk && (i == 0 || (before < limit && (!has_m || passes_minp(sh.eighth, s, logit_of(~(uint32_t)(sh.list[i] >> 32))))));
       before += w[j];
       keep += k;
       kept += k ? w[j] : 0ull;
@@ -504,11 +593,12 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
     keep = (int)__reduce_add_sync(0xffffffffu, (unsigned)keep);
     __syncthreads();
     if (lane == 0) sh.red32[warp] = (uint32_t)keep;
-    // the weights, beside the elements
+    // the first weights, beside the elements
     u64* wt = reinterpret_cast<u64*>(sh.cnt);
-    static_assert(sizeof(sh.cnt) + sizeof(sh.lo) >= kCap * 8, "the weights take the place of the bins");
+    static_assert(sizeof(sh.cnt) >= kCount * 8, "the weights take the place of the bins");
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) wt[kPer * threadIdx.x + j] = w[j];
+    for (int j = 0; j < kPer; ++j)
+      if (kPer * threadIdx.x + j < kCount) wt[kPer * threadIdx.x + j] = w[j];
     __syncthreads();
     keep = 0;
     for (int x = 0; x < kWarpsS; ++x) keep += (int)sh.red32[x];
@@ -516,7 +606,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
     const u64 goal = min(times(mass, u, false), mass - 1);
     auto pick = [&](int index, u64 wi) {
       p.token[row] = index;
-      if (p.logprob) p.logprob[row] = (float)log((double)wi / (double)mass);
+      if (p.logprob) p.logprob[row] = ln_ratio(wi, mass);
     };
     if (keep <= kCount) {
       const int i = threadIdx.x >> 1;
@@ -537,7 +627,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int i = kPer * threadIdx.x + j;
-        w[j] = i < keep ? weight(s, logit_of(~(uint32_t)sh.list[i])) : 0ull;
+        w[j] = i < keep ? weight(sh.eighth, s, logit_of(~(uint32_t)sh.list[i])) : 0ull;
         sum += w[j];
       }
       u64 run = block_incl(sum, sh.red, &mass) - sum;
@@ -556,23 +646,24 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
   uint32_t thr_key = 0;
   u64 thr_ties = ~0ull;
   if (has_k || has_p) {
-    // histogram with masses, up to the last bin that matters
-    cluster_sync();   // every CTA has read the counts
-    clear_bins(sh);
-    __syncthreads();
-    const float lim = (float)(last + 1);
-    sweep(z, i0, i1, vec, [&](float v, int) {
-      v = capped(s, v);
-      const float q = eighths(s, v);
-      if (q < lim) {
-        const int n = (int)q;
-        add_to_bin(sh, n, mantissa(s, v, q, n));
-      }
-    });
-    cluster_sync();
-    u64 cnt[2], mant[2];
-    merge_bins(sh, ctas, true, cnt, mant);
-    u64 mass[2] = {bin_mass(mant[0], 2 * threadIdx.x), bin_mass(mant[1], 2 * threadIdx.x + 1)};
+    if (has_p && has_k) {   // the masses too, up to the last bin that matters
+      cluster_sync();       // every CTA has read the counts
+      clear_bins(sh);
+      __syncthreads();
+      const float lim = (float)(last + 1);
+      part.heavy([&](float v, int) {
+        v = capped(s, v);
+        const float q = eighths(s, v);
+        if (q < lim) {
+          float nf;
+          const int n = whole(q, &nf);
+          add_to_bin(sh, n, mantissa(s, v, q, nf));
+        }
+      });
+      cluster_sync();
+      merge_bins(sh, ctas, true, cnt, mant);
+    }
+    u64 mass[2] = {bin_mass(sh.eighth, mant[0], 2 * threadIdx.x), bin_mass(sh.eighth, mant[1], 2 * threadIdx.x + 1)};
     u64 dummy;
     const u64 cnt_incl = block_incl(cnt[0] + cnt[1], sh.red, &dummy);
     const u64 mass_incl = block_incl(mass[0] + mass[1], sh.red, &dummy);
@@ -629,17 +720,21 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
         cluster_sync();   // every CTA has read the last histogram
         clear_bins(sh);
         __syncthreads();
-        sweep(z, i0, i1, vec, [&](float v, int) {
+        part.heavy([&](float v, int) {
           v = capped(s, v);
           const uint32_t k = key_of(v);
-          if (k - k_lo <= width) add_to_bin(sh, (int)((k_hi - k) >> shift), mantissa(s, v, eighths(s, v), bin));
+          if (k - k_lo <= width) {
+            const int b = (int)((k_hi - k) >> shift);
+            if (has_p) add_to_bin(sh, b, mantissa(s, v, eighths(s, v), (float)bin));
+            else atomicAdd(&sh.cnt[b], 1u);
+          }
         });
         cluster_sync();
         u64 c[2], m[2];
-        merge_bins(sh, ctas, true, c, m);
+        merge_bins(sh, ctas, has_p, c, m);
         u64 t;
         const u64 ci = block_incl(c[0] + c[1], sh.red, &t);
-        const u64 m_sub[2] = {bin_mass(m[0], bin), bin_mass(m[1], bin)};
+        const u64 m_sub[2] = {bin_mass(sh.eighth, m[0], bin), bin_mass(sh.eighth, m[1], bin)};
         const u64 mi = block_incl(m_sub[0] + m_sub[1], sh.red, &t);
         if (threadIdx.x == 0) sh.cross_bin = -1;
         __syncthreads();
@@ -675,7 +770,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
         if (shift == 0) {
           thr_key = k_hi;
           const float v = logit_of(k_hi);
-          const u64 w = weight_of(mantissa(s, v, eighths(s, v), bin), bin);
+          const u64 w = weight_of(sh.eighth, mantissa(s, v, eighths(s, v), (float)bin), bin);
           const u64 rest = goal > (by_mass ? m_before : c_before) ? goal - (by_mass ? m_before : c_before) : 1ull;
           thr_ties = by_mass ? (w ? (rest + w - 1) / w : ~0ull) : rest;
           *mass_out = m_before + w * (by_mass ? 0ull : thr_ties);
@@ -697,48 +792,39 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
   // masses and ties of the segments of this CTA's range
   cluster_sync();   // sh.list / sh.seg are free, every histogram read
   const int n_seg = (i1 - i0 + kSeg - 1) / kSeg;
-  auto kept = [&](float v) { return key_of(v) > thr_key && (!has_m || passes_minp(s, v)); };
-  auto tied = [&](float v) { return key_of(v) == thr_key && thr_key != 0 && (!has_m || passes_minp(s, v)); };
-  // four consecutive indices of a segment per lane; past the end: -inf
-  auto load4 = [&](int i, float (&v)[4]) {
-    if (vec && i + 4 <= i1) {
-      if constexpr (sizeof(T) == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(z + i);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(z + i);
-        const T* e = reinterpret_cast<const T*>(&x);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = as_float(e[k]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = i + k < i1 ? as_float(z[i + k]) : -CUDART_INF_F;
-    }
+  const bool cuts = thr_key != 0;
+  const float cut = cuts ? logit_of(thr_key) : -CUDART_INF_F;   // (copies: descend() holds references to the others)
+  const u64 cut_ties = thr_ties;
+  auto kept = [&](float v) { return v > cut && (!has_m || passes_minp(sh.eighth, s, v)); };
+  auto tied = [&](float v) { return cuts && v == cut && (!has_m || passes_minp(sh.eighth, s, v)); };
+  // four consecutive indices of a segment per lane
+  auto load4 = [&](int g, float (&v)[4]) {
+    load_logits<T, 4>(z, i0 + g * kSeg + 4 * lane, i1, vec, v);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = capped(s, v[k]);
   };
-  constexpr int kAtOnce = 4;   // segments of a warp at once: their loads overlap
-  for (int g0 = warp * kAtOnce; g0 < n_seg; g0 += kWarpsS * kAtOnce) {
-    float v[kAtOnce][4];
+  {
+    float next[4];
+    load4(warp, next);
+#pragma unroll 1
+    for (int g = warp; g < n_seg; g += kWarpsS) {
+      float v[4];
 #pragma unroll
-    for (int x = 0; x < kAtOnce; ++x)
-      if (g0 + x < n_seg) load4(i0 + (g0 + x) * kSeg + 4 * lane, v[x]);
-#pragma unroll
-    for (int x = 0; x < kAtOnce; ++x) {
-      if (g0 + x >= n_seg) break;
+      for (int k = 0; k < 4; ++k) v[k] = next[k];
+      load4(g + kWarpsS, next);
       u64 sum = 0;
       uint32_t ties = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (kept(v[x][k])) sum += weight(s, v[x][k]);
-        ties += tied(v[x][k]);
+        const u64 wk = weight(sh.eighth, s, v[k]);
+        sum += kept(v[k]) ? wk : 0ull;
+        ties += tied(v[k]);
       }
       // the lanes' sums are below 2^45: two pieces of 23 bits
       const u64 lo = __reduce_add_sync(0xffffffffu, (uint32_t)sum & 0x7fffffu);
       const u64 hi = __reduce_add_sync(0xffffffffu, (uint32_t)(sum >> 23));
       ties = __reduce_add_sync(0xffffffffu, ties);
-      if (lane == 0) sh.seg[g0 + x] = lo + (hi << 23), sh.tie[g0 + x] = ties;
+      if (lane == 0) sh.seg[g] = lo + (hi << 23), sh.tie[g] = ties;
     }
   }
   __syncthreads();
@@ -751,16 +837,20 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
   }
   u64 cta_ties, cta_mass;
   u64 t_run = block_incl(t_sum, sh.red, &cta_ties) - t_sum;
-  if (threadIdx.x == 0) sh.ties = (uint32_t)cta_ties;
-  cluster_sync();
-  for (uint32_t r = 0; r < rank; ++r) t_run += ld_cluster_u32(tc::cluster_addr(&sh.ties, r));
-  const u64 w_tie = thr_key ? weight(s, logit_of(thr_key)) : 0ull;
+  if (cuts) {   // else nothing is tied
+    if (threadIdx.x == 0) sh.ties = cta_ties;
+    cluster_sync();
+    u64 before;
+    cluster_sum(&sh.ties, rank, ctas, &before);
+    t_run += before;
+  }
+  const u64 w_tie = cuts ? weight(sh.eighth, s, cut) : 0ull;
   const u64 t_first = t_run;
   m_sum = 0;
   for (int j = 0; j < kPerS; ++j) {
     const int g = threadIdx.x * kPerS + j;
     if (g < n_seg) {
-      const u64 left = thr_ties > t_run ? thr_ties - t_run : 0ull;
+      const u64 left = cut_ties > t_run ? cut_ties - t_run : 0ull;
       t_run += sh.tie[g];
       sh.seg[g] += w_tie * min((u64)sh.tie[g], left);
       m_sum += sh.seg[g];
@@ -769,12 +859,8 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
   u64 m_run = block_incl(m_sum, sh.red, &cta_mass) - m_sum;
   if (threadIdx.x == 0) sh.mine = cta_mass;
   cluster_sync();
-  u64 mass = 0, before = 0;
-  for (uint32_t r = 0; r < ctas; ++r) {
-    const u64 t = ld_cluster_u64(tc::cluster_addr(&sh.mine, r));
-    if (r < rank) before += t;
-    mass += t;
-  }
+  u64 before;
+  const u64 mass = cluster_sum(&sh.mine, rank, ctas, &before);
   const u64 goal = min(times(mass, u, false), mass - 1);
   m_run += before;
   t_run = t_first;
@@ -796,7 +882,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
   if (warp == 0 && sh.cross_bin >= 0) {
     const int i = i0 + sh.cross_bin * kSeg + 4 * lane;
     float v[4];
-    load4(i, v);
+    load4(sh.cross_bin, v);
     u64 w[4], sum = 0;
     uint32_t ties = 0;
 #pragma unroll
@@ -804,8 +890,8 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
     u64 t_at = sh.scan_total + warp_incl(ties) - ties;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      w[k] = kept(v[k]) ? weight(s, v[k]) : 0ull;
-      if (tied(v[k])) w[k] = t_at++ < thr_ties ? w_tie : 0ull;
+      w[k] = kept(v[k]) ? weight(sh.eighth, s, v[k]) : 0ull;
+      if (tied(v[k])) w[k] = t_at++ < cut_ties ? w_tie : 0ull;
       sum += w[k];
     }
     u64 run = sh.cross_mass + warp_incl(sum) - sum;
@@ -813,7 +899,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
     for (int k = 0; k < 4; ++k) {
       if (run <= goal && run + w[k] > goal) {
         p.token[row] = i + k;
-        if (p.logprob) p.logprob[row] = (float)log((double)w[k] / (double)mass);
+        if (p.logprob) p.logprob[row] = ln_ratio(w[k], mass);
       }
       run += w[k];
     }
@@ -821,8 +907,8 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const __grid_constant__
   cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
-template <typename T>
-static int launch(const Params& p, int rows, int cluster, cudaStream_t s) {
+template <typename T, bool KEEP>
+static int launch_k(const Params& p, int rows, int cluster, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster, rows);
   cfg.blockDim = dim3(kThr);
@@ -836,8 +922,13 @@ static int launch(const Params& p, int rows, int cluster, cudaStream_t s) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sample_kernel<T, KEEP>, p);
   return e == cudaSuccess ? Q4_OK : cuda_fail(e, "sampling launch");
+}
+
+template <typename T>
+static int launch(const Params& p, int rows, int cluster, bool keep, cudaStream_t s) {
+  return keep ? launch_k<T, true>(p, rows, cluster, s) : launch_k<T, false>(p, rows, cluster, s);
 }
 
 }  // namespace sample
@@ -845,14 +936,23 @@ static int launch(const Params& p, int rows, int cluster, cudaStream_t s) {
 int launch_logits_sample(const void* z, long long stride, int dtype, int rows, int V, const float* u,
                          const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                          int32_t* token, float* logprob, const DeviceInfo& dev, cudaStream_t s) {
-  (void)dev;
   sample::Params p = {z, stride, u, temperature, top_k, top_p, min_p, token, logprob, V, 0};
-  const int cluster = V > 16384 ? 8 : V > 4096 ? 2 : 1;
+  // CTAs per row: while the rows leave SMs free, eight (a row's time is what
+  // counts); with many rows fewer, as every phase that one CTA runs alone and
+  // every cluster barrier idles the others.  Not more indices per CTA than a
+  // 32-bit bin holds, nor CTAs for a few thousand indices.
+  int cluster = 8;
+  while (cluster > 1 && rows * cluster > 2 * dev.sms) cluster >>= 1;
+  while (cluster > 1 && V <= 2048 * cluster) cluster >>= 1;
+  while (V > cluster * sample::kSeg * sample::kMaxSegs) cluster <<= 1;
   const int segs = (V + sample::kSeg * cluster - 1) / (sample::kSeg * cluster);
   p.range = segs * sample::kSeg;
-  return dtype == Q4_F32   ? sample::launch<float>(p, rows, cluster, s)
-         : dtype == Q4_F16 ? sample::launch<__half>(p, rows, cluster, s)
-                           : sample::launch<__nv_bfloat16>(p, rows, cluster, s);
+  // Few rows: one CTA per SM with its part of the row in registers.  Many: two
+  // CTAs per SM that read it again from L2.
+  const bool keep = p.range <= sample::kKeep * sample::kThr && rows * cluster <= dev.sms;
+  return dtype == Q4_F32   ? sample::launch<float>(p, rows, cluster, keep, s)
+         : dtype == Q4_F16 ? sample::launch<__half>(p, rows, cluster, keep, s)
+                           : sample::launch<__nv_bfloat16>(p, rows, cluster, keep, s);
 }
 
 }  // namespace q4w
