@@ -10,8 +10,10 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
 
 import torch
 
@@ -77,9 +79,9 @@ _SIGS = {
     "q4_gemv_stage": (ci, [ctypes.POINTER(q4_matrix), ctypes.POINTER(ci), ci, ci, vp, ci, cf, ci,
                            ctypes.POINTER(vp), ctypes.POINTER(vp), vp]),
     "q4_rmsnorm_f16": (ci, [vp, ci, cf, vp, vp]),
-    "kv_append": (ci, [ctypes.POINTER(q4_kv_cache), ci, vp, cll, vp, cll, ci, vp, cll, ci, vp, vp, ci, ci, vp, vp,
+    "kv_append": (ci, [vp, ci, vp, cll, vp, cll, ci, vp, cll, ci, vp, vp, ci, ci, vp, vp,
                        vp]),
-    "kv_attention": (ci, [ctypes.POINTER(q4_kv_cache), ci, ci, vp, cll, ci, cf, ci, vp, vp, vp, vp, csz, vp]),
+    "kv_attention": (ci, [vp, ci, ci, vp, cll, ci, cf, ci, vp, vp, vp, vp, csz, vp]),
     "logits_sample": (ci, [vp, cll, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp]),
     "q4_workspace_bytes": (csz, [ci, ci, ci, ci]),
     "q4_status_string": (ctypes.c_char_p, [ci]),
@@ -136,7 +138,7 @@ def _stream():
 
 def _here(t):
     """Whether t is on the current CUDA device (the only one there is, as a rule)."""
-    return t.is_cuda and t.device.index == (0 if _one_device else torch.cuda.current_device())
+    return t.get_device() == (0 if _one_device else torch.cuda.current_device())
 
 
 def _numel(t, n, name):
@@ -149,7 +151,7 @@ def _numel(t, n, name):
 def _dev(t, dtype, name):
     if t is None:
         return
-    if t.dtype is dtype and _here(t) and t.is_contiguous():
+    if _one_device and t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.device.index == 0:
         return
     if not t.is_cuda:
         raise Q4Error(f"{name} must be a CUDA tensor")
@@ -584,6 +586,10 @@ def kv_rope_steps(rot_dim, theta=10000.0, device="cuda", freqs=None):
     return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
 
 
+# The calls of a decode step are short enough on the device for the host's time
+# to count, so the checks of the functions below avoid what is slow in Python:
+# helper calls per tensor and ctypes structures.
+
 def _heads(t, dtype, heads, dim, T, name):
     """A [T, heads, dim] tensor whose heads and elements are contiguous; returns the token stride."""
     if t.dtype is not dtype or not _here(t):
@@ -596,15 +602,23 @@ def _heads(t, dtype, heads, dim, T, name):
     return st if T > 1 else heads * dim
 
 
+_CACHE = struct.Struct("@5P7i4x")   # q4_kv_cache
+assert _CACHE.size == ctypes.sizeof(q4_kv_cache)
+
+
 def _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens):
+    """The checked cache as (the bytes of its q4_kv_cache, its dtype, n_kv, head_dim, n_seqs)."""
     dtype = k_cache.dtype
     if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise Q4Error(f"k_cache must be torch.float16 or torch.bfloat16, got {dtype}")
-    _dev(k_cache, dtype, "k_cache")
-    _dev(v_cache, dtype, "v_cache")
-    _dev(block_table, torch.int32, "block_table")
-    _dev(cu_tokens, torch.int32, "cu_tokens")
-    _dev(kv_lens, torch.int32, "kv_lens")
+    i32 = torch.int32
+    if not (v_cache.dtype is dtype and block_table.dtype is i32 and cu_tokens.dtype is i32 and kv_lens.dtype is i32
+            and _here(k_cache) and _here(v_cache) and _here(block_table) and _here(cu_tokens) and _here(kv_lens)
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()
+            and cu_tokens.is_contiguous() and kv_lens.is_contiguous()):
+        for t, dt, name in ((k_cache, dtype, "k_cache"), (v_cache, dtype, "v_cache"), (block_table, i32, "block_table"),
+                            (cu_tokens, i32, "cu_tokens"), (kv_lens, i32, "kv_lens")):
+            _dev(t, dt, name)   # names the fault
     shape, tshape = k_cache.shape, block_table.shape
     if len(shape) != 4 or shape != v_cache.shape:
         raise Q4Error(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} must both be "
@@ -612,10 +626,11 @@ def _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens):
     n = kv_lens.numel()
     if len(tshape) != 2 or tshape[0] != n:
         raise Q4Error(f"block_table has shape {tuple(tshape)}; kv_lens implies ({n}, max_pages)")
-    _numel(cu_tokens, n + 1, "cu_tokens")
+    if cu_tokens.numel() != n + 1:
+        _numel(cu_tokens, n + 1, "cu_tokens")
     pages, heads, page, dim = shape
-    return q4_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_tokens.data_ptr(),
-                       kv_lens.data_ptr(), _DTYPES[dtype], pages, heads, page, dim, n, tshape[1])
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_tokens.data_ptr(),
+                       kv_lens.data_ptr(), _DTYPES[dtype], pages, heads, page, dim, n, tshape[1]), dtype, heads, dim, n
 
 
 def kv_append(k, v, k_cache, v_cache, block_table, cu_tokens, kv_lens, steps=None, q=None, positions=None,
@@ -626,37 +641,51 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_tokens, kv_lens, steps=Non
     queries q [T, n_q, D] in the cache's type, or None without q.  kv_lens
     counts the new tokens already; see include/q4w.h for the layout."""
     lib = load()
-    cache = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
-    T, D = k.shape[0], cache.head_dim
-    if k.dtype not in _DTYPES:
-        raise Q4Error(f"k must be float32, float16 or bfloat16, got {k.dtype}")
+    cache, dtype, n_kv, D, _ = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
+    T, kt = k.shape[0], k.dtype
+    if kt not in _DTYPES:
+        raise Q4Error(f"k must be float32, float16 or bfloat16, got {kt}")
     if T == 0:
-        return None if q is None else torch.empty((0, q.shape[1], D), dtype=k_cache.dtype, device=k.device)
-    ks = _heads(k, k.dtype, cache.n_kv, D, T, "k")
-    vs = _heads(v, k.dtype, cache.n_kv, D, T, "v")
+        return None if q is None else torch.empty((0, q.shape[1], D), dtype=dtype, device=k.device)
+    ks = _heads(k, kt, n_kv, D, T, "k")
+    vs = _heads(v, kt, n_kv, D, T, "v")
     qs = n_q = 0
+    q_ptr = out_ptr = None
     if q is not None:
         n_q = q.shape[1] if q.dim() == 3 else 0
-        qs = _heads(q, k.dtype, n_q, D, T, "q")
+        qs = _heads(q, kt, n_q, D, T, "q")
         if q_out is None:
-            q_out = torch.empty((T, n_q, D), dtype=k_cache.dtype, device=q.device)
-        _dev(q_out, k_cache.dtype, "q_out")
-        _numel(q_out, T * n_q * D, "q_out")
+            q_out = torch.empty((T, n_q, D), dtype=dtype, device=q.device)
+        else:
+            _dev(q_out, dtype, "q_out")
+            _numel(q_out, T * n_q * D, "q_out")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise Q4Error("q_out without q")
-    _dev(steps, torch.int64, "steps")
-    _dev(positions, torch.int32, "positions")
-    _dev(err, torch.int32, "err")
+    steps_ptr, rot = None, 0
+    if steps is not None:
+        _dev(steps, torch.int64, "steps")
+        steps_ptr, rot = steps.data_ptr(), 2 * steps.numel()
     if positions is not None:
+        _dev(positions, torch.int32, "positions")
         _numel(positions, T, "positions")
-    _check(lib.kv_append(ctypes.byref(cache), T, _ptr(k), ks, _ptr(v), vs, _DTYPES[k.dtype], _ptr(q), qs, n_q,
-                         _ptr(q_out), _ptr(steps), 0 if steps is None else 2 * steps.numel(), int(interleaved),
-                         _ptr(positions), _ptr(err), _stream()), "kv_append")
+    if err is not None:
+        _dev(err, torch.int32, "err")
+    status = lib.kv_append(cache, T, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[kt], q_ptr, qs, n_q, out_ptr,
+                           steps_ptr, rot, 1 if interleaved else 0, _ptr(positions), _ptr(err), _stream())
+    if status:
+        _check(status, "kv_append")
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
+def _attention_ws_bytes(rows, head_dim, pairs, device):
+    return q4_workspace_bytes(Q4_OP_KV_ATTENTION, rows, head_dim, pairs)
+
+
 def kv_attention_ws(max_q, n_q, n_kv, head_dim, n_seqs, device):
-    n = q4_workspace_bytes(Q4_OP_KV_ATTENTION, max_q * (n_q // n_kv), head_dim, n_seqs * n_kv)
+    device = torch.device(device)
+    n = _attention_ws_bytes(max_q * (n_q // n_kv), head_dim, n_seqs * n_kv, device.index)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
@@ -667,29 +696,48 @@ def kv_attention(q, k_cache, v_cache, block_table, cu_tokens, kv_lens, max_q=Non
     the new tokens of a sequence (None: T); scale None: 1/sqrt(D); window: how
     many positions a token sees (0: all); lse: f32 [T, n_q] to fill, or None."""
     lib = load()
-    cache = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
+    cache, dtype, n_kv, D, n_seqs = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
     if q.dim() != 3:
         raise Q4Error(f"q has shape {tuple(q.shape)}; [T, n_q, head_dim] is wanted")
-    T, n_q, D = q.shape[0], q.shape[1], cache.head_dim
+    T, n_q, _ = q.shape
     if T == 0:
         return (torch.empty_like(q) if out is None else out), lse
-    qs = _heads(q, k_cache.dtype, n_q, D, T, "q")
+    qs = _heads(q, dtype, n_q, D, T, "q")
     if out is None:
-        out = torch.empty((T, n_q, D), dtype=q.dtype, device=q.device)
-    _dev(out, k_cache.dtype, "out")
-    _dev(lse, torch.float32, "lse")
-    _dev(err, torch.int32, "err")
-    _dev(ws, torch.uint8, "ws")
-    _numel(out, T * n_q * D, "out")
-    _numel(lse, T * n_q, "lse")
-    max_q = T if max_q is None else max_q
-    if n_q < 1 or n_q % cache.n_kv:
-        raise Q4Error(f"n_q={n_q} must be a multiple of n_kv={cache.n_kv}")
+        out = torch.empty((T, n_q, D), dtype=dtype, device=q.device)
+    else:
+        _dev(out, dtype, "out")
+        _numel(out, T * n_q * D, "out")
+    lse_ptr = None
+    if lse is not None:
+        _dev(lse, torch.float32, "lse")
+        _numel(lse, T * n_q, "lse")
+        lse_ptr = lse.data_ptr()
+    if err is not None:
+        _dev(err, torch.int32, "err")
+    if max_q is None:
+        max_q = T
+    if n_q < 1 or n_q % n_kv:
+        raise Q4Error(f"n_q={n_q} must be a multiple of n_kv={n_kv}")
     if ws is None:
-        ws = kv_attention_ws(max_q, n_q, cache.n_kv, D, cache.n_seqs, q.device)
-    _check(lib.kv_attention(ctypes.byref(cache), T, max_q, _ptr(q), qs, n_q, D ** -0.5 if scale is None else scale,
-                            window, _ptr(out), _ptr(lse), _ptr(err), _ptr(ws), ws.numel(), _stream()), "kv_attention")
+        ws = kv_attention_ws(max_q, n_q, n_kv, D, n_seqs, q.device)
+    else:
+        _dev(ws, torch.uint8, "ws")
+    status = lib.kv_attention(cache, T, max_q, q.data_ptr(), qs, n_q, D ** -0.5 if scale is None else scale, window,
+                              out.data_ptr(), lse_ptr, _ptr(err), ws.data_ptr(), ws.numel(), _stream())
+    if status:
+        _check(status, "kv_attention")
     return out, lse
+
+
+def _row_setting(t, dtype, b, name):
+    """Pointer of a per-row array of b values, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not _here(t) or t.shape != (b,) or not t.is_contiguous():
+        _dev(t, dtype, name)
+        _numel(t, b, name)
+    return t.data_ptr()
 
 
 def logits_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprobs=None):
@@ -697,26 +745,29 @@ def logits_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
     random numbers u [b] in [0, 1): returns (tokens int32 [b], logprobs f32 [b]).
     temperature, top_p, min_p: f32 [b]; top_k: int32 [b]; None turns one off."""
     lib = load()
-    if logits.dim() != 2 or logits.dtype not in _DTYPES:
-        raise Q4Error(f"logits must be [b, V] of float32, float16 or bfloat16, got {tuple(logits.shape)} {logits.dtype}")
+    dtype = logits.dtype
+    if logits.dim() != 2 or dtype not in _DTYPES:
+        raise Q4Error(f"logits must be [b, V] of float32, float16 or bfloat16, got {tuple(logits.shape)} {dtype}")
     b, V = logits.shape
-    tokens = torch.empty(b, dtype=torch.int32, device=logits.device) if tokens is None else tokens
-    logprobs = torch.empty(b, dtype=torch.float32, device=logits.device) if logprobs is None else logprobs
+    f32, i32 = torch.float32, torch.int32
+    if tokens is None:
+        tokens = torch.empty(b, dtype=i32, device=logits.device)
+    if logprobs is None:
+        logprobs = torch.empty(b, dtype=f32, device=logits.device)
     if b == 0:
         return tokens, logprobs
     if not _here(logits):
-        _dev(logits[:0], logits.dtype, "logits")   # names the fault
-    if V > 1 and logits.stride(1) != 1:
-        raise Q4Error(f"a row of logits must be contiguous, the strides are {tuple(logits.stride())}")
-    for t, dt, nm in ((u, torch.float32, "u"), (temperature, torch.float32, "temperature"),
-                      (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"),
-                      (min_p, torch.float32, "min_p"), (tokens, torch.int32, "tokens"),
-                      (logprobs, torch.float32, "logprobs")):
-        _dev(t, dt, nm)
-        _numel(t, b, nm)
-    _check(lib.logits_sample(_ptr(logits), logits.stride(0) if b > 1 else V, _DTYPES[logits.dtype], b, V, _ptr(u),
-                             _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens), _ptr(logprobs),
-                             _stream()), "logits_sample")
+        _dev(logits[:0], dtype, "logits")   # names the fault
+    rs, es = logits.stride()
+    if V > 1 and es != 1:
+        raise Q4Error(f"a row of logits must be contiguous, the strides are {(rs, es)}")
+    status = lib.logits_sample(logits.data_ptr(), rs if b > 1 else V, _DTYPES[dtype], b, V,
+                               _row_setting(u, f32, b, "u"), _row_setting(temperature, f32, b, "temperature"),
+                               _row_setting(top_k, i32, b, "top_k"), _row_setting(top_p, f32, b, "top_p"),
+                               _row_setting(min_p, f32, b, "min_p"), _row_setting(tokens, i32, b, "tokens"),
+                               _row_setting(logprobs, f32, b, "logprobs"), _stream())
+    if status:
+        _check(status, "logits_sample")
     return tokens, logprobs
 
 

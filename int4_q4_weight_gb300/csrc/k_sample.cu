@@ -937,19 +937,21 @@ int launch_logits_sample(const void* z, long long stride, int dtype, int rows, i
                          const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                          int32_t* token, float* logprob, const DeviceInfo& dev, cudaStream_t s) {
   sample::Params p = {z, stride, u, temperature, top_k, top_p, min_p, token, logprob, V, 0};
-  // CTAs per row: while the rows leave SMs free, eight (a row's time is what
-  // counts); with many rows fewer, as every phase that one CTA runs alone and
-  // every cluster barrier idles the others.  Not more indices per CTA than a
-  // 32-bit bin holds, nor CTAs for a few thousand indices.
-  int cluster = 8;
-  while (cluster > 1 && rows * cluster > 2 * dev.sms) cluster >>= 1;
+  // CTAs per row.  Few rows: eight, one CTA per SM with its part of the row in
+  // registers (a cluster lies in one GPC, so not every SM can be used; 8 rows of
+  // 262144: 15.9 us for top-64, 55 us for top-p, against 22 and 74 with four
+  // that read again).  More: four, two CTAs per SM that read the row again from
+  // L2: every phase that one CTA runs alone idles fewer (16 rows: 23 us against
+  // 27; 192 rows: 95 us, with eight 122, with two, whose rows together exceed L2,
+  // 124).  Not more indices per CTA than a 32-bit bin holds, nor CTAs for a few
+  // thousand indices.
+  const bool few = rows * 8 <= dev.sms * 2 / 3;
+  int cluster = few ? 8 : 4;
   while (cluster > 1 && V <= 2048 * cluster) cluster >>= 1;
   while (V > cluster * sample::kSeg * sample::kMaxSegs) cluster <<= 1;
   const int segs = (V + sample::kSeg * cluster - 1) / (sample::kSeg * cluster);
   p.range = segs * sample::kSeg;
-  // Few rows: one CTA per SM with its part of the row in registers.  Many: two
-  // CTAs per SM that read it again from L2.
-  const bool keep = p.range <= sample::kKeep * sample::kThr && rows * cluster <= dev.sms;
+  const bool keep = few && p.range <= sample::kKeep * sample::kThr;
   return dtype == Q4_F32   ? sample::launch<float>(p, rows, cluster, keep, s)
          : dtype == Q4_F16 ? sample::launch<__half>(p, rows, cluster, keep, s)
                            : sample::launch<__nv_bfloat16>(p, rows, cluster, keep, s);
