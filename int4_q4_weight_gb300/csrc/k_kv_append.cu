@@ -13,7 +13,9 @@
 // Bound: HBM (every input element is read and every output written once); at
 // decode sizes the launch.  A thread owns 16 elements of a row (eight pairs):
 // the eight sines and cosines are formed once and used for every row (head)
-// of the token that the thread takes.
+// of the token that the thread takes.  The rows are loaded one ahead, the first
+// before the position is looked up: those lookups are three loads one after the
+// other, and while they run nothing else would be in flight.
 #include "q4w_device.cuh"
 #include "q4w_internal.cuh"
 #include "q4w_kv.cuh"
@@ -21,7 +23,7 @@
 namespace q4w {
 namespace append {
 
-constexpr int kThr = 256;
+constexpr int kThr = 128;
 constexpr int kChunk = 16;   // elements of a row per thread: eight pairs
 
 struct Params {
@@ -36,22 +38,36 @@ struct Params {
   int rows, groups, rows_per_group;          // rows: n_q + 2 n_kv heads of a token
 };
 
-// Eight consecutive elements as fp32.
+// 16 bytes of an input: read once, and never written by this kernel, so the loads
+// of the next rows may pass the stores of the last.
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 r;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+// Eight consecutive elements, as loaded and as fp32.
 template <typename IN>
-__device__ __forceinline__ void load8(const IN* p, float (&x)[8]) {
-  if constexpr (sizeof(IN) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Eight {
+  uint4 w[sizeof(IN) / 2];
+  __device__ __forceinline__ void load(const IN* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = Half16<IN>::unpack(w[i]);
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    for (int i = 0; i < (int)sizeof(IN) / 2; ++i) w[i] = ld16(p + 4 * i);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t* u = &w[0].x;
+    if constexpr (sizeof(IN) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = Half16<IN>::unpack(u[i]);
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+      }
     }
   }
-}
+};
 
 template <typename OUT>
 __device__ __forceinline__ void store8(OUT* p, const float (&x)[8]) {
@@ -69,6 +85,22 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Pa
   const long long tg = idx / chunks;
   const int grp = (int)(tg % p.groups);
   const int tok = (int)min(tg / p.groups, (long long)p.T);   // T: past the end
+  // where the thread's two halves of eight elements lie in a row
+  const bool rotates = c < p.rot / kChunk;
+  const int lo = rotates && !p.interleaved ? c * 8 : c * kChunk;
+  const int hi = rotates && !p.interleaved ? lo + p.rot / 2 : lo + 8;
+  const int r0 = grp * p.rows_per_group, r1 = min(r0 + p.rows_per_group, p.rows);
+  auto source = [&](int r) {
+    if (r < p.n_q) return static_cast<const IN*>(p.q) + tok * p.q_stride + (long long)r * p.D;
+    r -= p.n_q;
+    if (r < p.kv.n_kv) return static_cast<const IN*>(p.k) + tok * p.k_stride + (long long)r * p.D;
+    return static_cast<const IN*>(p.v) + tok * p.v_stride + (long long)(r - p.kv.n_kv) * p.D;
+  };
+  Eight<IN> na, nb;   // the next row's
+  if (tok < p.T) {
+    na.load(source(r0) + lo);
+    nb.load(source(r0) + hi);
+  }
   // the sequence of this block's first token: how many sequences end at or
   // before it (counted by all threads; a thread's own token is a few further)
   if (threadIdx.x == 0) first_sh = 0;
@@ -91,14 +123,8 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Pa
   const bool stored = page >= 0;
   if (!stored && c == 0 && p.err) *p.err = 1;
 
-  // where the thread's two halves of eight elements lie in a row
-  int lo, hi;
-  const int rot_chunks = p.rot / kChunk;
-  const bool rotates = c < rot_chunks;
   float cs[8], sn[8];
   if (rotates) {
-    lo = p.interleaved ? c * kChunk : c * 8;
-    hi = p.interleaved ? lo + 8 : lo + p.rot / 2;
     const long long at = p.positions ? p.positions[tok] : pos;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -106,32 +132,26 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Pa
       // the upper 32 bits as a signed fraction of a half turn
       sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn[i], &cs[i]);
     }
-  } else {
-    lo = c * kChunk, hi = lo + 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
   }
 
-  const int r0 = grp * p.rows_per_group, r1 = min(r0 + p.rows_per_group, p.rows);
-#pragma unroll 2
+#pragma unroll 1
   for (int r = r0; r < r1; ++r) {
-    const IN* src;
+    float a[8], b[8];
+    na.get(a);
+    nb.get(b);
+    if (r + 1 < r1) {
+      na.load(source(r + 1) + lo);
+      nb.load(source(r + 1) + hi);
+    }
     OUT* dst;
     const bool is_q = r < p.n_q, is_k = !is_q && r < p.n_q + p.kv.n_kv;
     if (is_q) {
-      src = static_cast<const IN*>(p.q) + tok * p.q_stride + (long long)r * p.D;
       dst = static_cast<OUT*>(p.q_out) + ((long long)tok * p.n_q + r) * p.D;
     } else {
       if (!stored) continue;
       const int h = is_k ? r - p.n_q : r - p.n_q - p.kv.n_kv;
-      src = is_k ? static_cast<const IN*>(p.k) + tok * p.k_stride + (long long)h * p.D
-                 : static_cast<const IN*>(p.v) + tok * p.v_stride + (long long)h * p.D;
-      dst = static_cast<OUT*>(is_k ? p.k_cache : p.v_cache) +
-            (kv_row(p.kv, page, h) + pos % p.kv.page_size) * p.D;
+      dst = static_cast<OUT*>(is_k ? p.k_cache : p.v_cache) + (kv_row(p.kv, page, h) + pos % p.kv.page_size) * p.D;
     }
-    float a[8], b[8];
-    load8(src + lo, a);
-    load8(src + hi, b);
     if (rotates && (is_q || is_k)) {
       if (p.interleaved) {
         float x[16];
