@@ -14,8 +14,10 @@
 //   O^T[D][8 rows]        += V^T[D][16] P^T       (V by transposing ldmatrix)
 // P^T is S^T's own registers after a transposition of 8x8 blocks in registers.
 // Every warp streams its own units of 16 keys (K, then V) through a private
-// ring of TMA boxes in the 128-byte swizzle and synchronises with no other warp
-// until its CTA's part of the keys is done; 192 KB are in flight on an SM.
+// ring by 16-byte asynchronous copies, which place the 128-byte swizzle and leave
+// zeros for rows that nothing may see, and synchronises with no other warp until
+// its CTA's part of the keys is done; 192 KB are in flight on an SM.  (TMA boxes
+// of 16 rows moved 17 bytes a cycle and SM at head size 128, where HBM gives 23.)
 //
 // Split: one CTA per SM.  The steps (one unit per warp) of all (sequence, KV
 // head) pairs form one line that is cut into equal shares, so ragged lengths
@@ -28,7 +30,6 @@
 #include "q4w_attn.cuh"
 #include "q4w_device.cuh"
 #include "q4w_internal.cuh"
-#include "q4w_tc.cuh"
 
 namespace q4w {
 namespace dec {
@@ -50,13 +51,9 @@ struct Shape {
 };
 
 struct Params {
-  CUtensorMap tm_k, tm_v;
   AttnParams a;
   AttnSplit split;
-  unsigned* dev_err;
-  long long wait_limit;
   int group;             // query heads per KV head
-  int total_rows;        // of the cache
   int grid;
 };
 
@@ -66,6 +63,10 @@ __device__ __forceinline__ int steps_of(const Seq& s) {
 }
 
 // ------------------------------------------------------------ instructions ---
+// 16 bytes from global to shared memory, zeros where `in` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -127,17 +128,13 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float* merge = reinterpret_cast<float*>(ring + kRingBytes);
-  __shared__ uint64_t bars[W * SLOTS];
   __shared__ float2 ml_sh[W][8 * NT];
   __shared__ long long scan_sh[W];
   __shared__ int start_sh[3];
-  __shared__ int abort_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AttnParams& a = p.a;
 
-  for (int i = threadIdx.x; i < W * SLOTS; i += S::kThr) tc::mbar_init(tc::smem_u32(bars + i), 1);
-  if (threadIdx.x == 0) abort_sh = 0, start_sh[0] = a.kv.n_seqs;
-  tc::mbar_fence_init();
+  if (threadIdx.x == 0) start_sh[0] = a.kv.n_seqs;
   pdl_wait();
   pdl_trigger();
 
@@ -188,10 +185,7 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
   const int n_steps = (int)max(0ll, min(share, total - first_step));
   if (n_steps == 0) return;
 
-  const uint32_t ring0 = tc::smem_u32(ring) + warp * SLOTS * S::kSlotBytes;
-  const uint32_t bar0 = tc::smem_u32(bars) + warp * SLOTS * 8;
-  const uint64_t policy = tc::policy_evict_first();
-  bool dead = false;   // a wait ran out: nothing more is loaded or computed
+  const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + warp * SLOTS * S::kSlotBytes;
 
   Walk<S::kStep> lw;   // of the loads, ahead of the computation
   lw.seq = start_sh[0], lw.head = start_sh[1], lw.local = start_sh[2];
@@ -202,40 +196,56 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
   // lane (-1: a page that is none of the cache, -2: behind the end)
   int l_step = 0, l_half = 0;        // next load: step of the share, 0 = K, 1 = V
   int row_base = -32, rows = -2;
-  int l_row = 0;                     // the unit's row; total_rows, out of the cache, gives zeros
-  uint32_t l_slot = 0;               // loads issued
+  int l_row = 0;                     // the unit's first row
+  int l_slot = 0;                    // its slot
   uint32_t skip = 0;                 // per slot of K: nothing in it counts
+  // a lane's 16-byte pieces of a slot: piece c0 (and + 32 for D = 512) of rows
+  // r0, r0 + rows at once, ..
+  constexpr int PIECES = D / 8, LR = PIECES < 32 ? 32 / PIECES : 1, COPIES = kUnit * PIECES / 32;
+  const int r0 = PIECES < 32 ? lane / PIECES : 0, c0 = PIECES < 32 ? lane % PIECES : lane;
   auto issue = [&]() {
-    if (l_step >= n_steps || dead) return;
-    const int slot = (int)(l_slot % SLOTS);
-    if (l_half == 0) {
-      if (lw.local < row_base || lw.local >= row_base + 32) {
-        row_base = lw.local;
-        const int pos = lw.s.base + ((row_base + lane) * W + warp) * kUnit;
-        rows = -2;
-        if (pos < lw.s.end) {
-          const int page = kv_page(a.kv, lw.seq, pos);
-          rows = page < 0 ? -1 : (int)kv_row(a.kv, page, lw.head) + pos % a.kv.page_size;
-          if (page < 0 && a.err) *a.err = 1;
+    if (l_step < n_steps) {
+      const int k0 = lw.s.base + (lw.local * W + warp) * kUnit;
+      if (l_half == 0) {
+        if (lw.local < row_base || lw.local >= row_base + 32) {
+          row_base = lw.local;
+          const int pos = lw.s.base + ((row_base + lane) * W + warp) * kUnit;
+          rows = -2;
+          if (pos < lw.s.end) {
+            const int page = kv_page(a.kv, lw.seq, pos);
+            rows = page < 0 ? -1 : (int)kv_row(a.kv, page, lw.head) + pos % a.kv.page_size;
+            if (page < 0 && a.err) *a.err = 1;
+          }
         }
+        l_row = __shfl_sync(0xffffffffu, rows, lw.local - row_base);
+        skip = l_row < 0 ? skip | (1u << l_slot) : skip & ~(1u << l_slot);
       }
-      const int row = __shfl_sync(0xffffffffu, rows, lw.local - row_base);
-      l_row = row < 0 ? p.total_rows : row;
-      skip = row < 0 ? skip | (1u << slot) : skip & ~(1u << slot);
+      // rows that a token may see; what lies in the others may be anything, and 0
+      // times infinity is no zero
+      const int lo = l_row < 0 ? kUnit : kv_first(lw.s.pos0, a.window) - k0, hi = lw.s.end - k0;
+      const T* src = static_cast<const T*>(l_half ? a.v : a.k) + (long long)max(l_row, 0) * D + (r0 * D + c0 * 8);
+      const uint32_t dst = ring0 + l_slot * S::kSlotBytes;
+#pragma unroll
+      for (int i = 0; i < COPIES; ++i) {
+        const int r = PIECES <= 32 ? r0 + i * LR : i >> 1, c = PIECES <= 32 ? c0 : c0 + 32 * (i & 1);
+        copy16(dst + (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + (PIECES <= 32 ? i * LR * D : (i >> 1) * D + (i & 1) * 256),
+               r >= lo && r < hi);
+      }
+      l_slot = l_slot + 1 == SLOTS ? 0 : l_slot + 1;
+      if (l_half) {
+        l_half = 0;
+        ++l_step;
+        if (l_step < n_steps && lw.next(a)) row_base = -32;
+      } else {
+        l_half = 1;
+      }
     }
-    if (lane == 0) {
-      const uint32_t bar = bar0 + 8 * slot;
-      tc::mbar_expect_tx(bar, S::kSlotBytes);
-      tc::tma_load_3d(ring0 + slot * S::kSlotBytes, l_half ? &p.tm_v : &p.tm_k, 0, l_row, 0, bar, policy);
-    }
-    ++l_slot;
-    if (l_half) {
-      l_half = 0;
-      ++l_step;
-      if (l_step < n_steps && lw.next(a)) row_base = -32;
-    } else {
-      l_half = 1;
-    }
+    asm volatile("cp.async.commit_group;" ::: "memory");   // an empty one behind the last
+  };
+  // SLOTS groups are in flight; the oldest has landed, for every lane
+  auto landed = [&]() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+    __syncwarp();
   };
   for (int i = 0; i < SLOTS; ++i) issue();
 
@@ -268,22 +278,19 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
   };
   begin();
 
-  uint32_t c_slot = 0;   // slots consumed
+  int c_slot = 0;   // next slot to consume
   bool opens = cw.local == 0;
   for (int step = 0; step < n_steps; ++step) {
     // ------------------------------------------------ one unit of 16 keys
     const int k0 = cw.s.base + (cw.local * W + warp) * kUnit;
-    const uint32_t k_slot = c_slot % SLOTS;
-    const uint32_t ks = ring0 + k_slot * S::kSlotBytes, kb = bar0 + 8 * k_slot;
-    const uint32_t kpar = (c_slot / SLOTS) & 1;
-    ++c_slot;
-    const uint32_t vs = ring0 + (c_slot % SLOTS) * S::kSlotBytes, vb = bar0 + 8 * (c_slot % SLOTS);
-    const uint32_t vpar = (c_slot / SLOTS) & 1;
-    ++c_slot;
-    const bool valid = !((skip >> k_slot) & 1);
-    if (!dead) dead = !__all_sync(0xffffffffu, tc::mbar_wait(kb, kpar, p.wait_limit, &abort_sh, p.dev_err));
+    const uint32_t ks = ring0 + c_slot * S::kSlotBytes;
+    const bool valid = !((skip >> c_slot) & 1);
+    c_slot = c_slot + 1 == SLOTS ? 0 : c_slot + 1;
+    const uint32_t vs = ring0 + c_slot * S::kSlotBytes;
+    c_slot = c_slot + 1 == SLOTS ? 0 : c_slot + 1;
+    landed();
     float s[NT][4];
-    if (valid && !dead) {
+    if (valid) {
       float acc[NT][2][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -308,7 +315,7 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
     __syncwarp();
     issue();   // into the slot of K
     uint32_t pf[NT][2];
-    if (valid && !dead) {
+    if (valid) {
       // masks: only units at the ends of what the tokens see
       const int last = cw.s.pos0 + cw.s.n - 1;
       if (k0 + kUnit - 1 > cw.s.pos0 || k0 < kv_first(last, a.window) || k0 + kUnit > cw.s.end) {
@@ -360,19 +367,8 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
         pf[t][1] = transpose8(Half16<T>::pack(e2, e3));
       }
     }
-    if (!dead) dead = !__all_sync(0xffffffffu, tc::mbar_wait(vb, vpar, p.wait_limit, &abort_sh, p.dev_err));
-    if (valid && !dead) {
-      // what no token sees may be anything, and 0 times infinity is no zero
-      const int see0 = kv_first(cw.s.pos0, a.window);
-      if (k0 < see0 || k0 + kUnit > cw.s.end) {
-        for (int i = lane; i < kUnit * SLABS * 8; i += 32) {
-          const int r = (i >> 3) & 15, c = k0 + r;
-          if (c < see0 || c >= cw.s.end)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs + i * 16), "r"(0) : "memory");
-        }
-        tc::fence_proxy_async();   // before the slot's next load
-        __syncwarp();
-      }
+    landed();
+    if (valid) {
       const int row = (lane & 7) + ((lane >> 4) << 3);
       const uint32_t rbase = vs + row * 128;
 #pragma unroll
@@ -485,10 +481,6 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
       begin();
     }
   }
-  if (dead) {   // what is in flight lands before the CTA leaves
-    for (uint32_t q = l_slot > (uint32_t)SLOTS ? l_slot - SLOTS : 0u; q < l_slot; ++q)
-      tc::mbar_drain(bar0 + 8 * (q % SLOTS), (q / SLOTS) & 1, 2000000000LL, p.dev_err);
-  }
 }
 
 template <typename T, int D, int NT>
@@ -542,17 +534,10 @@ size_t attn_decode_ws_bytes(int max_rows, int D, const DeviceInfo& dev) {
 int launch_attn_decode(const AttnParams& a, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s) {
   dec::Params p = {};
   const bool bf16 = c.dtype == Q4_BF16;
-  const uint64_t rows = (uint64_t)c.n_pages * c.n_kv * c.page_size;
-  int st = encode_cache_rows(&p.tm_k, c.k, bf16, c.head_dim, rows, dec::kUnit, c.head_dim / 64, "the K cache");
-  if (st == Q4_OK) st = encode_cache_rows(&p.tm_v, c.v, bf16, c.head_dim, rows, dec::kUnit, c.head_dim / 64, "the V cache");
-  if (st != Q4_OK) return st;
   p.a = a;
   p.group = a.n_q / c.n_kv;
   const int nt = dec::nt_of(a.max_q * p.group);
   p.grid = dev.sms;
-  p.total_rows = (int)rows;
-  p.wait_limit = wait_limit();
-  p.dev_err = device_error_word();
   p.split = attn_split(ws, p.grid, 8 * nt, c.head_dim);
   return bf16 ? dec::launch_t<__nv_bfloat16>(p, c.head_dim, nt, dev, s)
               : dec::launch_t<__half>(p, c.head_dim, nt, dev, s);
