@@ -19,7 +19,7 @@ __device__ __forceinline__ int join_groups(int parts, int used, int dv) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n_recs, int n_q, int rows, int D, int dv,
+__global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n_recs, int R, int n_q, int rows, int D, int dv,
                                                         void* out_, float* lse) {
   __shared__ float4 sum_sh[kJoinThr];
   __shared__ float2 ml_sh[16][8];
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
     if (threadIdx.x < n_recs) {
       const SplitRec r = p.recs[threadIdx.x];
       rec_sh[threadIdx.x] = r;
-      n = r.last < 0 ? 0 : (r.used + 7) / 8 * (dv * join_groups(r.last - (int)threadIdx.x + 1, r.used, dv) / 256);
+      n = r.last < 0 ? 0 : (r.used + 7) / 8 * (dv * join_groups(r.last - (int)threadIdx.x / R + 1, r.used, dv) / 256);
     }
     int incl = n;
 #pragma unroll
@@ -58,12 +58,12 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
       if (first_sh[mid] <= task) lo = mid; else hi = mid;
     }
     const SplitRec rec = rec_sh[lo];
-    const int c0 = lo, sub = task - first_sh[lo], np = rec.last - c0 + 1;
+    const int c0 = lo / R, sub = task - first_sh[lo], np = rec.last - c0 + 1;
     const int groups = join_groups(np, rec.used, dv), quads = 64 / groups, col_tasks = dv * groups / 256;
     const int part = (threadIdx.x >> 3) / quads, dl = (threadIdx.x >> 3) % quads, d = (sub % col_tasks * quads + dl) * 4;
     const int lr = sub / col_tasks * 8 + rr;
     const bool in = lr < rec.used;
-    auto slot = [&](int i) { return i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i); };
+    auto slot = [&](int i) { return (i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i)) * R + lo % R; };
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f, m = -CUDART_INF_F;
     if (in) {
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
 
 }  // namespace attn
 
-int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int D, int dv, bool bf16, int grid,
+int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int D, int dv, bool bf16, int grid, int R,
                      cudaStream_t s) {
   if (grid > attn::kJoinThr) return fail(Q4_ERR_SHAPE, "attention: %d SMs are more than the join handles", grid);
   cudaLaunchConfig_t cfg = {};
@@ -127,8 +127,8 @@ int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int 
   cfg.attrs = at;
   cfg.numAttrs = 1;
   const cudaError_t e =
-      bf16 ? cudaLaunchKernelEx(&cfg, attn::join_kernel<__nv_bfloat16>, split, grid, a.n_q, rows, D, dv, a.out, a.lse)
-           : cudaLaunchKernelEx(&cfg, attn::join_kernel<__half>, split, grid, a.n_q, rows, D, dv, a.out, a.lse);
+      bf16 ? cudaLaunchKernelEx(&cfg, attn::join_kernel<__nv_bfloat16>, split, grid, R, a.n_q, rows, D, dv, a.out, a.lse)
+           : cudaLaunchKernelEx(&cfg, attn::join_kernel<__half>, split, grid, R, a.n_q, rows, D, dv, a.out, a.lse);
   return e == cudaSuccess ? Q4_OK : cuda_fail(e, "attention join launch");
 }
 

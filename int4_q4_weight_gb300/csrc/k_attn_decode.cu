@@ -505,7 +505,7 @@ static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, D, NT>, p);
   if (e != cudaSuccess) return cuda_fail(e, "decode attention launch");
-  return launch_attn_join(p.a, p.split, 8 * NT, D, D, std::is_same<T, __nv_bfloat16>::value, p.grid, s);
+  return launch_attn_join(p.a, p.split, 8 * NT, D, D, std::is_same<T, __nv_bfloat16>::value, p.grid, 1, s);
 }
 
 // The largest NT: registers hold NT (D/8 + D/4) values of Q and O.

@@ -15,15 +15,25 @@
 // not fit: its two column halves of O are items of their own, which form the
 // scores twice (1.5 times the products).
 //
+// Two CTAs, a cluster, take the two tiles of a pair as one (cta_group::2): an MMA
+// of 256 rows takes Q, P and the accumulators of each CTA's 128 rows from that
+// CTA, and half of the keys of K (of the columns of V) from each.  Alone, a CTA
+// is bound by its shared memory at head size 256: a step's products read 128 KB
+// for QK^T and 64 KB for PV, and 128 KB of K and V are written, 2560 cycles at 128
+// bytes a cycle against 2048 of products, and 3450 were measured, also when the
+// two CTAs shared their loads by multicast.  As a pair it is 96, 32 and 64 KB, and
+// the rings hold two and a half steps.
+//
 // Warps: 0-7 softmax (warp w the rows 32 (w mod 4) .., keys 64 (w div 4) ..), 8
-// issues the MMAs, 9 and 10 the loads of K and of V, 11 those of the next item's
+// issues the MMAs in the even CTA, and in the odd one passes on to it that slots
+// have landed, 9 and 10 the loads of K and of V, 11 those of the next item's
 // query rows (a box of whole tokens: a tile has floor(128 / group) of them).
 // The softmax is written to be short: a path that is taken once per item and
 // unrolled to hundreds of instructions cost 20000 cycles of instruction fetches.
 // K and V have a ring of slots each, so that the next keys load while the values
-// wait for P: K slots of [128 keys][64 or 128 dims], V slots of [64 or 128
-// keys][DV], loaded in boxes of 16 to 64 rows (the page size's share), 128-byte
-// swizzle.
+// wait for P: K slots of [64 keys][<= 128 dims], V slots of [64 or 128 keys][128
+// or 64 columns], loaded in boxes of 16 to 64 rows (the page size's share),
+// 128-byte swizzle.
 //
 // Split: the steps of all items (sequence, KV head, tile) form one line that is
 // cut into equal shares, one CTA per SM; causal tiles of any length and ragged
@@ -43,24 +53,23 @@ constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = kSoftWarps, kKWarp = kMmaWarp + 1, kVWarp = kKWarp + 1, kQWarp = kVWarp + 1;
 constexpr int kThr = (kQWarp + 1) * 32;
 constexpr long long kDrainCycles = 2000000000LL;
+constexpr long long kShortDrainCycles = 4000000LL;   // aborting: copies in flight land well within this
 constexpr int kBadRing = 16;
 
 template <int D>
 struct Shape {
   static constexpr int kDV = D < 256 ? D : 256;              // columns of O of an item
   static constexpr int kParts = D / kDV;                     // items per tile
-  static constexpr int kKD = D == 128 || D == 256 ? 128 : 64;   // dims of a K slot
+  static constexpr int kN = D == 64 ? 128 : kDV;             // columns of the MMA (D = 64: the odd CTA's are zeros)
+  static constexpr int kKD = D < 256 ? D : 256;              // dims of a K slot
   static constexpr int kNK = D / kKD;                        // K slots per step
-  static constexpr int kKSlot = kKeys * kKD * 2;             // bytes: 32 KB, 16 KB for D = 64 and 512
-  static constexpr int kVSlot = D == 64 ? 16384 : 32768;
-  static constexpr int kVK = kVSlot / (kDV * 2);             // keys of a V slot: 128, 128, 64, 64
-  static constexpr int kNV = kKeys / kVK;                    // V slots per step
+  static constexpr int kKSlot = kKeys / 2 * kKD * 2;         // bytes: 8, 16, 32, 32 KB
+  static constexpr int kVSlot = kKeys * kN;                  // all keys of a step, kN / 2 columns a CTA: 16, 16, 32, 32 KB
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kKSlots = D == 64 ? 6 : D == 128 ? 3 : 2;   // rings of K and of V
-  static constexpr int kVSlots = D == 64 ? 6 : D <= 256 ? 3 : 2;   // all of a step's: its rows are cleared together
-  static_assert(kVSlots >= kNV, "the softmax waits for a whole step of V");
+  static constexpr int kKSlots = D <= 128 ? 6 : 2;           // rings of K and of V
+  static constexpr int kVSlots = D <= 128 ? 6 : D == 256 ? 3 : 1;
   static constexpr int kRing = kKSlots * kKSlot + kVSlots * kVSlot;
-  static_assert(kVK >= 64, "a slot of V holds the largest box");
+  static_assert(kQBytes + kRing <= 229376, "shared memory");
   static constexpr size_t kSmem = kQBytes + kRing;   // with the static part, all 227 KB
 };
 
@@ -70,12 +79,13 @@ struct Params {
   AttnSplit split;
   unsigned* dev_err;
   long long wait_limit;
-  int group, tokens;     // query heads per KV head, tokens of a tile
-  int total_rows, grid;
+  int group, tokens;     // query heads per KV head, tokens of a tile (a pair has twice as many)
+  int total_rows, pairs; // pairs: of CTAs
   int box;               // rows of a TMA box: 16, 32 or 64, a divisor of the page size
 };
 
-// Keys that tile t of a sequence sees: [base, end), and its steps.
+// Keys that pair t of tiles of a sequence sees: [base, end), and its steps;
+// `tokens`: of a pair.
 struct Span {
   int lo, base, end, steps;   // lo: the first key that its first token sees
 };
@@ -99,7 +109,7 @@ struct Walk {
   Span x;
 };
 template <int PARTS>
-__device__ __forceinline__ void walk_item(Walk& w, const Params& p) { w.x = span_of(p.a, w.s, p.tokens, w.t, p.box); }
+__device__ __forceinline__ void walk_item(Walk& w, const Params& p) { w.x = span_of(p.a, w.s, 2 * p.tokens, w.t, p.box); }
 // To the next item (the caller knows that there is one).
 template <int PARTS>
 __device__ __forceinline__ void walk_next(Walk& w, const Params& p) {
@@ -114,7 +124,7 @@ __device__ __forceinline__ void walk_next(Walk& w, const Params& p) {
           ++w.seq;
           if (w.seq >= p.a.kv.n_seqs) return;
           w.s = seq_of(p.a, w.seq, p.box);
-          w.n_tiles = tiles_of(w.s, p.tokens);
+          w.n_tiles = tiles_of(w.s, 2 * p.tokens);
         } while (w.n_tiles == 0);
       }
     }
@@ -123,22 +133,22 @@ __device__ __forceinline__ void walk_next(Walk& w, const Params& p) {
 }
 
 // Instruction descriptor, kind::f16: fp32 accumulators, A and B of one 16-bit
-// type, M = 128, N = n; bit 16: B is MN-major (its N index is the contiguous one).
+// type, M = 256 (both CTAs' rows), N = n; bit 16: B is MN-major (its N index is the contiguous one).
 __host__ __device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(2 * kRows >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(accum)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(accum)
       : "memory");
 }
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     return;
   }
   uint8_t* ring = smem + S::kQBytes;
-  __shared__ uint64_t bars[2 * NS + 8];
+  __shared__ uint64_t bars[2 * NS + 7];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   __shared__ int start_sh[6];
@@ -169,22 +179,25 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
   __shared__ uint32_t bad_sh[kBadRing];   // per step: boxes whose page is none of the cache
   __shared__ float row_sh[2][2][kRows];   // per half of the keys: the rows' maxima of a step, their sums of an item
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair = blockIdx.x >> 1, rank = blockIdx.x & 1;   // clusters of two along x
   const AttnParams& a = p.a;
   const uint32_t full0 = tc::smem_u32(bars), empty0 = full0 + 8 * NS;
   const uint32_t qfull = empty0 + 8 * NS, qempty = qfull + 8, sfull0 = qempty + 8, pready0 = sfull0 + 16,
-                 odone = pready0 + 16, drain = odone + 8;
+                 drain = pready0 + 16;
   volatile int* abort_flag = &abort_sh;
 
   if (warp == 0) {
     if (lane == 0) abort_sh = 0, start_sh[0] = -1;
-    if (lane < 2 * NS + 8) {
+    if (lane < 2 * NS + 7) {
       unsigned count = 1;
-      if (lane == 2 * NS + 4 || lane == 2 * NS + 5) count = kSoftWarps;  // pready
+      // the even CTA's barriers for what its MMAs wait for count both CTAs
+      if (rank == 0 && (lane < NS || lane == 2 * NS)) count = 2;                                 // full, qfull
+      if (lane == 2 * NS + 4 || lane == 2 * NS + 5) count = rank == 0 ? 2 * kSoftWarps : 1;      // pready
       tc::mbar_init(tc::smem_u32(bars + lane), count);
     }
     tc::mbar_fence_init();
   }
-  if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&tmem_sh), 512);
+  if (warp == kMmaWarp) tc::tmem_alloc_pair(tc::smem_u32(&tmem_sh), 512);
   pdl_wait();
   pdl_trigger();
 
@@ -195,9 +208,9 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     int* steps_sh = reinterpret_cast<int*>(ring);   // steps of one head and part of each sequence
     for (int q = warp; q < a.kv.n_seqs; q += kThr / 32) {
       const Seq s = seq_of(a, q, p.box);
-      const int nt = tiles_of(s, p.tokens);
+      const int nt = tiles_of(s, 2 * p.tokens);
       int sum = 0;
-      for (int t = lane; t < nt; t += 32) sum += span_of(a, s, p.tokens, t, p.box).steps;
+      for (int t = lane; t < nt; t += 32) sum += span_of(a, s, 2 * p.tokens, t, p.box).steps;
       sum = __reduce_add_sync(0xffffffffu, sum);
       if (lane == 0) {
         steps_sh[q] = sum;
@@ -225,8 +238,8 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       if (w < warp) before += scan_sh[w];
       total += scan_sh[w];
     }
-    share = (total + p.grid - 1) / p.grid;
-    const long long mine = share * blockIdx.x;
+    share = (total + p.pairs - 1) / p.pairs;
+    const long long mine = share * pair;
     if (sum > 0 && mine >= before && mine < before + sum) {
       long long left = mine - before;
       int q = q0;
@@ -241,17 +254,17 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     tc::fence_proxy_async();   // the sums' last use, before the ring's first loads
     __syncthreads();
   }
-  const long long first_step = share * blockIdx.x;
+  const long long first_step = share * pair;
   const int n_steps = start_sh[0] < 0 ? 0 : (int)max(0ll, min(share, total - first_step));
   Walk w = {};
   if (n_steps > 0) {
     // the tile: every warp scans the sequence's tiles, 32 at a time
     w.seq = start_sh[0], w.head = start_sh[1], w.part = start_sh[2];
     w.s = seq_of(a, w.seq, p.box);
-    w.n_tiles = tiles_of(w.s, p.tokens);
+    w.n_tiles = tiles_of(w.s, 2 * p.tokens);
     int left = start_sh[3];
     for (int t0 = 0;; t0 += 32) {
-      const int n = t0 + lane < w.n_tiles ? span_of(a, w.s, p.tokens, t0 + lane, p.box).steps : 0;
+      const int n = t0 + lane < w.n_tiles ? span_of(a, w.s, 2 * p.tokens, t0 + lane, p.box).steps : 0;
       int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -270,6 +283,10 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     walk_item<PARTS>(w, p);
   }
   tc::fence_before();
+  // both CTAs' barriers are initialised, and TMEM allocated, before either signals
+  // the other
+  tc::cluster_arrive_release();
+  tc::cluster_wait();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_sh;
@@ -282,7 +299,8 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     // ---------------------------------------------------------- TMA loads
     const bool is_k = warp == kKWarp;
     const uint64_t policy = tc::policy_evict_last();
-    const int nb = kKeys / p.box;
+    const int nb = kKeys / p.box;                // boxes of a step's keys
+    const int k_box0 = rank * (nb / 2);          // this CTA's half of them for K
     const int slots = is_k ? NKS : NVS, slot0 = is_k ? 0 : NKS, bytes = is_k ? S::kKSlot : S::kVSlot;
     const uint32_t base = is_k ? ring0 : v_ring0;
     int slot = 0;
@@ -321,7 +339,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
         if (mask && a.err) *a.err = 1;
       }
       __syncwarp();
-      const int n_slots = is_k ? S::kNK : S::kNV;
+      const int n_slots = is_k ? S::kNK : 1;
       for (int h = 0; h < n_slots; ++h) {
         const uint32_t full = full0 + 8 * (slot0 + slot), dst = base + slot * bytes;
         const bool f = tc::mbar_wait(empty0 + 8 * (slot0 + slot), (round & 1) ^ 1, p.wait_limit, abort_flag, p.dev_err);
@@ -333,29 +351,33 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
         __syncwarp();
         if (is_k) {
           constexpr int slabs = S::kKD / 64;
-          const int b = lane % nb, sl = lane / nb, r = __shfl_sync(0xffffffffu, row, b);
-          if (sl < slabs) tc::tma_load_3d(dst + sl * (kKeys * 128) + b * p.box * 128, &p.tm_k, 0, r, h * slabs + sl, full, policy);
+          const int b = lane % (nb / 2), sl = lane / (nb / 2), r = __shfl_sync(0xffffffffu, row, k_box0 + b);
+          if (sl < slabs) tc::tma_load_3d(dst + sl * (kKeys / 2 * 128) + b * p.box * 128, &p.tm_k, 0, r, h * slabs + sl, full, policy);
         } else {
-          constexpr int slabs = S::kDV / 64;
-          const int vb = S::kVK / p.box;   // boxes of the slot's keys
-          const int b = lane % vb, sl = lane / vb, r = __shfl_sync(0xffffffffu, row, h * vb + b);
+          constexpr int slabs = S::kN / 128;   // this CTA's half of the columns (D = 64: the odd CTA's lie outside)
+          const int b = lane % nb, sl = lane / nb, r = __shfl_sync(0xffffffffu, row, b);
           if (sl < slabs)
-            tc::tma_load_3d(dst + sl * (S::kVK * 128) + b * p.box * 128, &p.tm_v, 0, r, cur.part * slabs + sl, full, policy);
+            tc::tma_load_3d(dst + sl * (kKeys * 128) + b * p.box * 128, &p.tm_v, 0, r, (cur.part * 2 + rank) * slabs + sl, full, policy);
         }
         if (++slot == slots) slot = 0, ++round;
       }
     }
-    // what was issued lands before the CTA leaves: the slots of this round, and
-    // of the one before those not yet filled again
+    // Before the CTA leaves, what was issued has landed and been used (that signal
+    // may come from the other CTA): the slots of this round, and of the one before
+    // those not yet filled again.
     for (int i = 0; i < slots; ++i) {
       const bool again = i < slot;
-      if (again || round > 0)
-        tc::mbar_drain(full0 + 8 * (slot0 + i), (again ? round : round - 1) & 1, kDrainCycles, p.dev_err);
+      if (!again && round == 0) continue;
+      const uint32_t par = (again ? round : round - 1) & 1;
+      const long long lim = *abort_flag ? kShortDrainCycles : kDrainCycles;
+      tc::mbar_drain(full0 + 8 * (slot0 + i), par, lim, p.dev_err);
+      tc::mbar_drain(empty0 + 8 * (slot0 + i), par, lim, p.dev_err);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------- MMA issuer
-    constexpr uint32_t id_s = idesc(kKeys, BF16, false), id_o = idesc(S::kDV, BF16, true);
+    // The odd CTA's warp walks the same way and tells the even one what has landed.
+    constexpr uint32_t id_s = idesc(kKeys, BF16, false), id_o = idesc(S::kN, BF16, true);
     int ks = 0, vs = 0;                // slots
     uint32_t kround = 0, vround = 0;
     int item = 0;
@@ -363,51 +385,51 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     auto wait_all = [&](uint32_t bar, uint32_t par) {
       const bool f = tc::mbar_wait(bar, par, p.wait_limit, abort_flag, p.dev_err);
       ok = __all_sync(0xffffffffu, f);
+      if (ok && rank == 1 && lane == 0) tc::mbar_arrive_cluster(bar, 0);
       return ok;
     };
     auto scores = [&](int j, bool first, bool last) {
       if (first && !wait_all(qfull, item & 1)) return;
       for (int h = 0; h < S::kNK; ++h) {
-        const uint32_t slot = ks;
-        if (!wait_all(full0 + 8 * slot, kround & 1)) return;
-        tc::fence_after();
-        if (tc::elect_one()) {
-          const uint32_t kb = ring0 + slot * S::kKSlot, qb = q_addr + h * (S::kKD / 64) * (kRows * 128);
+        if (!wait_all(full0 + 8 * ks, kround & 1)) return;
+        if (rank == 0) {
+          tc::fence_after();
+          if (tc::elect_one()) {
+            const uint32_t kb = ring0 + ks * S::kKSlot, qb = q_addr + h * (S::kKD / 64) * (kRows * 128);
 #pragma unroll
-          for (int k = 0; k < S::kKD / 16; ++k) {
-            const uint32_t off = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
-            mma_ss(tmem + (j & 1) * 128, tc::desc_sw128(qb + off), tc::desc_sw128(kb + off), id_s, (h > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < S::kKD / 16; ++k)
+              mma_ss(tmem + (j & 1) * 128, tc::desc_sw128(qb + (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                     tc::desc_sw128(kb + (k >> 2) * (kKeys / 2 * 128) + (k & 3) * 32), id_s, (h > 0 || k > 0) ? 1u : 0u);
+            tc::commit_pair(empty0 + 8 * ks);
           }
-          tc::commit(empty0 + 8 * slot);
+          __syncwarp();
         }
-        __syncwarp();
         if (++ks == NKS) ks = 0, ++kround;
       }
-      if (tc::elect_one()) {
-        tc::commit(sfull0 + 8 * (j & 1));
-        if (last) tc::commit(qempty);
+      if (rank == 0) {
+        if (tc::elect_one()) {
+          tc::commit_pair(sfull0 + 8 * (j & 1));
+          if (last) tc::commit_pair(qempty);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       if (last) ++item;
     };
     auto values = [&](int j, bool first) {
-      if (!wait_all(pready0 + 8 * (j & 1), (j >> 1) & 1)) return;
-      for (int h = 0; h < S::kNV; ++h) {
-        const uint32_t slot = NKS + vs;
-        if (!wait_all(full0 + 8 * slot, vround & 1)) return;
+      if (rank == 0 && !wait_all(pready0 + 8 * (j & 1), (j >> 1) & 1)) return;
+      if (!wait_all(full0 + 8 * (NKS + vs), vround & 1)) return;
+      if (rank == 0) {
         tc::fence_after();
         if (tc::elect_one()) {
-          const uint32_t vb = v_ring0 + vs * S::kVSlot, pa = tmem + (j & 1) * 128 + h * (S::kVK / 2);
+          const uint32_t vb = v_ring0 + vs * S::kVSlot, pa = tmem + (j & 1) * 128;
 #pragma unroll
-          for (int k = 0; k < S::kVK / 16; ++k)
-            mma_ts(o_tmem, pa + 8 * k, desc_mn_sw128(vb + k * 2048, S::kVK * 128), id_o, (first && h == 0 && k == 0) ? 0u : 1u);
-          tc::commit(empty0 + 8 * slot);
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ts(o_tmem, pa + 8 * k, desc_mn_sw128(vb + k * 2048, kKeys * 128), id_o, (first && k == 0) ? 0u : 1u);
+          tc::commit_pair(empty0 + 8 * (NKS + vs));   // also: O holds this step
         }
         __syncwarp();
-        if (++vs == NVS) vs = 0, ++vround;
       }
-      if (tc::elect_one()) tc::commit(odone);
-      __syncwarp();
+      if (++vs == NVS) vs = 0, ++vround;
     };
     // per step: whether it is the first of an item in this share, and whether the
     // next step belongs to the same item
@@ -429,10 +451,10 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       first = !same;
       has = next_has;
     }
-    // every tcgen05 operation has finished before TMEM is freed
-    if (tc::elect_one()) tc::commit(drain);
+    // every tcgen05 operation has finished, in both CTAs, before TMEM is freed
+    if (rank == 0 && tc::elect_one()) tc::commit_pair(drain);
     __syncwarp();
-    tc::mbar_drain(drain, 0, kDrainCycles, p.dev_err);
+    tc::mbar_drain(drain, 0, *abort_flag ? kShortDrainCycles : kDrainCycles, p.dev_err);
     __syncwarp();
   } else if (warp >= kQWarp) {
     // ------------------------------------------------------- query rows
@@ -444,7 +466,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       // tokens behind the sequence's are another's or, behind the last, zeros:
       // their rows are masked and not written
       if (lane < D / 64)
-        tc::tma_load_4d(q_addr + lane * (kRows * 128), &p.tm_q, 0, w.head * p.group, w.s.cu + w.t * p.tokens, lane, qfull);
+        tc::tma_load_4d(q_addr + lane * (kRows * 128), &p.tm_q, 0, w.head * p.group, w.s.cu + (2 * w.t + rank) * p.tokens, lane, qfull);
       j += w.x.steps - w.local;
       if (j < n_steps) walk_next<PARTS>(w, p);
     }
@@ -472,8 +494,10 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       if (!dead) dead = !__all_sync(0xffffffffu, tc::mbar_wait(bar, par, p.wait_limit, abort_flag, p.dev_err));
       tc::fence_after();
     };
+    // O holds step i: the MMAs that read its slot of V are complete
+    auto wait_values = [&](int i) { wait(empty0 + 8 * (NKS + i % NVS), (i / NVS) & 1); };
     auto begin = [&]() {
-      tok = w.t * p.tokens + row_tok;
+      tok = (2 * w.t + rank) * p.tokens + row_tok;
       const int pos = tok < w.s.n ? w.s.pos0 + tok : -1;
       lo = kv_first(pos, a.window);
       hi = min(pos, w.x.end - 1);
@@ -528,7 +552,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
         m = m2;
         l *= f;
         if (!first) {   // O holds the steps before: let the last one finish
-          wait(odone, (j - 1) & 1);
+          wait_values(j - 1);
 #pragma unroll 1
           for (int c = 0; c < kHalfO; c += 32) {
             float t[32];
@@ -559,25 +583,22 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       // values that no row of the tile sees may be anything, and 0 times
       // infinity is no zero: they are cleared in shared memory
       if (k0 < w.x.lo || k0 + kKeys > w.x.end) {
-        const int vq = S::kNV * j;   // V slots before the step's
-        for (int h = 0; h < S::kNV; ++h) wait(full0 + 8 * (NKS + (vq + h) % NVS), ((vq + h) / NVS) & 1);
-        for (int h = 0; h < S::kNV; ++h) {
-          const uint32_t vb = v_ring0 + (vq + h) % NVS * S::kVSlot;
-          // a thread clears one 16-byte piece of a row of every slab
-          for (int i = threadIdx.x; i < S::kVK * 8; i += kSoftWarps * 32) {
-            const int c = k0 + h * S::kVK + (i >> 3);
-            if (c < w.x.lo || c >= w.x.end) {
+        wait(full0 + 8 * (NKS + j % NVS), (j / NVS) & 1);
+        const uint32_t vb = v_ring0 + j % NVS * S::kVSlot;
+        // a thread clears one 16-byte piece of a row of every slab
+        for (int i = threadIdx.x; i < kKeys * 8; i += kSoftWarps * 32) {
+          const int c = k0 + (i >> 3);
+          if (c < w.x.lo || c >= w.x.end) {
 #pragma unroll
-              for (int sl = 0; sl < S::kDV / 64; ++sl)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + sl * (S::kVK * 128) + i * 16), "r"(0) : "memory");
-            }
+            for (int sl = 0; sl < S::kN / 128; ++sl)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + sl * (kKeys * 128) + i * 16), "r"(0) : "memory");
           }
         }
         tc::fence_proxy_async();
       }
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(pready0 + 8 * (j & 1));
+      if (lane == 0) tc::mbar_arrive_cluster(pready0 + 8 * (j & 1), 0);
       first = false;
       if (same) {
         ++w.local;
@@ -586,8 +607,8 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       // ---- the item's part is complete.  The barrier's parity tells two
       // neighbouring phases apart, so the step before is waited for first (the
       // one before that is complete: this step's scores were issued after it).
-      if (j > 0) wait(odone, (j - 1) & 1);
-      wait(odone, j & 1);
+      if (j > 0) wait_values(j - 1);
+      wait_values(j);
       const bool closes = w.local + 1 == w.x.steps, whole = opens && closes;
       const bool in = tok < w.s.n && !dead;
       // the row's sum: of both halves
@@ -595,7 +616,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       meet();
       l = row_sh[0][j & 1][row] + row_sh[1][j & 1][row];
       const long long orow = (long long)(w.s.cu + tok) * a.n_q + w.head * p.group + row_head;
-      const long long slot = 2ll * blockIdx.x + (opens ? 1 : 0);
+      const long long slot = (2ll * pair + (opens ? 1 : 0)) * 2 + rank;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       T* out = static_cast<T*>(a.out) + orow * D + w.part * S::kDV + half * kHalfO;
       float* po = p.split.part_o + (slot * S::kDV + half * kHalfO) * kRows + row * 4;
@@ -619,8 +640,8 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
         if (!whole) p.split.part_ml[slot * kRows + row] = make_float2(m, l);
         else if (in && w.part == 0 && a.lse) a.lse[orow] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
         if (opens && !closes && row == 0)
-          p.split.recs[blockIdx.x] = {(int)((first_step + j - w.local + w.x.steps - 1) / share), w.s.cu + w.t * p.tokens,
-                                      min(p.tokens, w.s.n - w.t * p.tokens) * p.group, w.head * p.group, p.group, w.part};
+          p.split.recs[blockIdx.x] = {(int)((first_step + j - w.local + w.x.steps - 1) / share), w.s.cu + (2 * w.t + rank) * p.tokens,
+                                      max(min(p.tokens, w.s.n - (2 * w.t + rank) * p.tokens), 0) * p.group, w.head * p.group, p.group, w.part};
       }
       tc::fence_before();
       if (j + 1 < n_steps) {
@@ -631,11 +652,14 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     }
   }
 
+  // no CTA leaves while the other still loads into it or signals its barriers
   tc::fence_before();
-  __syncthreads();
+  __syncwarp();
+  tc::cluster_arrive_release();
+  tc::cluster_wait();
   if (warp == kMmaWarp) {
     tc::fence_after();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -649,18 +673,34 @@ static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
     attr.set(dev.ordinal);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid);
+  cfg.gridDim = dim3(2 * p.pairs);
   cfg.blockDim = dim3(kThr);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  // as many pairs as the device holds at once (asked once per device)
+  static int most[64] = {0};
+  int n = dev.ordinal >= 0 && dev.ordinal < 64 ? most[dev.ordinal] : 0;
+  if (n == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, tile_kernel<T, D>, &cfg);
+    if (e != cudaSuccess) return cuda_fail(e, "tile attention cluster occupancy");
+    if (n < 1) return fail(Q4_ERR_CUDA, "tile attention: no cluster of two CTAs fits the device");
+    if (dev.ordinal >= 0 && dev.ordinal < 64) most[dev.ordinal] = n;
+  }
+  if (n < p.pairs) p.pairs = n;
+  cfg.gridDim = dim3(2 * p.pairs);
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, p);
   if (e != cudaSuccess) return cuda_fail(e, "tile attention launch");
-  return launch_attn_join(p.a, p.split, kRows, D, S::kDV, std::is_same<T, __nv_bfloat16>::value, p.grid, s);
+  return launch_attn_join(p.a, p.split, kRows, D, S::kDV, std::is_same<T, __nv_bfloat16>::value, 2 * p.pairs, 2, s);
 }
 
 template <typename T>
@@ -689,11 +729,11 @@ int launch_attn_tile(const AttnParams& a, const q4_kv_cache& c, void* ws, const 
   if (st == Q4_OK) st = encode_query_rows(&p.tm_q, a.q, bf16, c.head_dim, a.n_q, a.T, a.q_stride, p.group, p.tokens);
   if (st != Q4_OK) return st;
   p.a = a;
-  p.grid = dev.sms;
+  p.pairs = dev.sms / 2;
   p.total_rows = (int)rows;
   p.wait_limit = wait_limit();
   p.dev_err = device_error_word();
-  p.split = attn_split(ws, p.grid, tile::kRows, c.head_dim < 256 ? c.head_dim : 256);
+  p.split = attn_split(ws, dev.sms, tile::kRows, c.head_dim < 256 ? c.head_dim : 256);
   return bf16 ? tile::launch_t<__nv_bfloat16>(p, c.head_dim, dev, s) : tile::launch_t<__half>(p, c.head_dim, dev, s);
 }
 

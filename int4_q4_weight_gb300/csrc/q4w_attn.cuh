@@ -39,11 +39,12 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // The parts of work that is cut.  The steps of all items form one line that is
-// cut into equal shares; CTA c leaves the part of an item that began before it
-// in slot 2 c, and the part of one that it begins and does not end in slot
-// 2 c + 1, with a record of how far that item goes.
+// cut into equal shares; the team of R CTAs c (R is 1, or 2 that work in step on
+// a tile each) leaves the part of an item that began before it in slot 2 c, and
+// the part of one that it begins and does not end in slot 2 c + 1, times R plus
+// the CTA's rank, with a record per CTA of how far that item goes.
 struct SplitRec {
-  int last;              // CTA that ends the item; -1: this CTA begins none that it does not end
+  int last;              // team that ends the item; -1: this one begins none that it does not end
   int token, used;       // first token of the item's tile, its rows
   int head0, group;      // first query head, heads per token: row r is token r / group, head r % group
   int col;               // column part of D
@@ -71,7 +72,7 @@ inline AttnSplit attn_split(void* ws, int grid, int rows, int dv) {
 }
 
 // Joins what the recorded items left in their slots, in the order of the keys.
-int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int D, int dv, bool bf16, int grid,
+int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int D, int dv, bool bf16, int grid, int R,
                      cudaStream_t s);
 
 }  // namespace q4w

@@ -73,6 +73,18 @@ __device__ __forceinline__ bool mbar_test_for(uint32_t a, uint32_t parity, uint3
 // millisecond.
 constexpr uint32_t kSuspendNs = 200000;
 
+// Arrives on the mbarrier at this place of CTA `rank` of the cluster.  The release
+// is of CTA scope: what the other side then reads was written by TMA or into
+// TMEM, or behind a fence of the caller (a release of cluster scope drains the
+// thread's global stores too, 1200 cycles).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t a, uint32_t rank) {
+  asm volatile(
+      "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, %1;\n"
+      " mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(a),
+      "r"(rank)
+      : "memory");
+}
+
 // Bounded wait on phase `parity` of an mbarrier.  False when the budget ran
 // out (the CTA's abort flag and bit 0 of *err are then set) or when another
 // role of the CTA is aborting.  The first check does not suspend and the
@@ -199,6 +211,23 @@ __device__ __forceinline__ void fence_after() {
 __device__ __forceinline__ void commit(uint32_t mbar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar)
                : "memory");
+}
+// The pair form (cta_group::2), issued by the even CTA of a pair: arrives on the
+// mbarrier at this place of both.
+__device__ __forceinline__ void commit_pair(uint32_t mbar) {
+  asm volatile(
+      "{\n .reg .b16 m;\n mov.b16 m, 3;\n"
+      " tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}" ::"r"(mbar)
+      : "memory");
+}
+// TMEM columns for pair MMAs: both CTAs of a pair call these.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
 
 // TMEM columns: allocated by one whole warp, address written to shared memory.
