@@ -5,7 +5,7 @@
 namespace q4w {
 namespace attn {
 
-// Task: 8 rows of one recorded item and 256 / P of their elements; P groups of
+// Task: 8 rows (32 when P is 1) of one recorded item and 256 / P of their elements; P groups of
 // threads take every P-th part (P = 1, 4 or 16: two parts of a tile are read by
 // as many threads as there are elements; the 152 parts of the few rows of a
 // single long sequence by 16 groups side by side, as there are no other tasks:
@@ -14,12 +14,27 @@ namespace attn {
 // whatever CTA recorded them.
 constexpr int kJoinThr = 512;
 
-__device__ __forceinline__ int join_groups(int parts, int used, int dv) {
-  return max(parts <= 4 ? 1 : parts > 16 && used <= 16 ? 16 : 4, 256 / dv);
+// log2 of P; lg_dv: log2 of the columns.
+__device__ __forceinline__ int join_groups(int parts, int used, int lg_dv) {
+  return max(parts <= 4 ? 0 : parts > 16 && used <= 16 ? 4 : 2, 8 - lg_dv);
 }
 
+// Sums of what a thread has of a row, scaled to a running maximum (units of log2 e).
+struct JoinSum {
+  float4 o;
+  float m, l;
+  __device__ __forceinline__ void clear() { o = make_float4(0.f, 0.f, 0.f, 0.f), m = -CUDART_INF_F, l = 0.f; }
+  __device__ __forceinline__ void add(const float2 ml, const float4 v) {
+    const float m2 = fmaxf(m, ml.x), mb = m2 == -CUDART_INF_F ? 0.f : m2;
+    const float f0 = ex2(m - mb), f = ex2(ml.x - mb);
+    m = m2;
+    l = fmaf(ml.y, f, l * f0);
+    o.x = fmaf(v.x, f, o.x * f0), o.y = fmaf(v.y, f, o.y * f0), o.z = fmaf(v.z, f, o.z * f0), o.w = fmaf(v.w, f, o.w * f0);
+  }
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n_recs, int R, int n_q, int rows, int D, int dv,
+__global__ void __launch_bounds__(kJoinThr, 2) join_kernel(const AttnSplit p, int n_recs, int R, int n_q, int rows, int D, int dv,
                                                         void* out_, float* lse) {
   __shared__ float4 sum_sh[kJoinThr];
   __shared__ float2 ml_sh[16][8];
@@ -27,13 +42,15 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
   __shared__ SplitRec rec_sh[kJoinThr];
   __shared__ int warp_sh[kJoinThr / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lg_dv = 31 - __clz(dv);   // 64, 128 or 256
   pdl_wait();
   {
     int n = 0;
     if (threadIdx.x < n_recs) {
       const SplitRec r = p.recs[threadIdx.x];
       rec_sh[threadIdx.x] = r;
-      n = r.last < 0 ? 0 : (r.used + 7) / 8 * (dv * join_groups(r.last - (int)threadIdx.x / R + 1, r.used, dv) / 256);
+      const int g = join_groups(r.last - (int)threadIdx.x / R + 1, r.used, lg_dv), lg_rows = g == 0 ? 5 : 3;
+      n = r.last < 0 ? 0 : ((r.used + (1 << lg_rows) - 1) >> lg_rows) << (lg_dv + g - 8);
     }
     int incl = n;
 #pragma unroll
@@ -59,13 +76,60 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
     }
     const SplitRec rec = rec_sh[lo];
     const int c0 = lo / R, sub = task - first_sh[lo], np = rec.last - c0 + 1;
-    const int groups = join_groups(np, rec.used, dv), quads = 64 / groups, col_tasks = dv * groups / 256;
-    const int part = (threadIdx.x >> 3) / quads, dl = (threadIdx.x >> 3) % quads, d = (sub % col_tasks * quads + dl) * 4;
-    const int lr = sub / col_tasks * 8 + rr;
-    const bool in = lr < rec.used;
-    auto slot = [&](int i) { return (i == 0 ? 2ll * c0 + 1 : 2ll * (c0 + i)) * R + lo % R; };
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f, m = -CUDART_INF_F;
+    const int lg = join_groups(np, rec.used, lg_dv), groups = 1 << lg, lg_cols = lg_dv + lg - 8;
+    const int part = threadIdx.x >> (9 - lg), dl = (threadIdx.x >> 3) & ((64 >> lg) - 1);
+    const int d = (((sub & ((1 << lg_cols) - 1)) << (6 - lg)) + dl) * 4;
+    // row `rr` of the task's first 8: of part 0, and of part i >= 1 at i - 1 steps
+    // behind part 1
+    const int r0 = (sub >> lg_cols) * (lg == 0 ? 32 : 8) + rr;
+    const long long slot0 = (2ll * c0 + 1) * R + lo % R, slot1 = (2ll * c0 + 2) * R + lo % R;
+    const float* const o0 = p.part_o + (slot0 * dv + d) * rows + 4 * r0;
+    const float* const o1 = p.part_o + (slot1 * dv + d) * rows + 4 * r0;
+    const float2* const ml0 = p.part_ml + slot0 * rows + r0;
+    const float2* const ml1 = p.part_ml + slot1 * rows + r0;
+    const int o_step = 2 * R * dv * rows, ml_step = 2 * R * rows;
+    auto part_ml = [&](int i, int row) { return (i == 0 ? ml0 : ml1 + (long long)(i - 1) * ml_step)[row]; };
+    auto part_o = [&](int i, int row) {
+      return *reinterpret_cast<const float4*>((i == 0 ? o0 : o1 + (long long)(i - 1) * o_step) + 4 * row);
+    };
+    const uint32_t by_group = 65536u / rec.group + 1;   // rows below 128: row / group = row * this >> 16
+    auto write = [&](int lr, const JoinSum& x) {
+      const int tok = (int)(lr * by_group >> 16);
+      const long long row = (long long)(rec.token + tok) * n_q + rec.head0 + lr - tok * rec.group;
+      const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
+      *reinterpret_cast<uint2*>(static_cast<T*>(out_) + row * D + rec.col * dv + d) =
+          make_uint2(Half16<T>::pack(x.o.x * inv, x.o.y * inv), Half16<T>::pack(x.o.z * inv, x.o.w * inv));
+      if (d == 0 && rec.col == 0 && lse) lse[row] = x.l == 0.f ? -CUDART_INF_F : (x.m + log2f(x.l)) * 0.6931471805599453f;
+    };
+    if (lg == 0) {   // few parts: four rows a thread, their loads side by side
+      JoinSum x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k].clear();
+#pragma unroll 1
+      for (int i = 0; i < np; i += 2) {
+        float2 ml[2][4];
+        float4 v[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const bool in = i + h < np && r0 + 8 * k < rec.used;
+            ml[h][k] = in ? part_ml(i + h, 8 * k) : make_float2(-CUDART_INF_F, 0.f);
+            v[h][k] = in ? part_o(i + h, 8 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k].add(ml[h][k], v[h][k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (r0 + 8 * k < rec.used) write(r0 + 8 * k, x[k]);
+      continue;
+    }
+    const bool in = r0 < rec.used;
+    JoinSum x;
+    x.clear();
     if (in) {
       for (int i = part; i < np; i += 4 * groups) {   // four parts at a time
         float2 ml[4];
@@ -73,41 +137,21 @@ __global__ void __launch_bounds__(kJoinThr) join_kernel(const AttnSplit p, int n
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int at = i + groups * k;
-          ml[k] = at < np ? p.part_ml[slot(at) * rows + lr] : make_float2(-CUDART_INF_F, 0.f);
-          v[k] = at < np ? *reinterpret_cast<const float4*>(p.part_o + (slot(at) * dv + d) * rows + 4 * lr) : make_float4(0.f, 0.f, 0.f, 0.f);
+          ml[k] = at < np ? part_ml(at, 0) : make_float2(-CUDART_INF_F, 0.f);
+          v[k] = at < np ? part_o(at, 0) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const float m2 = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
-        const float mb = m2 == -CUDART_INF_F ? 0.f : m2, f0 = ex2(m - mb);
-        m = m2;
-        l *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float f = ex2(ml[k].x - mb);
-          l = fmaf(ml[k].y, f, l);
-          o.x = fmaf(v[k].x, f, o.x), o.y = fmaf(v[k].y, f, o.y), o.z = fmaf(v[k].z, f, o.z), o.w = fmaf(v[k].w, f, o.w);
-        }
+        for (int k = 0; k < 4; ++k) x.add(ml[k], v[k]);
       }
     }
     __syncthreads();
-    sum_sh[threadIdx.x] = o;
-    if (dl == 0) ml_sh[part][rr] = make_float2(m, l);
+    sum_sh[threadIdx.x] = x.o;
+    if (dl == 0) ml_sh[part][rr] = make_float2(x.m, x.l);
     __syncthreads();
     if (part == 0 && in) {
-      float mm = -CUDART_INF_F;
-      for (int i = 0; i < groups; ++i) mm = fmaxf(mm, ml_sh[i][rr].x);
-      const float mb = mm == -CUDART_INF_F ? 0.f : mm;
-      l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < groups; ++i) {
-        const float f = ex2(ml_sh[i][rr].x - mb);
-        const float4 v = sum_sh[threadIdx.x + 8 * quads * i];
-        l = fmaf(ml_sh[i][rr].y, f, l);
-        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-      }
-      const long long row = (long long)(rec.token + lr / rec.group) * n_q + rec.head0 + lr % rec.group;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      *reinterpret_cast<uint2*>(static_cast<T*>(out_) + row * D + rec.col * dv + d) =
-          make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
-      if (d == 0 && rec.col == 0 && lse) lse[row] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
+      x.clear();
+      for (int i = 0; i < groups; ++i) x.add(ml_sh[i][rr], sum_sh[threadIdx.x + (i << (9 - lg))]);
+      write(r0, x);
     }
   }
 }
@@ -118,7 +162,7 @@ int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int 
                      cudaStream_t s) {
   if (grid > attn::kJoinThr) return fail(Q4_ERR_SHAPE, "attention: %d SMs are more than the join handles", grid);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(4 * grid);
+  cfg.gridDim = dim3(2 * grid);
   cfg.blockDim = dim3(attn::kJoinThr);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
