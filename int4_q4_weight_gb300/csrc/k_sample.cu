@@ -261,8 +261,52 @@ struct Part {
       }
     }
   }
-  // The same for long bodies, expanded for one load only, the next one in flight
-  // meanwhile.
+  // Calls act(logit, index) for the few logits that pred holds for: the test is
+  // expanded for every element, the body exists once.
+  template <typename P, typename A>
+  __device__ __forceinline__ void rare(P pred, A act) const {
+    int base = 0;
+    uint32_t hits = 0;   // of 32 elements
+    auto take = [&](int first) {
+      while (hits) {
+        const int b = first + __ffs(hits) - 1;
+        hits &= hits - 1;
+        const int i = base + b / E * step + b % E;
+        act(as_float(row[i]), i);
+      }
+    };
+    base = i0 + E * (int)threadIdx.x;
+    if constexpr (KEEP) {
+      uint32_t all[kKeep / 32];
+#pragma unroll
+      for (int h = 0; h < kKeep / 32; ++h) {
+        all[h] = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) all[h] |= pred(v[32 * h + k]) ? 1u << k : 0u;
+      }
+#pragma unroll 1
+      for (int h = 0; h < kKeep / 32; ++h) {
+        hits = h == 0 ? all[0] : all[1];
+        take(32 * h);
+      }
+      static_assert(kKeep == 64, "two words of hits");
+    } else {
+#pragma unroll 1
+      for (; base < i1; base += 32 / E * step) {
+        hits = 0;
+#pragma unroll
+        for (int x = 0; x < 32 / E; ++x) {
+          float t[E];
+          load_logits<T, E>(row, base + x * step, i1, vec, t);
+#pragma unroll
+          for (int k = 0; k < E; ++k) hits |= pred(t[k]) ? 1u << (x * E + k) : 0u;
+        }
+        take(0);
+      }
+    }
+  }
+  // The same as light() for long bodies, expanded for one load only, the next one
+  // in flight meanwhile.
   template <typename F>
   __device__ __forceinline__ void heavy(F f) const {
     float next[E];
@@ -538,14 +582,11 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
     // ---- C: the candidates into the leader
     const uint32_t list0 = tc::cluster_addr(sh.list, 0), count0 = tc::cluster_addr(&sh.n_list, 0);
     const float lim = (float)(last + 1);
-    part.light([&](float v, int i) {
-      v = capped(s, v);
-      if (eighths(s, v) < lim) {
-        uint32_t at;
-        asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(count0) : "memory");
-        const u64 c = ((u64)~key_of(v) << 32) | (uint32_t)i;
-        if (at < (uint32_t)kCap) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list0 + 8 * at), "l"(c) : "memory");
-      }
+    part.rare([&](float v) { return eighths(s, capped(s, v)) < lim; }, [&](float v, int i) {
+      uint32_t at;
+      asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(count0) : "memory");
+      const u64 c = ((u64)~key_of(capped(s, v)) << 32) | (uint32_t)i;
+      if (at < (uint32_t)kCap) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list0 + 8 * at), "l"(c) : "memory");
     });
     cluster_sync();
     if (rank != 0) return;   // only the leader's own memory is used from here
@@ -651,14 +692,12 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
       clear_bins(sh);
       __syncthreads();
       const float lim = (float)(last + 1);
-      part.heavy([&](float v, int) {
+      part.rare([&](float v) { return eighths(s, capped(s, v)) < lim; }, [&](float v, int) {
         v = capped(s, v);
         const float q = eighths(s, v);
-        if (q < lim) {
-          float nf;
-          const int n = whole(q, &nf);
-          add_to_bin(sh, n, mantissa(s, v, q, nf));
-        }
+        float nf;
+        const int n = whole(q, &nf);
+        add_to_bin(sh, n, mantissa(s, v, q, nf));
       });
       cluster_sync();
       merge_bins(sh, ctas, true, cnt, mant);
@@ -720,14 +759,13 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
         cluster_sync();   // every CTA has read the last histogram
         clear_bins(sh);
         __syncthreads();
-        part.heavy([&](float v, int) {
+        // (on the logits: the key of a NaN lies outside)
+        const float v_lo = logit_of(k_lo), v_hi = logit_of(k_hi);
+        part.rare([&](float v) { v = capped(s, v); return v >= v_lo && v <= v_hi; }, [&](float v, int) {
           v = capped(s, v);
-          const uint32_t k = key_of(v);
-          if (k - k_lo <= width) {
-            const int b = (int)((k_hi - k) >> shift);
-            if (has_p) add_to_bin(sh, b, mantissa(s, v, eighths(s, v), (float)bin));
-            else atomicAdd(&sh.cnt[b], 1u);
-          }
+          const int b = (int)((k_hi - key_of(v)) >> shift);
+          if (has_p) add_to_bin(sh, b, mantissa(s, v, eighths(s, v), (float)bin));
+          else atomicAdd(&sh.cnt[b], 1u);
         });
         cluster_sync();
         u64 c[2], m[2];
