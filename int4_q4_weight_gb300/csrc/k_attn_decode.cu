@@ -6,7 +6,7 @@
 // moved only when a score passes it by 2^8, so that most steps rescale nothing.
 // The final division makes the result independent of that choice.
 //
-// Bound: HBM.  A 16-bit cache element takes part in 8 to 64 multiply-adds, too
+// Bound: HBM.  A 16-bit cache element takes part in 8 or 16 multiply-adds, too
 // many for the CUDA cores at 6.8 TB/s (3.4e12 elements/s x 8 x 2 is 54 TFLOP/s)
 // and too few to fill a 128-row tensor tile, so the keys are the M rows of
 // m16n8k16 (no row is padding at 8 query rows) and the query rows its N:
@@ -37,15 +37,19 @@ namespace dec {
 constexpr int kUnit = 16;              // keys per unit
 constexpr int kRingBytes = 196608;     // of a CTA
 
-template <int D>
+template <int D, int NT>
 struct Shape {
-  static constexpr int kWarps = D == 512 ? 4 : 8;
+  // A warp holds NT D / 4 + NT D / 8 registers of O and Q.  Twelve warps where
+  // that leaves them without spills: 8 rows of head size 64 stream at 6.1 TB/s,
+  // with eight warps at 5.4; 16 rows of head size 128 at 5.4 (spills), with eight 6.2.
+  static constexpr int kWarps = D == 512 ? 4 : NT * D <= 128 ? 12 : 8;
   static constexpr int kSlotBytes = kUnit * D * 2;
   static constexpr int kSlots = kRingBytes / kWarps / kSlotBytes;   // 3, 3, 6, 12: K and V alternate
   static constexpr int kThr = kWarps * 32;
   static constexpr int kStep = kWarps * kUnit;                      // keys per step of the CTA
   static constexpr int kRowPad = D + 4;                             // floats per row of the output staging
-  static constexpr int kMergeBytes = kWarps / 2 * 8 * D * 4;         // half the warps' outputs of 8 rows
+  static constexpr int kMergeBytes = kWarps / 2 * NT * 8 * D * 4;    // half the warps' outputs
+  static_assert(kMergeBytes >= NT * 8 * kRowPad * 4, "the output staging shares it");
   static_assert(kMergeBytes >= 8 * kRowPad * 4, "the output staging shares it");
   static constexpr size_t kSmem = 1024 + kRingBytes + kMergeBytes;
 };
@@ -122,8 +126,8 @@ struct Walk {
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_constant__ Params p) {
-  using S = Shape<D>;
+__global__ void __launch_bounds__((Shape<D, NT>::kThr), 1) decode_kernel(const __grid_constant__ Params p) {
+  using S = Shape<D, NT>;
   constexpr int W = S::kWarps, SLOTS = S::kSlots, KS = D / 16, SLABS = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -407,49 +411,57 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
       if (opens && !closes && threadIdx.x == 0)   // goes on in the next CTAs
         p.split.recs[blockIdx.x] = {(int)((first_step + step - cw.local + cw.n_local - 1) / share), cw.s.cu, R,
                                     cw.head * p.group, p.group, 0};
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      {
         // every warp to the common maximum
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 8 * t + 2 * (lane & 3) + j;
-          float mm = -CUDART_INF_F;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int w = 0; w < W; ++w) mm = fmaxf(mm, ml_sh[w][r].x);
-          const float f = m[t][j] == -CUDART_INF_F ? 0.f : ex2(m[t][j] - mm);
+          for (int j = 0; j < 2; ++j) {
+            const int r = 8 * t + 2 * (lane & 3) + j;
+            float mm = -CUDART_INF_F;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) o[t][i][j] *= f, o[t][i][j + 2] *= f;
-        }
-        // their sum, pairwise
+            for (int w = 0; w < W; ++w) mm = fmaxf(mm, ml_sh[w][r].x);
+            const float f = m[t][j] == -CUDART_INF_F ? 0.f : ex2(m[t][j] - mm);
 #pragma unroll
-        for (int half = W / 2; half > 0; half >>= 1) {
-          if (warp >= half && warp < 2 * half) {
-            float* b = merge + (warp - half) * 8 * D + lane;
+            for (int i = 0; i < D / 16; ++i) o[t][i][j] *= f, o[t][i][j + 2] *= f;
+          }
+        // their sum, pairwise: of n warps the upper n / 2 are added to the first
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+        for (int n = W; n > 1; n -= n / 2) {
+          const int half = n / 2;
+          if (warp >= n - half && warp < n) {
+            float* b = merge + (warp - (n - half)) * NT * 8 * D + lane;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) b[(4 * i + j) * 32] = o[t][i][j];
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[((t * (D / 16) + i) * 4 + j) * 32] = o[t][i][j];
           }
           __syncthreads();
           if (warp < half) {
-            const float* b = merge + warp * 8 * D + lane;
+            const float* b = merge + warp * NT * 8 * D + lane;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) o[t][i][j] += b[(4 * i + j) * 32];
+              for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[t][i][j] += b[((t * (D / 16) + i) * 4 + j) * 32];
           }
           __syncthreads();
         }
         if (warp == 0) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              merge[(2 * (lane & 3) + (j & 1)) * S::kRowPad + 16 * i + (lane >> 2) + 8 * (j >> 1)] = o[t][i][j];
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                merge[(8 * t + 2 * (lane & 3) + (j & 1)) * S::kRowPad + 16 * i + (lane >> 2) + 8 * (j >> 1)] = o[t][i][j];
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < 8 * (D / 4); i += S::kThr) {
-          const int rr = i & 7, r = 8 * t + rr, d = 4 * (i >> 3);
+        for (int i = threadIdx.x; i < NT * 8 * (D / 4); i += S::kThr) {
+          const int r = i % (8 * NT), d = 4 * (i / (8 * NT));
           if (r >= R) continue;
           float mm = -CUDART_INF_F, ll = 0.f;
 #pragma unroll
@@ -459,7 +471,7 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
             const float2 x = ml_sh[w][r];
             ll += x.x == -CUDART_INF_F ? 0.f : x.y * ex2(x.x - mm);
           }
-          const float4 v = *reinterpret_cast<const float4*>(merge + rr * S::kRowPad + d);
+          const float4 v = *reinterpret_cast<const float4*>(merge + r * S::kRowPad + d);
           if (whole) {
             const int tok = r / p.group;
             const long long row = (long long)(cw.s.cu + tok) * a.n_q + cw.head * p.group + r - tok * p.group;
@@ -485,7 +497,7 @@ __global__ void __launch_bounds__(Shape<D>::kThr, 1) decode_kernel(const __grid_
 
 template <typename T, int D, int NT>
 static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
-  using S = Shape<D>;
+  using S = Shape<D, NT>;
   static PerDevice attr;
   if (!attr.get(dev.ordinal)) {
     const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -508,20 +520,23 @@ static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
   return launch_attn_join(p.a, p.split, 8 * NT, D, D, std::is_same<T, __nv_bfloat16>::value, p.grid, 1, s);
 }
 
-// The largest NT: registers hold NT (D/8 + D/4) values of Q and O.
-constexpr int max_nt(int D) { return D >= 512 ? 1 : D == 256 ? 2 : 4; }
+// The largest NT.  More rows go to the tiles of 128 rows, although most of a
+// tile is padding then: 16 rows of head size 256 took 208 us here and 198 there (64
+// sequences of 16384), 32 rows of 128 took 223 and 146 (16 x 8 heads of 8192;
+// their O and Q spill here).
+constexpr int max_nt(int D) { return D >= 256 ? 1 : 2; }
 
 template <typename T>
 static int launch_t(Params& p, int D, int nt, const DeviceInfo& dev, cudaStream_t s) {
   switch (D) {
-    case 64: return nt == 1 ? launch<T, 64, 1>(p, dev, s) : nt == 2 ? launch<T, 64, 2>(p, dev, s) : launch<T, 64, 4>(p, dev, s);
-    case 128: return nt == 1 ? launch<T, 128, 1>(p, dev, s) : nt == 2 ? launch<T, 128, 2>(p, dev, s) : launch<T, 128, 4>(p, dev, s);
-    case 256: return nt == 1 ? launch<T, 256, 1>(p, dev, s) : launch<T, 256, 2>(p, dev, s);
+    case 64: return nt == 1 ? launch<T, 64, 1>(p, dev, s) : launch<T, 64, 2>(p, dev, s);
+    case 128: return nt == 1 ? launch<T, 128, 1>(p, dev, s) : launch<T, 128, 2>(p, dev, s);
+    case 256: return launch<T, 256, 1>(p, dev, s);
     default: return launch<T, 512, 1>(p, dev, s);
   }
 }
 
-static int nt_of(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+static int nt_of(int rows) { return rows <= 8 ? 1 : 2; }
 
 }  // namespace dec
 

@@ -209,6 +209,13 @@ def test_attention_chunks(cuda_lib, D, dtype, hq, hkv, page):
     check_attention(cuda_lib, c)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("hq,new", [(1, 7), (3, 3), (8, 2), (5, 4), (8, 3), (8, 4), (16, 2), (7, 5), (1, 40), (16, 9), (100, 1), (128, 2)])
+def test_attention_any_number_of_query_rows(cuda_lib, D, hq, new):
+    """1 to 256 query rows per KV head: every choice of kernel, groups that do not divide a tile."""
+    check_attention(cuda_lib, Case([new, 1, new], [new, 100, 300 + new], hq, 1, D, 16, BF16, seed=hq))
+
+
 @pytest.mark.parametrize("D,hq,hkv", [(64, 8, 2), (256, 8, 1), (512, 8, 1), (128, 4, 4)])
 @pytest.mark.parametrize("new", [1, 2, 4, 9, 70])
 @pytest.mark.parametrize("window", [1, 17, 100, 512])
