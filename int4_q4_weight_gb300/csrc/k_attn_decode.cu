@@ -40,8 +40,8 @@ constexpr int kRingBytes = 196608;     // of a CTA
 template <int D, int NT>
 struct Shape {
   // A warp holds NT D / 4 + NT D / 8 registers of O and Q.  Twelve warps where
-  // that leaves them without spills: 8 rows of head size 64 stream at 6.1 TB/s,
-  // with eight warps at 5.4; 16 rows of head size 128 at 5.4 (spills), with eight 6.2.
+  // that leaves them without spills: 8 rows of head size 64 stream at 6.2 TB/s,
+  // with eight warps at 5.4; 16 rows of head size 128 at 5.4 (spills), with eight 6.3.
   static constexpr int kWarps = D == 512 ? 4 : NT * D <= 128 ? 12 : 8;
   static constexpr int kSlotBytes = kUnit * D * 2;
   static constexpr int kSlots = kRingBytes / kWarps / kSlotBytes;   // 3, 3, 6, 12: K and V alternate
@@ -51,7 +51,7 @@ struct Shape {
   static constexpr int kMergeBytes = kWarps / 2 * NT * 8 * D * 4;    // half the warps' outputs
   static_assert(kMergeBytes >= NT * 8 * kRowPad * 4, "the output staging shares it");
   static_assert(kMergeBytes >= 8 * kRowPad * 4, "the output staging shares it");
-  static constexpr size_t kSmem = 1024 + kRingBytes + kMergeBytes;
+  static constexpr size_t kSmem = kRingBytes + kMergeBytes;
 };
 
 struct Params {
@@ -129,8 +129,7 @@ template <typename T, int D, int NT>
 __global__ void __launch_bounds__((Shape<D, NT>::kThr), 1) decode_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, NT>;
   constexpr int W = S::kWarps, SLOTS = S::kSlots, KS = D / 16, SLABS = D / 64;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t ring[];
   float* merge = reinterpret_cast<float*>(ring + kRingBytes);
   __shared__ float2 ml_sh[W][8 * NT];
   __shared__ long long scan_sh[W];
@@ -523,20 +522,20 @@ static int launch(Params& p, const DeviceInfo& dev, cudaStream_t s) {
 // The largest NT.  More rows go to the tiles of 128 rows, although most of a
 // tile is padding then: 16 rows of head size 256 took 208 us here and 198 there (64
 // sequences of 16384), 32 rows of 128 took 223 and 146 (16 x 8 heads of 8192;
-// their O and Q spill here).
-constexpr int max_nt(int D) { return D >= 256 ? 1 : 2; }
+// their O and Q spill here), 32 rows of 64, which do not, 141 and 273.
+constexpr int max_nt(int D) { return D >= 256 ? 1 : D == 128 ? 2 : 4; }
 
 template <typename T>
 static int launch_t(Params& p, int D, int nt, const DeviceInfo& dev, cudaStream_t s) {
   switch (D) {
-    case 64: return nt == 1 ? launch<T, 64, 1>(p, dev, s) : launch<T, 64, 2>(p, dev, s);
+    case 64: return nt == 1 ? launch<T, 64, 1>(p, dev, s) : nt == 2 ? launch<T, 64, 2>(p, dev, s) : launch<T, 64, 4>(p, dev, s);
     case 128: return nt == 1 ? launch<T, 128, 1>(p, dev, s) : launch<T, 128, 2>(p, dev, s);
     case 256: return launch<T, 256, 1>(p, dev, s);
     default: return launch<T, 512, 1>(p, dev, s);
   }
 }
 
-static int nt_of(int rows) { return rows <= 8 ? 1 : 2; }
+static int nt_of(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 }  // namespace dec
 

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       if (j < n_steps) walk_next<PARTS>(w, p);
     }
     // the loads land before the CTA leaves
-    if (item > 0) tc::mbar_drain(qfull, (item - 1) & 1, kDrainCycles, p.dev_err);
+    if (item > 0) tc::mbar_drain(qfull, (item - 1) & 1, *abort_flag ? kShortDrainCycles : kDrainCycles, p.dev_err);
     __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax

@@ -99,7 +99,7 @@ def check_attention(q4w, c, scale=None, window=0, max_q=None, q=None, err=0, **k
     tol = half * (A + np.abs(ro)) * 1.01 + (2 * ds[..., None] + 2e-6) * A + small + 1e-30
     bad = ~(np.abs(go - ro) <= tol)
     assert not bad.any(), (int(bad.sum()), float((np.abs(go - ro) / tol).max()))
-    assert np.all(np.abs(gl - rl)[~empty] <= (ds + 2e-6 * (1 + np.abs(rl)))[~empty])
+    assert np.all(np.abs(gl[~empty] - rl[~empty]) <= (ds + 2e-6 * (1 + np.abs(rl)))[~empty])
     return out, lse
 
 
@@ -355,3 +355,20 @@ def test_attention_cache_beyond_32_bits(cuda_lib):
         want, _ = q4w.kv_attention(q, kc[ids].contiguous(), vc[ids].contiguous(), small, cu, kvl)
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D", [64, 256, 512])
+def test_attention_zero_budget_times_out_then_recovers(cuda_lib, D):
+    """The tiles' bounded waits: with a zero cycle budget the kernel gives up, returns
+    and reports it; the next call is right again."""
+    q4w = cuda_lib
+    q4w.q4_device_status()
+    c = Case([200, 90], [3000, 500], 8, 1, D)
+    old = q4w.q4_set_wait_limit(0)
+    try:
+        q4w.kv_attention(c.q, *c.tables(), max_q=200)
+        with pytest.raises(q4w.Q4Error, match="Q4_ERR_TIMEOUT"):
+            q4w.q4_device_status()
+    finally:
+        q4w.q4_set_wait_limit(old)
+    check_attention(q4w, c)
