@@ -48,7 +48,7 @@ class Decoder:
                 qkv32=[torch.empty(n, dtype=torch.float32, device=device) for n in (N_Q * D, D, D)],
                 q16=torch.empty((1, N_Q, D), dtype=torch.float16, device=device),
                 att=torch.empty((1, N_Q, D), dtype=torch.float16, device=device),
-                ws=q4w.kv_attention_ws(1, N_Q, 1, D, 1, device)))
+                ws=q4w.kv_attention_ws(1, N_Q, 1, D, device)))
         self.embed = synth.normal((V, H), 1.0, synth.sub_seed(seed, "embed"), device).to(torch.float16)
         self.head = q4(V, H, "head")
         f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=device)   # noqa: E731

@@ -65,8 +65,7 @@ typedef enum q4_op {
   Q4_OP_GEMM_CHUNK = 1,
   Q4_OP_PLE = 2,
   Q4_OP_LMHEAD = 3,
-  Q4_OP_DECODE_PASS = 4,
-  Q4_OP_KV_ATTENTION = 5
+  Q4_OP_DECODE_PASS = 4
 } q4_op;
 
 /* Element types of the paged-cache and sampling entry points. */
@@ -393,16 +392,19 @@ int kv_append(const q4_kv_cache* cache, int T, const void* k, long long k_stride
  *   be freed; what lies in a page behind kv_lens may be anything.  A page
  *   outside [0, n_pages), or kv_lens beyond max_pages pages, leaves out those
  *   positions and sets the optional device int32 *err to 1 (never cleared).
- *   A NaN or infinity in V of a position reaches every token of its sequence
- *   whose head reads the same tile, masked or not, unless the position is
- *   outside the reach of all of them.
+ *   A NaN or infinity in V reaches, beside the tokens that see its position,
+ *   others of the same call and KV head: of the sequence's tokens that are
+ *   computed together (at most 256 query rows), those that do not see a position
+ *   that another of them sees.  Positions that none of them sees reach nothing.
  *   Arithmetic: scores, maximum, sum and output are fp32; the probabilities
  *   enter the second product rounded once to the cache's type.  The split of
  *   the keys over CTAs depends on the lengths only: repeated calls give the
  *   same bits.
- *   ws: q4_workspace_bytes(Q4_OP_KV_ATTENTION, max_q * n_q / n_kv, head_dim,
- *   n_seqs * n_kv) bytes, contents on entry do not matter; calls that share
- *   one must not overlap.                                                  */
+ *   ws: kv_attention_ws_bytes() bytes, contents on entry do not matter; calls
+ *   that share one must not overlap.
+ *   The kernel for many query rows waits on the device (bounded:
+ *   q4_set_wait_limit, q4_device_status).                                  */
+size_t kv_attention_ws_bytes(int max_q, int n_q, int n_kv, int head_dim);
 int kv_attention(const q4_kv_cache* cache, int T, int max_q, const void* q,
                  long long q_stride, int n_q, float scale, int window, void* out,
                  float* lse_opt, int32_t* err, void* ws, size_t ws_bytes,
@@ -522,10 +524,8 @@ int q4_rmsnorm_f16(const float* in, int H, float eps, uint16_t* out_f16, q4_stre
 /* ---------------------------------------------------------------------- */
 /* Bytes of workspace an operation needs (0 = none).  Arguments per op:
  *   Q4_OP_GEMV (N, K, batch), Q4_OP_GEMM_CHUNK (N, K, 64), Q4_OP_PLE (S, D, L),
- *   Q4_OP_LMHEAD (V, K, b), Q4_OP_DECODE_PASS (H, max q+2kv rows, max mlp),
- *   Q4_OP_KV_ATTENTION (max_q * n_q / n_kv, head_dim, n_seqs * n_kv).
- * Depends on the current device's SM count for Q4_OP_LMHEAD and
- * Q4_OP_KV_ATTENTION; returns 0 when
+ *   Q4_OP_LMHEAD (V, K, b), Q4_OP_DECODE_PASS (H, max q+2kv rows, max mlp).
+ * Depends on the current device's SM count for Q4_OP_LMHEAD; returns 0 when
  * the current device cannot be queried.                                   */
 size_t q4_workspace_bytes(int op, int a, int b, int c);
 

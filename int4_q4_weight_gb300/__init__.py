@@ -21,17 +21,17 @@ __all__ = [
     "load", "build", "Q4Error", "q4_quantize", "q4_gemv", "q4_gemv_weights_ro", "q4_gemv_stage", "q4_rmsnorm_f16",
     "q4_decode_pass", "q4_decode_pass_launches", "q2_gemv", "lmhead_softcap_argmax", "ple_gather_project", "q4_gemm_chunk",
     "q8_quantize", "ple_gather_project_q8", "q4_gemv_a8", "q4_gemm_chunk_a8", "q4_act_calibrate_a8",
-    "kv_append", "kv_rope_steps", "kv_attention", "logits_sample",
+    "kv_append", "kv_rope_steps", "kv_attention", "kv_attention_ws", "logits_sample",
     "q4_workspace_bytes", "q4_version", "Q4_IN_F16", "Q4_IN_RMS_F16", "Q4_IN_RMS_F32",
     "Q4_IN_RMS2_F32", "Q4_OP_GEMV", "Q4_OP_GEMM_CHUNK", "Q4_OP_PLE", "Q4_OP_LMHEAD",
-    "Q4_OP_DECODE_PASS", "Q4_OP_KV_ATTENTION", "q4_layer", "q4_matrix", "q4_kv_cache",
+    "Q4_OP_DECODE_PASS", "q4_layer", "q4_matrix", "q4_kv_cache",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libq4w.so")
 
 Q4_IN_F16, Q4_IN_RMS_F16, Q4_IN_RMS_F32, Q4_IN_RMS2_F32 = 0, 1, 2, 3
-Q4_OP_GEMV, Q4_OP_GEMM_CHUNK, Q4_OP_PLE, Q4_OP_LMHEAD, Q4_OP_DECODE_PASS, Q4_OP_KV_ATTENTION = 0, 1, 2, 3, 4, 5
+Q4_OP_GEMV, Q4_OP_GEMM_CHUNK, Q4_OP_PLE, Q4_OP_LMHEAD, Q4_OP_DECODE_PASS = 0, 1, 2, 3, 4
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4_dtype
 
 _lib = None
@@ -82,6 +82,7 @@ _SIGS = {
     "kv_append": (ci, [vp, ci, vp, cll, vp, cll, ci, vp, cll, ci, vp, vp, ci, ci, vp, vp,
                        vp]),
     "kv_attention": (ci, [vp, ci, ci, vp, cll, ci, cf, ci, vp, vp, vp, vp, csz, vp]),
+    "kv_attention_ws_bytes": (csz, [ci, ci, ci, ci]),
     "logits_sample": (ci, [vp, cll, ci, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp]),
     "q4_workspace_bytes": (csz, [ci, ci, ci, ci]),
     "q4_status_string": (ctypes.c_char_p, [ci]),
@@ -607,7 +608,7 @@ assert _CACHE.size == ctypes.sizeof(q4_kv_cache)
 
 
 def _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens):
-    """The checked cache as (the bytes of its q4_kv_cache, its dtype, n_kv, head_dim, n_seqs)."""
+    """The checked cache as (the bytes of its q4_kv_cache, its dtype, n_kv, head_dim)."""
     dtype = k_cache.dtype
     if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise Q4Error(f"k_cache must be torch.float16 or torch.bfloat16, got {dtype}")
@@ -630,7 +631,7 @@ def _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens):
         _numel(cu_tokens, n + 1, "cu_tokens")
     pages, heads, page, dim = shape
     return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_tokens.data_ptr(),
-                       kv_lens.data_ptr(), _DTYPES[dtype], pages, heads, page, dim, n, tshape[1]), dtype, heads, dim, n
+                       kv_lens.data_ptr(), _DTYPES[dtype], pages, heads, page, dim, n, tshape[1]), dtype, heads, dim
 
 
 def kv_append(k, v, k_cache, v_cache, block_table, cu_tokens, kv_lens, steps=None, q=None, positions=None,
@@ -641,7 +642,7 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_tokens, kv_lens, steps=Non
     queries q [T, n_q, D] in the cache's type, or None without q.  kv_lens
     counts the new tokens already; see include/q4w.h for the layout."""
     lib = load()
-    cache, dtype, n_kv, D, _ = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
+    cache, dtype, n_kv, D = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
     T, kt = k.shape[0], k.dtype
     if kt not in _DTYPES:
         raise Q4Error(f"k must be float32, float16 or bfloat16, got {kt}")
@@ -679,13 +680,17 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_tokens, kv_lens, steps=Non
 
 
 @functools.lru_cache(maxsize=256)
-def _attention_ws_bytes(rows, head_dim, pairs, device):
-    return q4_workspace_bytes(Q4_OP_KV_ATTENTION, rows, head_dim, pairs)
+def _attention_ws_bytes(max_q, n_q, n_kv, head_dim, device):
+    n = load().kv_attention_ws_bytes(max_q, n_q, n_kv, head_dim)
+    if n == 0:
+        raise Q4Error(f"no workspace size for max_q={max_q}, n_q={n_q}, n_kv={n_kv}, head_dim={head_dim} on this device")
+    return n
 
 
-def kv_attention_ws(max_q, n_q, n_kv, head_dim, n_seqs, device):
+def kv_attention_ws(max_q, n_q, n_kv, head_dim, device):
+    """A workspace for kv_attention calls of these sizes that do not overlap."""
     device = torch.device(device)
-    n = _attention_ws_bytes(max_q * (n_q // n_kv), head_dim, n_seqs * n_kv, device.index)
+    n = _attention_ws_bytes(max_q, n_q, n_kv, head_dim, device.index)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
@@ -696,7 +701,7 @@ def kv_attention(q, k_cache, v_cache, block_table, cu_tokens, kv_lens, max_q=Non
     the new tokens of a sequence (None: T); scale None: 1/sqrt(D); window: how
     many positions a token sees (0: all); lse: f32 [T, n_q] to fill, or None."""
     lib = load()
-    cache, dtype, n_kv, D, n_seqs = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
+    cache, dtype, n_kv, D = _kv_cache(k_cache, v_cache, block_table, cu_tokens, kv_lens)
     if q.dim() != 3:
         raise Q4Error(f"q has shape {tuple(q.shape)}; [T, n_q, head_dim] is wanted")
     T, n_q, _ = q.shape
@@ -720,7 +725,7 @@ def kv_attention(q, k_cache, v_cache, block_table, cu_tokens, kv_lens, max_q=Non
     if n_q < 1 or n_q % n_kv:
         raise Q4Error(f"n_q={n_q} must be a multiple of n_kv={n_kv}")
     if ws is None:
-        ws = kv_attention_ws(max_q, n_q, n_kv, D, n_seqs, q.device)
+        ws = kv_attention_ws(max_q, n_q, n_kv, D, q.device)
     else:
         _dev(ws, torch.uint8, "ws")
     status = lib.kv_attention(cache, T, max_q, q.data_ptr(), qs, n_q, D ** -0.5 if scale is None else scale, window,

@@ -176,8 +176,7 @@ int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int 
   return e == cudaSuccess ? Q4_OK : cuda_fail(e, "attention join launch");
 }
 
-size_t attn_ws_bytes(int max_rows, int D, int n_seqs, const DeviceInfo& dev) {
-  (void)n_seqs;
+size_t attn_ws_bytes(int max_rows, int D, const DeviceInfo& dev) {
   return attn_decode_fits(max_rows, D) ? attn_decode_ws_bytes(max_rows, D, dev) : attn_tile_ws_bytes(D, dev);
 }
 

@@ -43,7 +43,7 @@
 
 #include "q4w_attn.cuh"
 #include "q4w_device.cuh"
-#include "q4w_tc.cuh"
+#include "q4w_tc_pair.cuh"
 
 namespace q4w {
 namespace tile {
@@ -198,6 +198,10 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
     tc::mbar_fence_init();
   }
   if (warp == kMmaWarp) tc::tmem_alloc_pair(tc::smem_u32(&tmem_sh), 512);
+  if (lane == 0 && (warp == kKWarp || warp == kVWarp || warp == kQWarp)) {
+    const CUtensorMap* m = warp == kKWarp ? &p.tm_k : warp == kVWarp ? &p.tm_v : &p.tm_q;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
   pdl_wait();
   pdl_trigger();
 

@@ -52,6 +52,7 @@
 
 #include "q4w_device.cuh"
 #include "q4w_internal.cuh"
+#include "q4w_kv.cuh"
 #include "q4w_tc.cuh"
 #include "q4w_top2.cuh"
 

@@ -119,15 +119,6 @@ int launch_gemv_batch_decoded(const uint8_t* codes, const __half* scales, const 
 int encode_tensor_2d(CUtensorMap* tm, const void* base, CUtensorMapDataType type, int esize, uint64_t cols,
                      uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle,
                      const char* what);
-// The same for a cache of `rows` rows of D 16-bit elements, seen as D/64 slabs
-// of 64 elements: boxes of box_rows rows of every slab in the 128-byte
-// swizzle, laid out slab after slab.
-int encode_cache_rows(CUtensorMap* tm, const void* base, bool bf16, int D, uint64_t rows, uint32_t box_rows,
-                      uint32_t box_slabs, const char* what);
-// Query rows [T][n_q][D] of 16-bit elements with a token stride, as D/64 slabs:
-// boxes of `tokens` tokens of `heads` heads of one slab, 128-byte swizzle.
-int encode_query_rows(CUtensorMap* tm, const void* base, bool bf16, int D, int n_q, int T, long long stride,
-                      uint32_t heads, uint32_t tokens);
 size_t gemm_ws_bytes(int K);   // the bf16 copy of X [64][K]
 // act_scale > 0: the w4a8 form -- the token operand is the activation codes
 // q = clamp(rint(x / act_scale), -128, 127) and Y is scaled by act_scale.

@@ -3,6 +3,7 @@
 // V, so the rows of one KV head inside a page are contiguous.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -53,7 +54,16 @@ int launch_kv_append(const q4_kv_cache& c, int T, const void* k, long long k_str
                      const DeviceInfo& dev, cudaStream_t s);
 // Workspace of an attention call whose sequences have up to max_rows query
 // rows (tokens x query heads) per KV head.
-size_t attn_ws_bytes(int max_rows, int D, int n_seqs, const DeviceInfo& dev);
+size_t attn_ws_bytes(int max_rows, int D, const DeviceInfo& dev);
+// Tensor map of a cache of `rows` rows of D 16-bit elements, seen as D/64 slabs
+// of 64 elements: boxes of box_rows rows of box_slabs slabs in the 128-byte
+// swizzle, laid out slab after slab.
+int encode_cache_rows(CUtensorMap* tm, const void* base, bool bf16, int D, uint64_t rows, uint32_t box_rows,
+                      uint32_t box_slabs, const char* what);
+// Query rows [T][n_q][D] of 16-bit elements with a token stride, as D/64 slabs:
+// boxes of `tokens` tokens of `heads` heads of one slab, 128-byte swizzle.
+int encode_query_rows(CUtensorMap* tm, const void* base, bool bf16, int D, int n_q, int T, long long stride,
+                      uint32_t heads, uint32_t tokens);
 // Few query rows per KV head (k_attn_decode.cu).
 bool attn_decode_fits(int max_rows, int D);
 size_t attn_decode_ws_bytes(int max_rows, int D, const DeviceInfo& dev);

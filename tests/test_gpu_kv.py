@@ -288,12 +288,21 @@ def test_attention_bad_pages_are_left_out(cuda_lib, new, D):
     check_attention(cuda_lib, c, err=1)
 
 
+@pytest.mark.parametrize("new,D", [(1, 256), (1, 64), (30, 256), (30, 512)])
+def test_attention_lengths_beyond_the_table(cuda_lib, new, D):
+    """A length that max_pages pages do not hold: the positions that they do hold."""
+    c = Case([new, new], [300, 50], 8, 1, D)
+    c.table[0] = c.table[0].clamp(min=0)
+    c.kvl[0] = 16 * c.max_pages + 5
+    check_attention(cuda_lib, c, err=1)
+
+
 @pytest.mark.parametrize("new,D", [(1, 256), (1, 512), (50, 256), (50, 512)])
 def test_attention_same_bits_again_streams_and_graphs(cuda_lib, new, D):
     q4w = cuda_lib
     c = Case([new] * 5, [new + x for x in (3000, 10, 555, 0, 1200)], 8, 1, D)
     out, lse = check_attention(q4w, c)
-    ws = q4w.kv_attention_ws(new, 8, 1, D, 5, "cuda")
+    ws = q4w.kv_attention_ws(new, 8, 1, D, "cuda")
     ws.fill_(0xFF)                                     # its contents do not matter
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
