@@ -69,6 +69,8 @@ struct Params {
   float* logprob;              // NULL: not written
   int V;
   int range;                   // indices per CTA of the cluster, a multiple of kSeg
+  int rows;
+  int order;                   // more rows than run at once: costly ones first
 };
 
 // Order-preserving integer of a logit: larger logit, larger key; 0 and -0 tie.
@@ -359,6 +361,7 @@ struct Shared {
     u64 seg[kMaxSegs];                         // masses of the segments
   };
   uint32_t tie[kMaxSegs];                      // elements equal to the threshold, per segment
+  int row;                                     // of this cluster, where costly rows go first
   float top;                                   // this CTA's maximum
   int first;                                   // its first index that holds the row's
   u64 mine;                                    // this CTA's mass of S
@@ -455,18 +458,47 @@ __device__ __forceinline__ u64 bin_mass(const uint32_t* eighth, u64 m, int n) {
   return (sh >= 24 ? a >> (sh - 24) : a << (24 - sh)) + (sh < 60 ? b >> sh : 0ull);
 }
 
+// The row of a cluster when there are more rows than run at once.  Rows cost up to
+// six times one another by what is asked of them, so each 512 go in three classes,
+// costly ones first: top-p over the whole row, other samples of a whole row, top-k
+// and greedy rows.  192 rows of 262144 with mixed settings, in the order given: an
+// SM works 64 % of the time, the rest is the wait for the last rows.
+__device__ __forceinline__ int row_in_order(const Params& p, Shared& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int base = (int)blockIdx.y & ~(kThr - 1), r = base + threadIdx.x;
+  int cls = 3;
+  if (r < p.rows) {
+    const float temp = p.temperature ? p.temperature[r] : 1.f, top_p = p.top_p ? p.top_p[r] : 1.f;
+    const int k = p.top_k ? p.top_k[r] : 0;
+    cls = !(temp > 0.f) || top_p <= 0.f || (k > 0 && k < p.V) ? 2 : top_p < 1.f ? 0 : 1;
+  }
+  const uint32_t b0 = __ballot_sync(0xffffffffu, cls == 0), b1 = __ballot_sync(0xffffffffu, cls == 1),
+                 b2 = __ballot_sync(0xffffffffu, cls == 2);
+  if (lane == 0) sh.red32[warp] = __popc(b0) | __popc(b1) << 10 | __popc(b2) << 20;   // 512 rows: 10 bits each
+  __syncthreads();
+  const uint32_t n = lane < kWarpsS ? sh.red32[lane] : 0u;
+  const uint32_t all = __reduce_add_sync(0xffffffffu, n), before = __reduce_add_sync(0xffffffffu, lane < warp ? n : 0u);
+  const uint32_t mine = cls == 0 ? b0 : cls == 1 ? b1 : b2;
+  int at = (before >> 10 * cls & 0x3ffu) + __popc(mine & ((1u << lane) - 1u));
+  if (cls > 0) at += all & 0x3ffu;
+  if (cls > 1) at += all >> 10 & 0x3ffu;
+  if (cls < 3 && base + at == (int)blockIdx.y) sh.row = r;
+  __syncthreads();
+  return sh.row;
+}
+
 template <typename T, bool KEEP>
 __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid_constant__ Params p) {
   __shared__ Shared sh;
   uint32_t rank, ctas;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
-  const int row = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) sh.n_list = 0, sh.first = 0x7fffffff;
   if (threadIdx.x < 8) sh.eighth[threadIdx.x] = kEighth[threadIdx.x];
   clear_bins(sh);
   pdl_wait();
+  const int row = p.order ? row_in_order(p, sh) : (int)blockIdx.y;
   const T* z = static_cast<const T*>(p.z) + row * p.stride;
   const bool vec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
   const int i0 = min((int)rank * p.range, p.V), i1 = min(i0 + p.range, p.V);
@@ -974,7 +1006,7 @@ static int launch(const Params& p, int rows, int cluster, bool keep, cudaStream_
 int launch_logits_sample(const void* z, long long stride, int dtype, int rows, int V, const float* u,
                          const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                          int32_t* token, float* logprob, const DeviceInfo& dev, cudaStream_t s) {
-  sample::Params p = {z, stride, u, temperature, top_k, top_p, min_p, token, logprob, V, 0};
+  sample::Params p = {z, stride, u, temperature, top_k, top_p, min_p, token, logprob, V, 0, rows, 0};
   // CTAs per row.  Few rows: eight, one CTA per SM with its part of the row in
   // registers (a cluster lies in one GPC, so not every SM can be used; 8 rows of
   // 262144: 15.9 us for top-64, 55 us for top-p, against 22 and 74 with four
@@ -989,6 +1021,7 @@ int launch_logits_sample(const void* z, long long stride, int dtype, int rows, i
   while (V > cluster * sample::kSeg * sample::kMaxSegs) cluster <<= 1;
   const int segs = (V + sample::kSeg * cluster - 1) / (sample::kSeg * cluster);
   p.range = segs * sample::kSeg;
+  p.order = rows * cluster > 2 * dev.sms && (temperature || top_k || top_p);
   const bool keep = few && p.range <= sample::kKeep * sample::kThr;
   return dtype == Q4_F32   ? sample::launch<float>(p, rows, cluster, keep, s)
          : dtype == Q4_F16 ? sample::launch<__half>(p, rows, cluster, keep, s)

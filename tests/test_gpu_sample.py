@@ -147,6 +147,19 @@ def test_rows_with_their_own_settings_strides_streams_graphs(cuda_lib):
     assert torch.equal(tok, tok2) and torch.equal(lp, lp2)
 
 
+@pytest.mark.parametrize("b,V", [(512, 100), (700, 300), (1025, 70), (90, 9000)])
+def test_more_rows_than_run_at_once(cuda_lib, b, V):
+    """Rows are then taken by their settings, not in their order."""
+    z, u = rows(b, V, seed=b)
+    g = np.random.default_rng(b)
+    pick = lambda x, dt: torch.tensor(g.choice(x, b), dtype=dt, device="cuda")   # noqa: E731
+    t, k, p = pick([0.0, 0.5, 1.0, 2.0], F32), pick([0, 0, 1, 5, 50], torch.int32), pick([0.0, 0.5, 0.9, 1.0, 1.0], F32)
+    check(cuda_lib, z, u, t, k, p, pick([0.0, 0.1], F32))
+    check(cuda_lib, z, u, t)
+    check(cuda_lib, z, u, k=k)
+    check(cuda_lib, z, u, p=p)
+
+
 def test_frequencies_follow_the_distribution(cuda_lib):
     """Evenly spread u: each token is drawn in proportion to its probability."""
     z = torch.tensor([0.1, 0.4, 0.1, 0.3, 0.1], device="cuda").log()
