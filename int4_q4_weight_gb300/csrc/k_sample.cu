@@ -459,18 +459,18 @@ __device__ __forceinline__ u64 bin_mass(const uint32_t* eighth, u64 m, int n) {
 }
 
 // The row of a cluster when there are more rows than run at once.  Rows cost up to
-// six times one another by what is asked of them, so each 512 go in three classes,
-// costly ones first: top-p over the whole row, other samples of a whole row, top-k
-// and greedy rows.  192 rows of 262144 with mixed settings, in the order given: an
+// seven times one another by what is asked of them, so each 512 go in four classes,
+// costly ones first: top-p over the whole row, other samples of a whole row, top-k,
+// greedy rows.  192 rows of 262144 with mixed settings, in the order given: an
 // SM works 64 % of the time, the rest is the wait for the last rows.
 __device__ __forceinline__ int row_in_order(const Params& p, Shared& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int base = (int)blockIdx.y & ~(kThr - 1), r = base + threadIdx.x;
-  int cls = 3;
+  int cls = 4;
   if (r < p.rows) {
     const float temp = p.temperature ? p.temperature[r] : 1.f, top_p = p.top_p ? p.top_p[r] : 1.f;
     const int k = p.top_k ? p.top_k[r] : 0;
-    cls = !(temp > 0.f) || top_p <= 0.f || (k > 0 && k < p.V) ? 2 : top_p < 1.f ? 0 : 1;
+    cls = !(temp > 0.f) || top_p <= 0.f || k == 1 ? 3 : k > 0 && k < p.V ? 2 : top_p < 1.f ? 0 : 1;
   }
   const uint32_t b0 = __ballot_sync(0xffffffffu, cls == 0), b1 = __ballot_sync(0xffffffffu, cls == 1),
                  b2 = __ballot_sync(0xffffffffu, cls == 2);
@@ -478,11 +478,14 @@ __device__ __forceinline__ int row_in_order(const Params& p, Shared& sh) {
   __syncthreads();
   const uint32_t n = lane < kWarpsS ? sh.red32[lane] : 0u;
   const uint32_t all = __reduce_add_sync(0xffffffffu, n), before = __reduce_add_sync(0xffffffffu, lane < warp ? n : 0u);
-  const uint32_t mine = cls == 0 ? b0 : cls == 1 ? b1 : b2;
-  int at = (before >> 10 * cls & 0x3ffu) + __popc(mine & ((1u << lane) - 1u));
+  const uint32_t mine = cls == 0 ? b0 : cls == 1 ? b1 : cls == 2 ? b2 : b0 | b1 | b2;
+  int at = __popc(mine & ((1u << lane) - 1u));   // of the class before this one
+  if (cls < 3) at += before >> 10 * cls & 0x3ffu;
+  else at = (int)threadIdx.x - at - (before & 0x3ffu) - (before >> 10 & 0x3ffu) - (before >> 20);
   if (cls > 0) at += all & 0x3ffu;
   if (cls > 1) at += all >> 10 & 0x3ffu;
-  if (cls < 3 && base + at == (int)blockIdx.y) sh.row = r;
+  if (cls > 2) at += all >> 20;
+  if (cls < 4 && base + at == (int)blockIdx.y) sh.row = r;
   __syncthreads();
   return sh.row;
 }
