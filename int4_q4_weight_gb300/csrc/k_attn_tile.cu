@@ -31,14 +31,21 @@
 // The softmax is written to be short: a path that is taken once per item and
 // unrolled to hundreds of instructions cost 20000 cycles of instruction fetches.
 // K and V have a ring of slots each, so that the next keys load while the values
-// wait for P: K slots of [64 keys][<= 128 dims], V slots of [64 or 128 keys][128
-// or 64 columns], loaded in boxes of 16 to 64 rows (the page size's share),
-// 128-byte swizzle.
+// wait for P: K slots of [64 keys][<= 256 dims], V slots of [128 keys][<= 128
+// columns], loaded in boxes of 16 to 64 rows (the page size's share), 128-byte
+// swizzle.  A slot is as large as the ring allows: waiting for one and releasing
+// it costs the issuing thread about 100 cycles.
 //
 // Split: the steps of all items (sequence, KV head, tile) form one line that is
 // cut into equal shares, one CTA per SM; causal tiles of any length and ragged
 // sequences balance, and a short chunk over a long cache is split along the
 // keys.  Parts are joined by a second kernel in the order of the keys.
+//
+// Measured: four ragged prompts of up to 4096 tokens over contexts of up to 8192
+// (8 query heads on 1 KV head of 256, 326 GFLOP): 215 us with the join, 1.5
+// PFLOP/s, the tensor pipe active for 80 % of the cycles of the busy SMs.  A step
+// takes 2350 cycles; what else is lost lies at the ends of items, where O is read
+// out before the next item may write it, and in the join.
 #include <cuda.h>
 
 #include "q4w_attn.cuh"

@@ -16,6 +16,10 @@
 // of the token that the thread takes.  The rows are loaded one ahead, the first
 // before the position is looked up: those lookups are three loads one after the
 // other, and while they run nothing else would be in flight.
+//
+// Measured: 16 ragged prompts, 41000 tokens of 8 + 2 rows of 256, bf16 (421 MB):
+// 76 us, 5.5 TB/s, half of it writes.  Blocks of 128 threads so that few finish
+// late; more resident blocks, or two rows ahead, were slower.  8 tokens: 3.2 us.
 #include "q4w_device.cuh"
 #include "q4w_internal.cuh"
 #include "q4w_kv.cuh"

@@ -34,8 +34,8 @@
 //      order-preserving integer key (1024 sub-bins a level) until the
 //      threshold is a single key; then masses of 128-index segments, a scan of
 //      them, and the one segment that holds the target.
-// The row is read from HBM once; the later passes find it in L2, with 16-byte
-// loads, four in flight a thread.
+// The row is read from HBM once; the later passes find it in registers (few rows)
+// or in L2.
 #include <math_constants.h>
 
 #include "q4w_device.cuh"
