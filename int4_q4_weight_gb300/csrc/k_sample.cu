@@ -81,6 +81,9 @@ __device__ __forceinline__ uint32_t key_of(float z) {
 __device__ __forceinline__ float logit_of(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
+// The upper end of a range of keys as a logit.  The key below 0's is -0's, which no
+// logit has, and a comparison with -0 would let 0 in.
+__device__ __forceinline__ float logit_below(uint32_t k) { return logit_of(k == 0x7fffffffu ? k - 1 : k); }
 
 // What turns a logit of this row into a weight.
 struct Scale {
@@ -795,7 +798,7 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
         clear_bins(sh);
         __syncthreads();
         // (on the logits: the key of a NaN lies outside)
-        const float v_lo = logit_of(k_lo), v_hi = logit_of(k_hi);
+        const float v_lo = logit_of(k_lo), v_hi = logit_below(k_hi);
         part.rare([&](float v) { v = capped(s, v); return v >= v_lo && v <= v_hi; }, [&](float v, int) {
           v = capped(s, v);
           const int b = (int)((k_hi - key_of(v)) >> shift);

@@ -117,6 +117,23 @@ def test_signed_zeros_tie(cuda_lib):
         assert int(tok) == want
 
 
+def test_borders_next_to_zero(cuda_lib):
+    """The border among the smallest negative numbers, with zeros of both signs above."""
+    V = 12000
+    z = torch.full((16, V), -30.0, device="cuda")
+    u = torch.linspace(0.01, 0.99, 16, device="cuda")
+    for i in range(16):
+        z[i, 0] = 0.03 + 0.0013 * i   # the first bin ends at another key each time
+        z[i, 1:3000], z[i, 3000:4000] = 0.0, -0.0
+        for j in range(4):
+            z[i, 4000 + 1000 * j:5000 + 1000 * j] = -(j + 1) * 2.0 ** -149
+    for k in (4500, 5500, 6500, 7500):
+        check(cuda_lib, z, u, k=k)
+        check(cuda_lib, z, u, k=k, p=0.9)
+    for p in (0.45, 0.55, 0.7, 0.8):
+        check(cuda_lib, z, u, p=p)
+
+
 def test_rows_with_their_own_settings_strides_streams_graphs(cuda_lib):
     q4w = cuda_lib
     z, u = rows(9, 30007, seed=11)
