@@ -34,6 +34,13 @@
 //      order-preserving integer key (1024 sub-bins a level) until the
 //      threshold is a single key; then masses of 128-index segments, a scan of
 //      them, and the one segment that holds the target.
+//   E  top-p without top-k goes by the mass of the whole row.  Instead of B to D:
+//      a histogram of short weights bounds where the border lies; when at most
+//      2048 elements lie there, one pass forms the exact mass of the row and of
+//      the segments above them, and the leader sorts those few and cuts.
+//      (Exact weights are formed once, not twice, and a bin is one atomic
+//      addition, not three: 8 rows of 262144, top-p 0.9: 42 us, by B to D 53;
+//      192 rows 300 against 388.  The code costs top-64 of a few rows 1.3 us.)
 // The row is read from HBM once; the later passes find it in registers (few rows)
 // or in L2.
 #include <math_constants.h>
@@ -373,6 +380,12 @@ struct Shared {
   u64 red[kWarpsS];
   uint32_t red32[kWarpsS];
   u64 scan_total;
+  // a range of bins or keys that holds the border of top-p
+  int j_lo, j_hi;
+  u64 c_lo, c_hi, m_lo;
+  // of the leader: the last kept element of its list, and how many are kept
+  u64 last_kept;
+  int n_kept;
   uint32_t eighth[8];
   // the crossing bin of a scan
   int cross_bin;
@@ -459,6 +472,124 @@ __device__ __forceinline__ u64 bin_mass(const uint32_t* eighth, u64 m, int n) {
   const int sh = 17 + (n >> 3);
   if (sh > 80) return 0ull;
   return (sh >= 24 ? a >> (sh - 24) : a << (24 - sh)) + (sh < 60 ? b >> sh : 0ull);
+}
+
+// The smallest key in [-inf, top] whose logit `ok` holds for; it holds for the top
+// and, once it holds, for everything above.  A 32-way search, the same in each warp.
+template <typename F>
+__device__ __forceinline__ uint32_t smallest_key(const Scale& s, F ok) {
+  const int lane = threadIdx.x & 31;
+  uint32_t a = key_of(-CUDART_INF_F), b = key_of(s.top);
+  while (a < b) {
+    const uint32_t span = b - a, part = span / 32 + 1;
+    const uint32_t k = min(a + part * lane, b);
+    const uint32_t yes = __ballot_sync(0xffffffffu, k == b || ok(logit_of(k)));
+    const int f = yes ? __ffs(yes) - 1 : 32;   // the first that qualifies
+    const uint32_t below = __shfl_sync(0xffffffffu, k, f > 0 ? f - 1 : 0), at = __shfl_sync(0xffffffffu, k, f & 31);
+    if (yes) b = at;
+    if (f > 0) a = below + 1;
+  }
+  return b;
+}
+__device__ __forceinline__ uint32_t first_key(const Scale& s, float edge) {   // of the bins before `edge`
+  return smallest_key(s, [&](float v) { return eighths(s, v) < edge; });
+}
+__device__ __noinline__ uint32_t minp_key(const uint32_t* eighth, Scale s) {
+  return smallest_key(s, [&](float v) { return passes_minp(eighth, s, v); });
+}
+
+// 2^(x / 8), to 22 bits.
+__device__ __forceinline__ float ex2_eighth(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 0.125f));
+  return r;
+}
+
+// Top-p over a whole row: a range of keys [*k_lo, *k_hi], at most kCap elements,
+// that holds the border, from masses with error bounds.  False where kCap elements
+// lie closer to the border than the bounds: many ties, or p next to 1.
+//
+// A weight enters with 14 to 16 bits, rounded (as many as the sum of a CTA's part
+// leaves of 32), so that a bin is one atomic addition; its error, that of 8 t in
+// fp32 and of ex2.approx are below eps of it.  The prefix masses are exact sums.
+template <typename T, bool KEEP>
+__device__ __forceinline__ bool narrow(const Part<T, KEEP>& part, Shared& sh, const Scale& s, float top_p, int range,
+                                       uint32_t ctas, uint32_t* k_lo_out, uint32_t* k_hi_out) {
+  const int lane = threadIdx.x & 31, b0 = 2 * threadIdx.x;
+  const int bits = min(31 - (32 - __clz(range - 1)), 16);
+  const float unit = (float)(1 << bits), eps = 0.6f / unit + 1.6e-5f;
+  part.heavy([&](float v, int) {
+    const float q = eighths(s, capped(s, v));
+    if (q < (float)kBins) {
+      float nf;
+      const int n = whole(q, &nf);
+      atomicAdd(&sh.cnt[n], __float_as_uint(fmaf(ex2_eighth(nf - q), unit, 8388608.f)) & 0x7fffffu);
+    }
+  });
+  if (threadIdx.x == 0) sh.j_lo = sh.j_hi = kBins - 1;
+  cluster_sync();
+  u64 c[2], m[2], tot, all;
+  merge_bins(sh, ctas, false, c, m);
+  u64 w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) w[j] = bin_mass(sh.eighth, c[j] << (28 - bits), b0 + j);
+  const u64 w_in = block_incl(w[0] + w[1], sh.red, &tot), c_in = block_incl(c[0] + c[1], sh.red, &all);
+  // what the exact p mass(row) lies between; the cutting of weights to 2^-42 is below 2^-22 of the mass
+  const float want = top_p * (float)tot, cut = 3e-7f * (float)tot;
+  const float want_lo = want * (1.f - eps) - cut, want_hi = want * (1.f + eps) + cut;
+  // the first bins where S_p may end and where it must have ended
+  auto find = [&](bool lo0, bool lo1, bool hi0, bool hi1) {
+    const int lo = __reduce_min_sync(0xffffffffu, lo0 ? b0 : lo1 ? b0 + 1 : kBins - 1);
+    const int hi = __reduce_min_sync(0xffffffffu, hi0 ? b0 : hi1 ? b0 + 1 : kBins - 1);
+    if (lane == 0) atomicMin(&sh.j_lo, lo), atomicMin(&sh.j_hi, hi);
+    __syncthreads();
+  };
+  {
+    const float w0 = (float)(w_in - w[1]), w1 = (float)w_in;
+    find(w0 * (1.f + eps) >= want_lo, w1 * (1.f + eps) >= want_lo, w0 * (1.f - eps) >= want_hi, w1 * (1.f - eps) >= want_hi);
+  }
+  const int bin = sh.j_lo, bin_hi = sh.j_hi;
+  if ((bin & ~1) == b0) sh.c_lo = bin & 1 ? c_in - c[1] : c_in - c[1] - c[0], sh.m_lo = bin & 1 ? w_in - w[1] : w_in - w[1] - w[0];
+  if ((bin_hi & ~1) == b0) sh.c_hi = bin_hi & 1 ? c_in : c_in - c[1];
+  __syncthreads();
+  u64 inside = (u64)((float)(sh.c_hi - sh.c_lo) / (0.91f * unit)) + 1;   // at most: a weight is 0.917 units or more
+  float m_lo = (float)sh.m_lo * (1.f - eps), m_hi = (float)sh.m_lo * (1.f + eps);   // the mass before the range
+  uint32_t k_lo = first_key(s, (float)(bin_hi + 1)), k_hi = bin == 0 ? key_of(s.top) : first_key(s, (float)bin) - 1;
+  // three levels of 1024 reach single keys from any range; a level may also take
+  // less off, where the bounds are wide
+  for (int level = 0; inside > (u64)kCap; ++level) {
+    if (level == 3) return false;
+    int shift = 0;
+    while (((k_hi - k_lo) >> shift) >= (uint32_t)kBins) ++shift;
+    cluster_sync();   // every CTA has read the last histogram
+    clear_bins(sh);
+    if (threadIdx.x == 0) sh.j_lo = sh.j_hi = kBins - 1;
+    __syncthreads();
+    const float v_lo = logit_of(k_lo), v_hi = logit_below(k_hi);
+    part.rare([&](float v) { v = capped(s, v); return v >= v_lo && v <= v_hi; }, [&](float v, int) {
+      v = capped(s, v);
+      const uint32_t b = (k_hi - key_of(v)) >> shift;
+      atomicAdd(&sh.cnt[b], 1u);
+      atomicAdd(&sh.lo[b], (uint32_t)(ex2_eighth(fminf((float)bin - eighths(s, v), 0.f)) * 16384.f));   // cut off: within 1
+    });
+    cluster_sync();
+    merge_bins(sh, ctas, true, c, m);
+    const u64 ci = block_incl(c[0] + c[1], sh.red, &all), mi = block_incl(m[0] + m[1], sh.red, &all);
+    auto low = [&](u64 sum) { return m_lo + (float)bin_mass(sh.eighth, sum << 14, bin) * (1.f - 2e-5f); };
+    auto high = [&](u64 sum, u64 n) { return m_hi + (float)bin_mass(sh.eighth, (sum + n) << 14, bin) * (1.f + 2e-5f); };
+    find(high(mi - m[1], ci - c[1]) >= want_lo, high(mi, ci) >= want_lo, low(mi - m[1]) >= want_hi, low(mi) >= want_hi);
+    const int last = (int)((k_hi - k_lo) >> shift), lo = min(sh.j_lo, last), hi = min(sh.j_hi, last);
+    if ((lo & ~1) == b0) sh.c_lo = lo & 1 ? ci - c[1] : ci - c[1] - c[0], sh.m_lo = lo & 1 ? mi - m[1] : mi - m[1] - m[0];
+    if ((hi & ~1) == b0) sh.c_hi = hi & 1 ? ci : ci - c[1];
+    __syncthreads();
+    inside = sh.c_hi - sh.c_lo;
+    m_hi = high(sh.m_lo, sh.c_lo), m_lo = low(sh.m_lo);
+    const uint32_t to_lo = (uint32_t)(hi + 1) << shift;   // 0: 2^32
+    if (k_hi - k_lo >= to_lo && to_lo != 0) k_lo = k_hi - to_lo + 1;
+    k_hi -= (uint32_t)lo << shift;
+  }
+  *k_lo_out = k_lo, *k_hi_out = k_hi;
+  return true;
 }
 
 // The row of a cluster when there are more rows than run at once.  Rows cost up to
@@ -566,7 +697,15 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
   u64 total = 0;                 // mass of the row (top-p without top-k)
   u64 cnt[2] = {0, 0}, mant[2] = {0, 0};   // this thread's two bins of the row's histogram
   const bool row_mass = has_p && !has_k;
-  if (has_k || has_p || has_m) {
+  // E's first half: the range of keys that holds the border
+  uint32_t near_lo = 0, near_hi = 0;
+  const bool near = row_mass && narrow(part, sh, s, top_p, p.range, ctas, &near_lo, &near_hi);
+  if (row_mass && !near) {
+    cluster_sync();   // every CTA has read the last histogram
+    clear_bins(sh);
+    __syncthreads();
+  }
+  if (!near && (has_k || has_p || has_m)) {
     // ---- B: histogram over the row, with masses for top-p without top-k
     // (which goes by the mass of the whole row)
     if (row_mass) {
@@ -724,7 +863,7 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
   // thr_ties (by index) of those equal to it.
   uint32_t thr_key = 0;
   u64 thr_ties = ~0ull;
-  if (has_k || has_p) {
+  if (!near && (has_k || has_p)) {
     if (has_p && has_k) {   // the masses too, up to the last bin that matters
       cluster_sync();       // every CTA has read the counts
       clear_bins(sh);
@@ -767,28 +906,11 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
         return;
       }
       u64 c_before = sh.cross_cnt, m_before = sh.cross_mass;
-      // the keys of the bin: eighths() is monotone in the logit, so they are a
-      // range; each warp finds its ends by a 32-way search
+      // the keys of the bin: eighths() is monotone in the logit, so they are a range
       uint32_t k_lo, k_hi;   // keys of the bin: [k_lo, k_hi]
       {
-        const uint32_t top_key = key_of(s.top), inf_key = key_of(-CUDART_INF_F);
-        // the smallest key in [inf_key, top_key] whose logit lies below `edge` eighths
-        auto first_key = [&](float edge) {
-          uint32_t a = inf_key, b = top_key;   // b qualifies
-          while (a < b) {
-            const uint32_t span = b - a, part = span / 32 + 1;
-            const uint32_t k = min(a + part * lane, b);
-            const float q = eighths(s, logit_of(k));
-            const uint32_t yes = __ballot_sync(0xffffffffu, q < edge || k == b);
-            const int f = yes ? __ffs(yes) - 1 : 32;   // the first that qualifies
-            const uint32_t below = __shfl_sync(0xffffffffu, k, f > 0 ? f - 1 : 0), at = __shfl_sync(0xffffffffu, k, f & 31);
-            if (yes) b = at;
-            if (f > 0) a = below + 1;
-          }
-          return b;
-        };
-        k_lo = first_key((float)(bin + 1));
-        k_hi = bin == 0 ? top_key : first_key((float)bin) - 1;
+        k_lo = first_key(s, (float)(bin + 1));
+        k_hi = bin == 0 ? key_of(s.top) : first_key(s, (float)bin) - 1;
       }
       for (;;) {
         const uint32_t width = k_hi - k_lo;   // keys - 1
@@ -869,6 +991,8 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
   cluster_sync();   // sh.list / sh.seg are free, every histogram read
   const int n_seg = (i1 - i0 + kSeg - 1) / kSeg;
   const bool cuts = thr_key != 0;
+  u64* const seg = near ? reinterpret_cast<u64*>(sh.cnt) : sh.seg;   // (the list is in use beside it)
+  static_assert(sizeof(sh.cnt) + sizeof(sh.lo) == sizeof(sh.seg) && offsetof(Shared, lo) == sizeof(sh.cnt), "two rows of bins");
   const float cut = cuts ? logit_of(thr_key) : -CUDART_INF_F;   // (copies: descend() holds references to the others)
   const u64 cut_ties = thr_ties;
   auto kept = [&](float v) { return v > cut && (!has_m || passes_minp(sh.eighth, s, v)); };
@@ -879,7 +1003,100 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = capped(s, v[k]);
   };
-  {
+  // the sum of the lanes' masses, each below 2^45: two pieces of 23 bits
+  auto lanes_sum = [](u64 v) {
+    const u64 lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7fffffu);
+    return lo + ((u64)__reduce_add_sync(0xffffffffu, (uint32_t)(v >> 23)) << 23);
+  };
+  // near: kept is what lies above the range that holds the border, and the first of the range
+  const float v_min = near && has_m ? logit_of(minp_key(sh.eighth, s)) : -CUDART_INF_F, v_hi = logit_below(near_hi);
+  auto above_range = [&](float v) { return v > v_hi && v >= v_min; };
+  u64 last_kept = 0;
+  if (near) {
+    // ---- E: the mass of the row, those above the range, and its elements to the leader
+    const float v_lo = fmaxf(logit_of(near_lo), v_min);
+    const uint32_t list0 = tc::cluster_addr(sh.list, 0), count0 = tc::cluster_addr(&sh.n_list, 0);
+    u64 row_part = 0;
+    float next[4];
+    load4(warp, next);
+#pragma unroll 1
+    for (int g = warp; g < n_seg; g += kWarpsS) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = next[k];
+      load4(g + kWarpsS, next);
+      u64 sum = 0;
+      bool any = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const u64 wk = weight(sh.eighth, s, v[k]);
+        row_part += wk;
+        sum += above_range(v[k]) ? wk : 0ull;
+        any |= v[k] <= v_hi && v[k] >= v_lo;
+      }
+      if (any) {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const float x = k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
+          if (!(x <= v_hi && x >= v_lo)) continue;
+          uint32_t at;
+          asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(count0) : "memory");
+          const u64 c = ((u64)~key_of(x) << 32) | (uint32_t)(i0 + g * kSeg + 4 * lane + k);
+          if (at < (uint32_t)kCap) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list0 + 8 * at), "l"(c) : "memory");
+        }
+      }
+      __syncwarp();
+      sum = lanes_sum(sum);
+      if (lane == 0) seg[g] = sum;
+    }
+    __syncthreads();
+    u64 above = 0, cta_row, cta_above;
+    for (int g = threadIdx.x; g < n_seg; g += kThr) above += seg[g];
+    block_incl(row_part, sh.red, &cta_row);
+    block_incl(above, sh.red, &cta_above);
+    if (threadIdx.x == 0) sh.mine = cta_row, sh.ties = cta_above;
+    cluster_sync();
+    u64 unused;
+    const u64 row = cluster_sum(&sh.mine, rank, ctas, &unused);
+    above = cluster_sum(&sh.ties, rank, ctas, &unused);
+    if (rank == 0) {
+      const int n = (int)min(sh.n_list, (uint32_t)kCap);
+      int n2 = 64;
+      while (n2 < n) n2 <<= 1;
+      for (int i = n + threadIdx.x; i < n2; i += kThr) sh.list[i] = ~0ull;
+      bitonic(sh.list, n2);
+      constexpr int kPer = kCap / kThr;
+      u64 w[kPer], sum = 0, t;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = kPer * threadIdx.x + j;
+        w[j] = i < n ? weight(sh.eighth, s, logit_of(~(uint32_t)(sh.list[i] >> 32))) : 0ull;
+        sum += w[j];
+      }
+      u64 before = above + block_incl(sum, sh.red, &t) - sum;
+      const u64 limit = max(times(row, top_p, true), 1ull);
+      int keep = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        keep += kPer * (int)threadIdx.x + j < n && before < limit;
+        before += w[j];
+      }
+      keep = (int)__reduce_add_sync(0xffffffffu, (unsigned)keep);
+      if (threadIdx.x == 0) sh.n_kept = 0;
+      __syncthreads();
+      if (lane == 0) atomicAdd(&sh.n_kept, keep);
+      __syncthreads();
+      if (threadIdx.x == 0) sh.last_kept = sh.n_kept ? sh.list[sh.n_kept - 1] : 0ull;
+    }
+    cluster_sync();
+    const int n_kept = (int)ld_cluster_u32(tc::cluster_addr(&sh.n_kept, 0));
+    last_kept = ld_cluster_u64(tc::cluster_addr(&sh.last_kept, 0));
+    for (int i = threadIdx.x; i < n_kept; i += kThr) {
+      const u64 c = ld_cluster_u64(tc::cluster_addr(&sh.list[i], 0));
+      const int at = (int)(uint32_t)c - i0;
+      if (at >= 0 && at < i1 - i0) atomicAdd(&seg[at / kSeg], weight(sh.eighth, s, logit_of(~(uint32_t)(c >> 32))));
+    }
+  } else {
     float next[4];
     load4(warp, next);
 #pragma unroll 1
@@ -896,24 +1113,22 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
         sum += kept(v[k]) ? wk : 0ull;
         ties += tied(v[k]);
       }
-      // the lanes' sums are below 2^45: two pieces of 23 bits
-      const u64 lo = __reduce_add_sync(0xffffffffu, (uint32_t)sum & 0x7fffffu);
-      const u64 hi = __reduce_add_sync(0xffffffffu, (uint32_t)(sum >> 23));
+      sum = lanes_sum(sum);
       ties = __reduce_add_sync(0xffffffffu, ties);
-      if (lane == 0) sh.seg[g] = lo + (hi << 23), sh.tie[g] = ties;
+      if (lane == 0) seg[g] = sum, sh.tie[g] = ties;
     }
   }
   __syncthreads();
   // prefix of the ties: how many of a segment's are kept
   constexpr int kPerS = kMaxSegs / kThr;
   u64 t_sum = 0, m_sum = 0;
-  for (int j = 0; j < kPerS; ++j) {
-    const int g = threadIdx.x * kPerS + j;
-    if (g < n_seg) t_sum += sh.tie[g], m_sum += sh.seg[g];
-  }
-  u64 cta_ties, cta_mass;
-  u64 t_run = block_incl(t_sum, sh.red, &cta_ties) - t_sum;
+  u64 cta_ties, cta_mass, t_run = 0;
   if (cuts) {   // else nothing is tied
+    for (int j = 0; j < kPerS; ++j) {
+      const int g = threadIdx.x * kPerS + j;
+      if (g < n_seg) t_sum += sh.tie[g];
+    }
+    t_run = block_incl(t_sum, sh.red, &cta_ties) - t_sum;
     if (threadIdx.x == 0) sh.ties = cta_ties;
     cluster_sync();
     u64 before;
@@ -926,10 +1141,12 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
   for (int j = 0; j < kPerS; ++j) {
     const int g = threadIdx.x * kPerS + j;
     if (g < n_seg) {
-      const u64 left = cut_ties > t_run ? cut_ties - t_run : 0ull;
-      t_run += sh.tie[g];
-      sh.seg[g] += w_tie * min((u64)sh.tie[g], left);
-      m_sum += sh.seg[g];
+      if (cuts) {
+        const u64 left = cut_ties > t_run ? cut_ties - t_run : 0ull;
+        t_run += sh.tie[g];
+        seg[g] += w_tie * min((u64)sh.tie[g], left);
+      }
+      m_sum += seg[g];
     }
   }
   u64 m_run = block_incl(m_sum, sh.red, &cta_mass) - m_sum;
@@ -945,13 +1162,13 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
   for (int j = 0; j < kPerS; ++j) {
     const int g = threadIdx.x * kPerS + j;
     if (g < n_seg) {
-      if (m_run <= goal && m_run + sh.seg[g] > goal) {
+      if (m_run <= goal && m_run + seg[g] > goal) {
         sh.cross_bin = g;
         sh.cross_mass = m_run;
         sh.scan_total = t_run;
       }
-      m_run += sh.seg[g];
-      t_run += sh.tie[g];
+      m_run += seg[g];
+      t_run += cuts ? sh.tie[g] : 0u;
     }
   }
   __syncthreads();
@@ -966,7 +1183,9 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
     u64 t_at = sh.scan_total + warp_incl(ties) - ties;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      w[k] = kept(v[k]) ? weight(sh.eighth, s, v[k]) : 0ull;
+      const u64 c = (u64)~key_of(v[k]) << 32 | (uint32_t)(i + k);
+      const bool in = near ? above_range(v[k]) || (v[k] <= v_hi && c <= last_kept) : kept(v[k]);
+      w[k] = in ? weight(sh.eighth, s, v[k]) : 0ull;
       if (tied(v[k])) w[k] = t_at++ < cut_ties ? w_tie : 0ull;
       sum += w[k];
     }

@@ -117,6 +117,20 @@ def test_signed_zeros_tie(cuda_lib):
         assert int(tok) == want
 
 
+@pytest.mark.parametrize("V", [300, 5000, 60000, 262144])
+def test_top_p_over_whole_rows(cuda_lib, V):
+    """Borders from the first element to the last, spread and peaked rows, with min-p above and below the border."""
+    z, u = rows(4, V, seed=V + 1)
+    z[2] *= 3.0
+    z[3] = (z[3] * 4).round() / 4
+    for p in (1e-30, 1e-6, 0.01, 0.3, 0.9, 0.99, 0.999, 0.99999, 1 - 2.0 ** -24)[::1 if V < 200000 else 3]:
+        check(cuda_lib, z, u, p=p)
+        check(cuda_lib, z, u, p=p, t=2.5)
+    for m in (1e-5, 0.003, 0.02, 0.3, 1.0)[::1 if V < 200000 else 2]:
+        check(cuda_lib, z, u, p=0.7, m=m)
+        check(cuda_lib, z, u, p=0.98, m=m, t=1.5)
+
+
 def test_borders_next_to_zero(cuda_lib):
     """The border among the smallest negative numbers, with zeros of both signs above."""
     V = 12000
