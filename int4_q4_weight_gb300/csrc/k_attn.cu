@@ -5,18 +5,20 @@
 namespace q4w {
 namespace attn {
 
-// Task: 8 rows (32 when P is 1) of one recorded item and 256 / P of their elements; P groups of
-// threads take every P-th part (P = 1, 4 or 16: two parts of a tile are read by
-// as many threads as there are elements; the 152 parts of the few rows of a
-// single long sequence by 16 groups side by side, as there are no other tasks:
-// 16 us with 4 groups, 8 with 16; tiles have tasks enough, 17 us against 23).  Every block reads all the
-// records, so the tasks of the few items that were split spread over the device
-// whatever CTA recorded them.
+// Task: 8 rows (32 when P is 1) of one recorded item and 256 / P of their elements;
+// P groups of threads take every P-th part: P = 1, 4 or 16.  Two parts of a tile
+// are read by as many threads as there are elements where tiles give tasks enough
+// (17 us against 23 with 4 groups), by 4 groups where there are few items (one
+// chunk of 64 tokens over 512 keys, with the pass: 16 us against 20).  The 152
+// parts of the few rows of a single long sequence are read by 16 groups side by
+// side, as there are no other tasks: 16 us with 4 groups, 8 with 16.  Every block
+// reads all the records, so the tasks of the few items that were split spread over
+// the device whatever CTA recorded them.
 constexpr int kJoinThr = 512;
 
 // log2 of P; lg_dv: log2 of the columns.
-__device__ __forceinline__ int join_groups(int parts, int used, int lg_dv) {
-  return max(parts <= 4 ? 0 : parts > 16 && used <= 16 ? 4 : 2, 8 - lg_dv);
+__device__ __forceinline__ int join_groups(int parts, int used, int lg_dv, bool few) {
+  return max(parts <= 4 ? few ? 2 : 0 : parts > 16 && used <= 16 ? 4 : 2, 8 - lg_dv);
 }
 
 // Sums of what a thread has of a row, scaled to a running maximum (units of log2 e).
@@ -34,7 +36,7 @@ struct JoinSum {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThr, 2) join_kernel(const AttnSplit p, int n_recs, int R, int n_q, int rows, int D, int dv,
+__global__ void __launch_bounds__(kJoinThr, 2) join_kernel(const AttnSplit p, int n_recs, int R, int n_q, int rows, int D, int dv, bool few,
                                                         void* out_, float* lse) {
   __shared__ float4 sum_sh[kJoinThr];
   __shared__ float2 ml_sh[16][8];
@@ -49,7 +51,7 @@ __global__ void __launch_bounds__(kJoinThr, 2) join_kernel(const AttnSplit p, in
     if (threadIdx.x < n_recs) {
       const SplitRec r = p.recs[threadIdx.x];
       rec_sh[threadIdx.x] = r;
-      const int g = join_groups(r.last - (int)threadIdx.x / R + 1, r.used, lg_dv), lg_rows = g == 0 ? 5 : 3;
+      const int g = join_groups(r.last - (int)threadIdx.x / R + 1, r.used, lg_dv, few), lg_rows = g == 0 ? 5 : 3;
       n = r.last < 0 ? 0 : ((r.used + (1 << lg_rows) - 1) >> lg_rows) << (lg_dv + g - 8);
     }
     int incl = n;
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(kJoinThr, 2) join_kernel(const AttnSplit p, in
     }
     const SplitRec rec = rec_sh[lo];
     const int c0 = lo / R, sub = task - first_sh[lo], np = rec.last - c0 + 1;
-    const int lg = join_groups(np, rec.used, lg_dv), groups = 1 << lg, lg_cols = lg_dv + lg - 8;
+    const int lg = join_groups(np, rec.used, lg_dv, few), groups = 1 << lg, lg_cols = lg_dv + lg - 8;
     const int part = threadIdx.x >> (9 - lg), dl = (threadIdx.x >> 3) & ((64 >> lg) - 1);
     const int d = (((sub & ((1 << lg_cols) - 1)) << (6 - lg)) + dl) * 4;
     // row `rr` of the task's first 8: of part 0, and of part i >= 1 at i - 1 steps
@@ -161,6 +163,9 @@ __global__ void __launch_bounds__(kJoinThr, 2) join_kernel(const AttnSplit p, in
 int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int D, int dv, bool bf16, int grid, int R,
                      cudaStream_t s) {
   if (grid > attn::kJoinThr) return fail(Q4_ERR_SHAPE, "attention: %d SMs are more than the join handles", grid);
+  // items of the call, about: few when their tasks of 32 rows leave most blocks idle
+  const long long items = ((long long)a.T * a.n_q / rows + (long long)a.kv.n_seqs * a.kv.n_kv) * (D / dv);
+  const bool few = items * 8 <= 2 * grid;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * grid);
   cfg.blockDim = dim3(attn::kJoinThr);
@@ -171,8 +176,8 @@ int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int 
   cfg.attrs = at;
   cfg.numAttrs = 1;
   const cudaError_t e =
-      bf16 ? cudaLaunchKernelEx(&cfg, attn::join_kernel<__nv_bfloat16>, split, grid, R, a.n_q, rows, D, dv, a.out, a.lse)
-           : cudaLaunchKernelEx(&cfg, attn::join_kernel<__half>, split, grid, R, a.n_q, rows, D, dv, a.out, a.lse);
+      bf16 ? cudaLaunchKernelEx(&cfg, attn::join_kernel<__nv_bfloat16>, split, grid, R, a.n_q, rows, D, dv, few, a.out, a.lse)
+           : cudaLaunchKernelEx(&cfg, attn::join_kernel<__half>, split, grid, R, a.n_q, rows, D, dv, few, a.out, a.lse);
   return e == cudaSuccess ? Q4_OK : cuda_fail(e, "attention join launch");
 }
 
