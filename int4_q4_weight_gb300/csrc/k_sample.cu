@@ -1234,14 +1234,16 @@ int launch_logits_sample(const void* z, long long stride, int dtype, int rows, i
   sample::Params p = {z, stride, u, temperature, top_k, top_p, min_p, token, logprob, V, 0, rows, 0};
   // CTAs per row.  Few rows: eight, one CTA per SM with its part of the row in
   // registers (a cluster lies in one GPC, so not every SM can be used; 8 rows of
-  // 262144: 15.9 us for top-64, 55 us for top-p, against 22 and 74 with four
-  // that read again).  More: four, two CTAs per SM that read the row again from
-  // L2: every phase that one CTA runs alone idles fewer (16 rows: 23 us against
-  // 27; 192 rows: 95 us, with eight 122, with two, whose rows together exceed L2,
-  // 124).  Not more indices per CTA than a 32-bit bin holds, nor CTAs for a few
-  // thousand indices.
+  // 262144: 15.9 us for top-64, against 22 with four that read again).  Up to as
+  // many rows as run at once with eight, two CTAs per SM that read the row again
+  // from L2: eight, as a row's time counts where settings differ (32 rows: 52 us
+  // for mixed settings against 69 with four, top-64 for all 24.6 against 25.0,
+  // top-p 0.9 for all 73 against 68).  More: four, as every phase that one CTA runs
+  // alone idles fewer (64 rows: top-64 32 us against 45, top-p 100 against 139; 192
+  // rows, mixed: 151 against 184).  Not more indices per CTA than a 32-bit bin
+  // holds, nor CTAs for a few thousand indices.
   const bool few = rows * 8 <= dev.sms * 2 / 3;
-  int cluster = few ? 8 : 4;
+  int cluster = rows * 8 <= dev.sms * 7 / 4 ? 8 : 4;   // 7/8 of the places of two CTAs per SM
   while (cluster > 1 && V <= 2048 * cluster) cluster >>= 1;
   while (V > cluster * sample::kSeg * sample::kMaxSegs) cluster <<= 1;
   const int segs = (V + sample::kSeg * cluster - 1) / (sample::kSeg * cluster);
