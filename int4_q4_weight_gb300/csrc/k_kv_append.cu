@@ -18,7 +18,7 @@
 // other, and while they run nothing else would be in flight.
 //
 // Measured: 16 ragged prompts, 41000 tokens of 8 + 2 rows of 256, bf16 (421 MB):
-// 76 us, 5.5 TB/s, half of it writes.  Blocks of 128 threads so that few finish
+// 75 us, 5.6 TB/s, half of it writes.  Blocks of 128 threads so that few finish
 // late; more resident blocks, or two rows ahead, were slower.  8 tokens: 3.2 us.
 #include "q4w_device.cuh"
 #include "q4w_internal.cuh"
@@ -42,11 +42,13 @@ struct Params {
   int rows, groups, rows_per_group;          // rows: n_q + 2 n_kv heads of a token
 };
 
-// 16 bytes of an input: read once, and never written by this kernel, so the loads
-// of the next rows may pass the stores of the last.
+// 16 bytes of an input.  It is the output of the kernel before, which may still be
+// writing when this one starts: not the non-coherent load, and ordered (volatile, with
+// the clobber) behind the wait for that kernel.  The loads of the next row stand
+// before the stores of the last one in the source, so they need no freedom to pass them.
 __device__ __forceinline__ uint4 ld16(const void* p) {
   uint4 r;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
   return r;
 }
 

@@ -191,6 +191,52 @@ def test_append_many_sequences(cuda_lib):
     assert np.all(np.abs(c.kc.double().cpu().numpy() - rk) <= 2.0 ** -11 * np.abs(rk) * 1.01 + 6e-6 + 2.0 ** -25)
 
 
+@pytest.mark.parametrize("D,K", [(256, 1536), (512, 12288)])
+def test_append_right_behind_the_projection(cuda_lib, D, K):
+    """The stage that writes q, k and v lets the next kernel start early: the append
+    reads what it writes, not what lay there before, eagerly and in a graph."""
+    q4w = cuda_lib
+    c = Case([1], [37], 8, 1, D)
+    rows = (8 * D, D, D)
+    mats = [q4w.q4_quantize(normal(c.gen, n, K, dtype=F32, std=0.05)) for n in rows]
+    out = [torch.empty(n, device="cuda") for n in rows]
+    x = torch.empty(K, dtype=F16, device="cuda")
+    steps = q4w.kv_rope_steps(D)
+    q_out = torch.empty(1, 8, D, dtype=F16, device="cuda")
+
+    def append(q, k, v):
+        q4w.kv_append(k.view(1, 1, D), v.view(1, 1, D), *c.tables(), steps=steps, q=q.view(1, 8, D), q_out=q_out)
+
+    def both():
+        q4w.q4_gemv_stage(mats, x, q4w.Q4_IN_F16, out32=out)
+        append(*out)
+
+    page, slot = int(c.table[0, 36 // 16]), 36 % 16
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        both()
+    for i in range(12):
+        x.copy_(normal(c.gen, K))
+        q4w.q4_gemv_stage(mats, x, q4w.Q4_IN_F16, out32=out)
+        torch.cuda.synchronize()
+        append(*[t.clone() for t in out])
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (q_out, c.kc[page, 0, slot], c.vc[page, 0, slot])]
+        for t in out:
+            t.fill_(77.0)
+        for t in (q_out, c.kc, c.vc):
+            t.fill_(33.0)
+        torch.cuda.synchronize()
+        g.replay() if i % 2 else both()
+        torch.cuda.synchronize()
+        for a, b in zip(want, (q_out, c.kc[page, 0, slot], c.vc[page, 0, slot])):
+            assert torch.equal(a, b), i
+
+
 # --------------------------------------------------------------- attention ---
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
 @pytest.mark.parametrize("dtype", [F16, BF16])
