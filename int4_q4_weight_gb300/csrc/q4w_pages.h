@@ -30,10 +30,9 @@ Q4W_HD long long kv_row(int page, int n_kv, int page_size, int head) {
   return ((long long)page * n_kv + head) * page_size;
 }
 
-// First position that a token at `pos` sees with a window (0: all).
-Q4W_HD int kv_first(int pos, int window) {
-  const int f = pos - window + 1;
-  return window > 0 && f > 0 ? f : 0;
-}
+// First position that a token at `pos` sees with a window (0: all).  (The
+// difference is only formed where it is positive: a large window and a negative
+// position leave 32 bits.)
+Q4W_HD int kv_first(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
 
 }  // namespace q4w

@@ -301,6 +301,15 @@ def test_attention_rows_that_see_nothing(cuda_lib, D, hq, hkv, new):
     check_attention(cuda_lib, c)
 
 
+@pytest.mark.parametrize("D,hq,new", [(256, 1, 6), (512, 1, 8), (64, 3, 9), (256, 8, 64), (512, 4, 50), (128, 4, 90)])
+@pytest.mark.parametrize("window", [40, 2 ** 31 - 1])
+def test_attention_lengths_shorter_than_the_new_tokens_with_a_window(cuda_lib, D, hq, new, window):
+    """Tokens at negative positions see nothing, the others what the window leaves, as
+    far as the largest window that there is."""
+    c = Case([new, new, new, new], [0, 3, new - 1, 200], hq, 1, D, 16, F16, seed=new).stale(float("nan"))
+    check_attention(cuda_lib, c, window=window)
+
+
 @pytest.mark.parametrize("D,new", [(256, 1), (256, 40), (512, 1), (512, 40), (64, 6)])
 def test_attention_scores_of_any_size(cuda_lib, D, new):
     """Scores far apart, all equal, huge, negative scale, and one key that takes all."""

@@ -54,6 +54,15 @@ def test_pages_stay_inside_the_cache(pages):
     assert pages.first(5, 0) == 0 and pages.first(2 ** 31 - 1, 2 ** 31 - 1) == 1
 
 
+def test_first_position_of_a_window(pages):
+    """Any position with any window, the largest among them; positions below zero too."""
+    top = 2 ** 31 - 1
+    for pos in (-top - 1, -top, -4096, -3, -2, -1, 0, 1, 5, 4096, top - 1, top):
+        for w in (0, 1, 2, 3, 4096, top - 1, top):
+            want = max(0, pos - w + 1) if w else 0
+            assert pages.first(pos, w) == want, (pos, w)
+
+
 def test_rotation_is_a_complex_product():
     rng = np.random.default_rng(0)
     x = rng.standard_normal((3, 32))
