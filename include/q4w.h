@@ -391,7 +391,9 @@ int kv_append(const q4_kv_cache* cache, int T, const void* k, long long k_stride
  *   Positions outside every token's reach are never read, so their pages may
  *   be freed; what lies in a page behind kv_lens may be anything.  A page
  *   outside [0, n_pages), or kv_lens beyond max_pages pages, leaves out those
- *   positions and sets the optional device int32 *err to 1 (never cleared).
+ *   positions and sets the optional device int32 *err to 1 (never cleared).  So
+ *   does a call of more than 2^31 steps (of 64 to 192 keys) per SM, hours of work: it
+ *   computes nothing.
  *   A NaN or infinity in V reaches, beside the tokens that see its position,
  *   others of the same call and KV head: of the sequence's tokens that are
  *   computed together (at most 256 query rows), those that do not see a position

@@ -189,8 +189,11 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThr), 1) decode_kernel(const _
     __syncthreads();
   }
   const long long first_step = share * blockIdx.x;
-  const int n_steps = (int)max(0ll, min(share, total - first_step));
-  if (n_steps == 0) return;
+  const int n_steps = kv_share_steps(total, share, first_step);
+  if (n_steps <= 0) {   // below zero: more than 32 bits count, hours
+    if (n_steps < 0 && threadIdx.x == 0 && a.err) *a.err = 1;
+    return;
+  }
 
   const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + warp * SLOTS * S::kSlotBytes;
 

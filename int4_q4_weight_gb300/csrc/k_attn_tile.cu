@@ -55,7 +55,7 @@
 namespace q4w {
 namespace tile {
 
-constexpr int kRows = 128, kKeys = 128;
+constexpr int kRows = 128, kKeys = kv_tile_keys;
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = kSoftWarps, kKWarp = kMmaWarp + 1, kVWarp = kKWarp + 1, kQWarp = kVWarp + 1;
 constexpr int kThr = (kQWarp + 1) * 32;
@@ -91,19 +91,9 @@ struct Params {
   int box;               // rows of a TMA box: 16, 32 or 64, a divisor of the page size
 };
 
-// Keys that pair t of tiles of a sequence sees: [base, end), and its steps;
-// `tokens`: of a pair.
-struct Span {
-  int lo, base, end, steps;   // lo: the first key that its first token sees
-};
-__device__ __forceinline__ Span span_of(const AttnParams& a, const Seq& s, int tokens, int t, int box) {
-  Span x;
-  const int j0 = t * tokens, j1 = min(j0 + tokens, s.n) - 1;
-  x.lo = kv_first(s.pos0 + j0, a.window);
-  x.base = x.lo & ~(box - 1);
-  x.end = min(s.end, s.pos0 + j1 + 1);
-  x.steps = x.end > x.base ? (x.end - x.base + kKeys - 1) / kKeys : 1;
-  return x;
+// Keys that pair t of tiles of a sequence sees, and its steps; `tokens`: of a pair.
+__device__ __forceinline__ KvSpan span_of(const AttnParams& a, const Seq& s, int tokens, int t, int box) {
+  return kv_span(s.pos0, s.n, s.end, a.window, tokens, t, box);
 }
 __device__ __forceinline__ int tiles_of(const Seq& s, int tokens) { return (s.n + tokens - 1) / tokens; }
 
@@ -113,7 +103,7 @@ struct Walk {
   int seq, head, part, t, n_tiles;
   int local;             // step of the item
   Seq s;
-  Span x;
+  KvSpan x;
 };
 template <int PARTS>
 __device__ __forceinline__ void walk_item(Walk& w, const Params& p) { w.x = span_of(p.a, w.s, 2 * p.tokens, w.t, p.box); }
@@ -181,7 +171,8 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
   __shared__ uint64_t bars[2 * NS + 7];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
-  __shared__ int start_sh[6];
+  __shared__ int start_sh[3];
+  __shared__ long long left_sh;
   __shared__ long long scan_sh[kThr / 32];
   __shared__ uint32_t bad_sh[kBadRing];   // per step: boxes whose page is none of the cache
   __shared__ float row_sh[2][2][kRows];   // per half of the keys: the rows' maxima of a step, their sums of an item
@@ -216,13 +207,13 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
   // which holds nothing yet
   long long total, share;
   {
-    int* steps_sh = reinterpret_cast<int*>(ring);   // steps of one head and part of each sequence
+    long long* steps_sh = reinterpret_cast<long long*>(ring);   // steps of one head and part of each sequence
+    static_assert(S::kRing >= kMaxSeqs * 8, "the sums fit the ring");
     for (int q = warp; q < a.kv.n_seqs; q += kThr / 32) {
       const Seq s = seq_of(a, q, p.box);
-      const int nt = tiles_of(s, 2 * p.tokens);
-      int sum = 0;
-      for (int t = lane; t < nt; t += 32) sum += span_of(a, s, 2 * p.tokens, t, p.box).steps;
-      sum = __reduce_add_sync(0xffffffffu, sum);
+      long long sum = kv_tile_steps(s.pos0, s.n, s.end, a.window, 2 * p.tokens, p.box, lane, 32);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) {
         steps_sh[q] = sum;
         if (blockIdx.x == 0 && a.err && seq_bad(a, q)) *a.err = 1;
@@ -259,21 +250,25 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       start_sh[0] = q;
       start_sh[1] = hp / PARTS;
       start_sh[2] = hp % PARTS;
-      start_sh[3] = (int)(left % steps_sh[q]);
+      left_sh = left % steps_sh[q];
     }
     if (threadIdx.x == 0) p.split.recs[blockIdx.x].last = -1;
     tc::fence_proxy_async();   // the sums' last use, before the ring's first loads
     __syncthreads();
   }
   const long long first_step = share * pair;
-  const int n_steps = start_sh[0] < 0 ? 0 : (int)max(0ll, min(share, total - first_step));
+  int n_steps = start_sh[0] < 0 ? 0 : kv_share_steps(total, share, first_step);
+  if (n_steps < 0) {   // more steps than 32 bits count: hours
+    if (threadIdx.x == 0 && a.err) *a.err = 1;
+    n_steps = 0;
+  }
   Walk w = {};
   if (n_steps > 0) {
     // the tile: every warp scans the sequence's tiles, 32 at a time
     w.seq = start_sh[0], w.head = start_sh[1], w.part = start_sh[2];
     w.s = seq_of(a, w.seq, p.box);
     w.n_tiles = tiles_of(w.s, 2 * p.tokens);
-    int left = start_sh[3];
+    long long left = left_sh;
     for (int t0 = 0;; t0 += 32) {
       const int n = t0 + lane < w.n_tiles ? span_of(a, w.s, 2 * p.tokens, t0 + lane, p.box).steps : 0;
       int incl = n;
@@ -286,7 +281,7 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       if (past) {
         const int at = __ffs(past) - 1;
         w.t = t0 + at;
-        w.local = left - __shfl_sync(0xffffffffu, incl - n, at);
+        w.local = (int)left - __shfl_sync(0xffffffffu, incl - n, at);
         break;
       }
       left -= __shfl_sync(0xffffffffu, incl, 31);
