@@ -164,7 +164,11 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
   if (tc::smem_u32(smem) & 1023) {   // the swizzle needs it; there is no room to move the buffers
-    if (threadIdx.x == 0) atomicOr(p.dev_err, 1u);
+    pdl_wait();
+    if (threadIdx.x == 0) {
+      p.split.recs[blockIdx.x].last = -1;   // the join reads every CTA's record
+      atomicOr(p.dev_err, 1u);
+    }
     return;
   }
   uint8_t* ring = smem + S::kQBytes;
