@@ -431,10 +431,13 @@ int kv_attention(const q4_kv_cache* cache, int T, int max_q, const void* q,
  *   turn a filter off (temperature NULL: 1).
  *   token: int32 [b]; logprob_opt: f32 [b], or NULL.
  *   1 <= b <= 65535; 1 <= V <= 1048576; stride >= V.  No workspace.
- * Masses are sums of integers (weights in units of 2^-42 of the largest, each
- * within about 2^-29 of itself; weights below 2^-128 count as zero): the
- * result does not depend on the order of the sums, so the same inputs give
- * the same token on every call.                                            */
+ * Masses are sums of integers: weights in units of 2^-42 of the largest, each
+ * within about 2^-29 of itself and then cut down to whole units, so a mass of n
+ * weights is up to n 2^-42 too small and a weight below 2^-42 is no part of it.
+ * The result does not depend on the order of the sums, so the same inputs give
+ * the same token on every call.  logprob is (z_token - M) / temperature -
+ * ln(mass(S)), accurate for improbable tokens too; min_p is compared in units of
+ * 2^-59 (a smaller one counts as 2^-59).                                     */
 int logits_sample(const void* logits, long long stride, int dtype, int b, int V,
                   const float* u, const float* temperature, const int32_t* top_k,
                   const float* top_p, const float* min_p, int32_t* token,

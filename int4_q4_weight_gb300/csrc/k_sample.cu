@@ -20,7 +20,10 @@
 // through a degree-6 polynomial of 2^(-f/8) to a 28-bit mantissa; the weight is
 // mantissa * 2^(-(n mod 8)/8) * 2^-(n div 8), cut off to units of 2^-42.
 // Integer sums have no order, so atomics and cluster reductions give the same
-// bits on every run.  A weight is off by about 2^-29 of itself, unbiased.
+// bits on every run.  A weight is off by about 2^-29 of itself, and cut downwards by
+// less than a unit: a sum of n weights is up to n 2^-42 of the largest too small, and
+// nothing is left of a weight below 2^-42.  The log probability is therefore formed
+// from the chosen logit, ln of the mass alone from the integers.
 // Products of a mass with top_p or u are formed exactly in 128 bits (fp64 runs
 // at a sixtieth of the fp32 rate: one logarithm per row is all of it).
 //
@@ -194,7 +197,12 @@ __device__ __noinline__ u64 times(u64 m, float f, bool up) {
   return q + (up && rest ? 1 : 0);
 }
 
-__device__ __noinline__ float ln_ratio(u64 w, u64 mass) { return (float)log((double)w / (double)mass); }
+// ln of the chosen logit's share of the mass: from the logit, not from its weight in
+// whole units, of which a small one keeps few digits or none.
+__device__ __noinline__ float log_prob(const Params& p, int row, float top, float v, u64 mass) {
+  const float t = p.temperature ? fmaxf(p.temperature[row], 1e-36f) : 1.f;
+  return (float)(((double)v - (double)top) / (double)t - log((double)mass * 2.2737367544323206e-13));
+}
 
 template <typename T>
 __device__ __forceinline__ float as_float(T v) {
@@ -823,9 +831,9 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
     for (int x = 0; x < kWarpsS; ++x) keep += (int)sh.red32[x];
     // the first running mass, in vocabulary order, above the goal
     const u64 goal = min(times(mass, u, false), mass - 1);
-    auto pick = [&](int index, u64 wi) {
+    auto pick = [&](int index, uint32_t inverted_key) {
       p.token[row] = index;
-      if (p.logprob) p.logprob[row] = ln_ratio(wi, mass);
+      if (p.logprob) p.logprob[row] = log_prob(p, row, s.top, logit_of(~inverted_key), mass);
     };
     if (keep <= kCount) {
       const int i = threadIdx.x >> 1;
@@ -833,7 +841,7 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
       u64 run = 0;
       for (int j = threadIdx.x & 1; j < keep; j += 2) run += (uint32_t)sh.list[j] < at ? wt[j] : 0ull;
       run += __shfl_xor_sync(0xffffffffu, run, 1);
-      if ((threadIdx.x & 1) == 0 && i < keep && run <= goal && run + wt[i] > goal) pick((int)at, wt[i]);
+      if ((threadIdx.x & 1) == 0 && i < keep && run <= goal && run + wt[i] > goal) pick((int)at, (uint32_t)(sh.list[i] >> 32));
     } else {
       int n2 = 2 * kCount;
       while (n2 < keep) n2 <<= 1;
@@ -853,7 +861,7 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int i = kPer * threadIdx.x + j;
-        if (i < keep && run <= goal && run + w[j] > goal) pick((int)(sh.list[i] >> 32), w[j]);
+        if (i < keep && run <= goal && run + w[j] > goal) pick((int)(sh.list[i] >> 32), (uint32_t)sh.list[i]);
         run += w[j];
       }
     }
@@ -1195,7 +1203,7 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
     for (int k = 0; k < 4; ++k) {
       if (run <= goal && run + w[k] > goal) {
         p.token[row] = i + k;
-        if (p.logprob) p.logprob[row] = ln_ratio(w[k], mass);
+        if (p.logprob) p.logprob[row] = log_prob(p, row, s.top, v[k], mass);
       }
       run += w[k];
     }

@@ -205,3 +205,29 @@ def test_largest_vocabulary(cuda_lib):
     z, u = rows(1, 1048576, seed=12)
     check(cuda_lib, z, u, t=2.0)
     check(cuda_lib, z, u, k=500000, p=0.9, t=2.0)
+
+
+def tail_rows(V, near, depths, seed=3):
+    """A row per depth: index 0 lies that far below the maximum, `near` others within a
+    few of it, the rest where no weight counts (2^-200 and less)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    b = len(depths)
+    z = 1.5 - 140 - torch.rand(b, V, generator=g, device="cuda")
+    z[:, 1:1 + near] = 1.5 - 3 * torch.rand(b, near, generator=g, device="cuda")
+    z[:, near] = 1.5
+    z[:, 0] = 1.5 - torch.tensor(depths, device="cuda")
+    return z
+
+
+@pytest.mark.parametrize("V,near", [(2, 1), (300, 7), (9000, 100), (9000, 3000), (262144, 90), (262144, 5000)])
+def test_log_probability_of_an_improbable_token(cuda_lib, V, near):
+    """A drawn token of weight 2^-26 to 2^-42: its log probability keeps every digit."""
+    depths = [18.0, 20.3, 24.0, 26.7, 28.0, 28.9, 29.05] if V < 200000 else [20.3, 29.05]
+    z = tail_rows(V, near, depths)
+    u = torch.tensor([np.exp(-x) / (4 * near) for x in depths], dtype=F32, device="cuda")
+    for kw in (dict(), dict(k=near + 1), dict(m=1e-13)) if near + 1 < V else (dict(), dict(m=1e-13)):
+        tok, _ = check(cuda_lib, z, u, **kw)
+        assert tok.tolist() == [0] * len(depths)
+        if V < 200000:
+            check(cuda_lib, z * 0.5, u, t=0.5, **kw)
