@@ -433,7 +433,9 @@ int kv_attention(const q4_kv_cache* cache, int T, int max_q, const void* q,
  *   1 <= b <= 65535; 1 <= V <= 1048576; stride >= V.  No workspace.
  * Masses are sums of integers: weights in units of 2^-42 of the largest, each
  * within about 2^-29 of itself and then cut down to whole units, so a mass of n
- * weights is up to n 2^-42 too small and a weight below 2^-42 is no part of it.
+ * weights is up to n 2^-42 too small and a weight below 2^-42 is no part of it;
+ * for u = 0 the token is the first of S, whatever its weight (one below 2^-128
+ * counts as zero).
  * The result does not depend on the order of the sums, so the same inputs give
  * the same token on every call.  logprob is (z_token - M) / temperature -
  * ln(mass(S)), accurate for improbable tokens too; min_p is compared in units of

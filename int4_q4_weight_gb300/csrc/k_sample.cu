@@ -23,7 +23,8 @@
 // bits on every run.  A weight is off by about 2^-29 of itself, and cut downwards by
 // less than a unit: a sum of n weights is up to n 2^-42 of the largest too small, and
 // nothing is left of a weight below 2^-42.  The log probability is therefore formed
-// from the chosen logit, ln of the mass alone from the integers.
+// from the chosen logit, ln of the mass alone from the integers; and u = 0, which asks
+// for the first of S however small its weight, goes by the members of S instead.
 // Products of a mass with top_p or u are formed exactly in 128 bits (fp64 runs
 // at a sixtieth of the fp32 rate: one logarithm per row is all of it).
 //
@@ -835,7 +836,15 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
       p.token[row] = index;
       if (p.logprob) p.logprob[row] = log_prob(p, row, s.top, logit_of(~inverted_key), mass);
     };
-    if (keep <= kCount) {
+    if (u == 0.f) {   // the first of S, whose weight may be less than a unit
+      int first = 0x7fffffff;
+      for (int i = threadIdx.x; i < keep; i += kThr) first = min(first, (int)(uint32_t)sh.list[i]);
+      first = __reduce_min_sync(0xffffffffu, first);
+      if (lane == 0) atomicMin(&sh.first, first);
+      __syncthreads();
+      for (int i = threadIdx.x; i < keep; i += kThr)
+        if ((int)(uint32_t)sh.list[i] == sh.first) pick(sh.first, (uint32_t)(sh.list[i] >> 32));
+    } else if (keep <= kCount) {
       const int i = threadIdx.x >> 1;
       const uint32_t at = i < keep ? (uint32_t)sh.list[i] : 0u;
       u64 run = 0;
@@ -1163,6 +1172,26 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
   cluster_sync();
   u64 before;
   const u64 mass = cluster_sum(&sh.mine, rank, ctas, &before);
+  if (u == 0.f) {   // the first of S, whose weight may be less than a unit (the same in every CTA)
+    int first = 0x7fffffff;
+    part.heavy([&](float x, int i) {
+      const float v = capped(s, x);
+      const u64 c = (u64)~key_of(v) << 32 | (uint32_t)i;
+      const bool in = near ? above_range(v) || (v <= v_hi && c <= last_kept) : kept(v) || tied(v);   // the first that ties is kept
+      if (in && eighths(s, v) < (float)kBins) first = min(first, i);
+    });
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) atomicMin(&sh.first, first);
+    cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+      first = 0x7fffffff;
+      for (uint32_t r = 0; r < ctas; ++r) first = min(first, (int)ld_cluster_u32(tc::cluster_addr(&sh.first, r)));
+      p.token[row] = first;
+      if (p.logprob) p.logprob[row] = log_prob(p, row, s.top, capped(s, as_float(z[first])), mass);
+    }
+    cluster_sync();   // no CTA leaves while another reads its shared memory
+    return;
+  }
   const u64 goal = min(times(mass, u, false), mass - 1);
   m_run += before;
   t_run = t_first;

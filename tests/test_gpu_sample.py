@@ -231,3 +231,47 @@ def test_log_probability_of_an_improbable_token(cuda_lib, V, near):
         assert tok.tolist() == [0] * len(depths)
         if V < 200000:
             check(cuda_lib, z * 0.5, u, t=0.5, **kw)
+
+
+@pytest.mark.parametrize("V,near", [(2, 1), (300, 7), (9000, 100), (9000, 3000), (262144, 90), (262144, 5000)])
+def test_zero_takes_the_first_of_the_set(cuda_lib, V, near):
+    """u = 0: the first index of S, with weights from 2^-25 to 2^-126; u next to 0."""
+    depths = [17.4, 22.0, 28.0, 29.2, 31.0, 35.0, 41.6, 60.0, 87.0] if V < 200000 else [22.0, 41.6, 87.0]
+    z = tail_rows(V, near, depths)
+    u = torch.zeros(len(depths), device="cuda")
+    for kw in (dict(), dict(k=near + 1)) if near + 1 < V else (dict(),):
+        tok, _ = check(cuda_lib, z, u, **kw)
+        assert tok.tolist() == [0] * len(depths)
+    check(cuda_lib, z[:7], u[:7], m=2.0 ** -58)
+    # cut by a filter, it is not the first of S
+    for kw in (dict(p=0.9), dict(k=near, p=0.9), dict(m=0.01), dict(k=near)) if V < 200000 else (dict(p=0.9), dict(k=near)):
+        tok, _ = check(cuda_lib, z, u, **kw)
+        assert min(tok.tolist()) >= 1
+    # next to 0: below the weight of the first, and above it
+    few = depths[:3] if V < 200000 else depths[:1]
+    w = np.exp(-np.array(few))
+    for f, first in ((0.25, True), (3.0 * near, False)):
+        tok, _ = check(cuda_lib, z[:len(few)], torch.tensor(w * f / near, dtype=F32, device="cuda"))
+        assert [t == 0 for t in tok.tolist()] == [first] * len(few)
+
+
+@pytest.mark.parametrize("V", [20000, 262144])
+def test_zero_with_a_wide_set(cuda_lib, V):
+    """Top-p whose border lies among thousands of small weights, apart and tied."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    z = -13.0 - 0.7 * torch.rand(3, V, generator=g, device="cuda")
+    z[1] = -13.5
+    z[2, 1:] = (z[2, 1:] * 64).round() / 64
+    z[:, V // 2] = 0.0
+    z[:, 0] = -13.001
+    z[1, 0] = -13.5
+    u = torch.zeros(3, device="cuda")
+    n = float(torch.exp(z[0].double()).sum()) - 1.0        # the tail's share
+    for p in (1 - 0.5 * n / (1 + n), 1 - 0.2 * n / (1 + n)):
+        tok, _ = check(cuda_lib, z, u, p=p)
+        assert tok.tolist() == [0, 0, 0]
+        check(cuda_lib, z, u, p=p, m=1e-6)
+        check(cuda_lib, z, torch.full_like(u, 2.0 ** -24), p=p)
+    check(cuda_lib, z, u, k=5000, p=0.9999999)
+    check(cuda_lib, z, u, k=5000)
