@@ -172,6 +172,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThr), 1) decode_kernel(const _
     if (blockIdx.x == 0 && a.err) {
       for (int q = q0; q < q1; ++q)
         if (seq_bad(a, q)) *a.err = 1;
+      if (share > 0x7fffffff) *a.err = 1;   // more steps than 32 bits count: hours
     }
     if (threadIdx.x == 0) p.split.recs[blockIdx.x].last = -1;
     if (sum > 0 && mine >= before && mine < before + sum) {
@@ -189,11 +190,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThr), 1) decode_kernel(const _
     __syncthreads();
   }
   const long long first_step = share * blockIdx.x;
-  const int n_steps = kv_share_steps(total, share, first_step);
-  if (n_steps <= 0) {   // below zero: more than 32 bits count, hours
-    if (n_steps < 0 && threadIdx.x == 0 && a.err) *a.err = 1;
-    return;
-  }
+  const int n_steps = (int)max(0ll, min(share, total - first_step));
+  if (n_steps == 0 || share > 0x7fffffff) return;
 
   const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + warp * SLOTS * S::kSlotBytes;
 
