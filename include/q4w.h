@@ -399,7 +399,8 @@ int kv_append(const q4_kv_cache* cache, int T, const void* k, long long k_stride
  *   computed together (at most 256 query rows), those that do not see a position
  *   that another of them sees.  Positions that none of them sees reach nothing.
  *   Arithmetic: scores, maximum, sum and output are fp32; the probabilities
- *   enter the second product rounded once to the cache's type.  The split of
+ *   enter the second product rounded once to the cache's type (fp16: with an
+ *   absolute error of at least 2^-32 of the row's largest).  The split of
  *   the keys over CTAs depends on the lengths only: repeated calls give the
  *   same bits.
  *   ws: kv_attention_ws_bytes() bytes, contents on entry do not matter; calls

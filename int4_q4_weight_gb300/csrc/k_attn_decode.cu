@@ -2,8 +2,8 @@
 // drafted tokens): rows = new tokens x query heads of the group <= 8 NT.
 //
 // Mathematics: one pass over the keys with the running maximum and sum of a
-// softmax (scores in units of log2 e, so that e^s is one 2^x); the maximum is
-// moved only when a score passes it by 2^8, so that most steps rescale nothing.
+// softmax (scores in units of log2 e, so that e^s is one 2^x); the reference is
+// moved only when the maximum has grown by 2^8, so that most steps rescale nothing.
 // The final division makes the result independent of that choice.
 //
 // Bound: HBM.  A 16-bit cache element takes part in 8 or 16 multiply-adds, too
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThr), 1) decode_kernel(const _
             if (c > pos || c < kv_first(pos, a.window) || c >= cw.s.end) s[t][j] = -CUDART_INF_F;
           }
       }
-      // the maximum over the 16 keys; moved when it is passed by 2^8
+      // the maximum over the 16 keys; the reference moves when it is passed
       bool move = false;
       float mx[NT][2];
 #pragma unroll
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThr), 1) decode_kernel(const _
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
           mx[t][j] = v;
-          move |= v > m[t][j] + 8.f;
+          move |= v > m[t][j] + Reference<T>::move;
         }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThr), 1) decode_kernel(const _
           float f[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float m2 = fmaxf(m[t][j], mx[t][j]);
+            const float m2 = fmaxf(m[t][j], mx[t][j] - Reference<T>::below);
             f[j] = m2 == -CUDART_INF_F ? 1.f : ex2(m[t][j] - m2);
             m[t][j] = m2;
             l[t][j] *= f[j];

@@ -8,8 +8,8 @@
 //                                     each, S read from TMEM, P (16 bits)
 //                                     written over it
 //   O[128 rows][DV]      += P V       A = P in TMEM, B = V in shared memory
-// with the running maximum m and sum of each row in its threads.  m is moved
-// only when a score passes it by 2^8, so O (in TMEM) is rarely rescaled.
+// with the running reference m and sum of each row in its threads.  m is moved
+// only when the maximum has grown by 2^8, so O (in TMEM) is rarely rescaled.
 // Two S tiles alternate: the scores of step j + 1 are formed while the softmax
 // of step j runs.  TMEM: S 2 x 128 columns, O 256 = all 512.  Head size 512 does
 // not fit: its two column halves of O are items of their own, which form the
@@ -557,8 +557,8 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       }
       meet();
       const float mx = fmaxf(row_sh[0][j & 1][row], row_sh[1][j & 1][row]);
-      if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-        const float m2 = fmaxf(m, mx), f = m2 == -CUDART_INF_F ? 1.f : ex2(m - m2);
+      if (__any_sync(0xffffffffu, mx > m + Reference<T>::move)) {
+        const float m2 = fmaxf(m, mx - Reference<T>::below), f = m2 == -CUDART_INF_F ? 1.f : ex2(m - m2);
         m = m2;
         l *= f;
         if (!first) {   // O holds the steps before: let the last one finish

@@ -4,6 +4,8 @@
 
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "q4w_internal.cuh"
 #include "q4w_kv.cuh"
 
@@ -38,6 +40,18 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Where a row's running reference m lies (units of log2 e): it is set `below` under the
+// maximum and moved when a score passes it by `move`, so that most steps rescale nothing.
+// The probabilities 2^(s - m) enter the second product in 16 bits.  bf16 has the range of
+// fp32.  fp16 has 30 octaves of normal numbers, and what is used of them above 1 is
+// gained below: with m at the maximum a probability of 2^-20 kept four bits, and a
+// hundred thousand keys of 2^-25 each were lost whole; now 2^-21 of the largest is a
+// normal number and the absolute error 2^-32 of it.  2^15 fits, 65504 is the largest.
+template <typename T>
+struct Reference {
+  static constexpr float below = std::is_same<T, __half>::value ? 7.f : 0.f, move = below + 8.f;
+};
+
 // The parts of work that is cut.  The steps of all items form one line that is
 // cut into equal shares; the team of R CTAs c (R is 1, or 2 that work in step on
 // a tile each) leaves the part of an item that began before it in slot 2 c, and
@@ -51,7 +65,7 @@ struct SplitRec {
 };
 struct AttnSplit {
   float* part_o;         // [2 grid][dv / 4][rows][4]: sums of the values
-  float2* part_ml;       // [2 grid][rows]: maximum (in units of log2 e) and sum
+  float2* part_ml;       // [2 grid][rows]: reference (in units of log2 e) and sum
   SplitRec* recs;        // [grid]
 };
 

@@ -327,6 +327,32 @@ def test_attention_scores_of_any_size(cuda_lib, D, new):
     check_attention(cuda_lib, c, q=q, scale=1.0)
 
 
+@pytest.mark.parametrize("D,new,seqs,n", [(256, 1, 160, 1500), (64, 3, 160, 1500), (128, 2, 160, 1500), (512, 1, 160, 1500), (256, 1, 1, 20000),
+                                          (256, 40, 90, 600), (256, 40, 1, 20000), (64, 70, 1, 20000), (512, 20, 1, 20000)])
+@pytest.mark.parametrize("depth", [12.0, 16.3, 20.4, 24.8])
+def test_attention_many_keys_of_small_probability(cuda_lib, D, new, seqs, n, depth):
+    """One key that takes nearly all, and thousands of 2^-depth each whose values alone
+    make the output: their sum keeps the precision of 16 bits.  fp16 is the narrow type;
+    its probabilities have an absolute error of 2^-32 of the largest (a key's is 2^-depth)."""
+    q4w = cuda_lib
+    c = Case([new] * seqs, [n] * seqs, 2, 1, D, 64, F16, seed=new)
+    c.kc.zero_()
+    c.kc[..., 0] = -depth * math.log(2.0)
+    c.vc.fill_(1.0)
+    sink = n // 3                                       # before every new token
+    pages = c.table[:, sink // 64].long()
+    c.kc[pages, 0, sink % 64, 0] = 0.0
+    c.vc[pages, 0, sink % 64] = 0.0
+    q = torch.zeros_like(c.q)
+    q[..., 0] = 1.0
+    out, _ = q4w.kv_attention(q, *c.tables(), max_q=new, scale=1.0)
+    q4w.q4_device_status()
+    ro, _, A, S = O.attention(q.float().cpu().numpy(), *c.host(), 1.0)
+    tol = 2.0 ** -11 * (A + np.abs(ro)) * 1.01 + (16 * 2.0 ** -24 * S[..., None] + 2e-6) * A + 2.0 ** (depth - 32) * ro + 2.0 ** -25
+    err = np.abs(out.double().cpu().numpy() - ro)
+    assert np.all(err <= tol), float((err / tol).max())
+
+
 @pytest.mark.parametrize("new,hq", [(1, 8), (64, 8), (4, 8)])
 def test_attention_strided_queries_and_order(cuda_lib, new, hq):
     c = Case([new] * 3, [new + 100, new + 7, new], hq, 1, 256, 16, F16)
