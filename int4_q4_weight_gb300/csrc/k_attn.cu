@@ -181,8 +181,8 @@ int launch_attn_join(const AttnParams& a, const AttnSplit& split, int rows, int 
   return e == cudaSuccess ? Q4_OK : cuda_fail(e, "attention join launch");
 }
 
-size_t attn_ws_bytes(int max_rows, int D, const DeviceInfo& dev) {
-  return attn_decode_fits(max_rows, D) ? attn_decode_ws_bytes(max_rows, D, dev) : attn_tile_ws_bytes(D, dev);
+size_t attn_ws_bytes(long long max_rows, int D, const DeviceInfo& dev) {
+  return attn_decode_fits(max_rows, D) ? attn_decode_ws_bytes((int)max_rows, D, dev) : attn_tile_ws_bytes(D, dev);
 }
 
 int launch_kv_attention(const AttnParams& p, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s) {

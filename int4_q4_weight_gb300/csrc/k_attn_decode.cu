@@ -544,7 +544,7 @@ static int nt_of(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 }  // namespace dec
 
-bool attn_decode_fits(int max_rows, int D) { return max_rows <= 8 * dec::max_nt(D); }
+bool attn_decode_fits(long long max_rows, int D) { return max_rows <= 8 * dec::max_nt(D); }
 
 size_t attn_decode_ws_bytes(int max_rows, int D, const DeviceInfo& dev) {
   return attn_split_bytes(dev.sms, 8 * dec::nt_of(max_rows), D);

@@ -54,7 +54,7 @@ int launch_kv_append(const q4_kv_cache& c, int T, const void* k, long long k_str
                      const DeviceInfo& dev, cudaStream_t s);
 // Workspace of an attention call whose sequences have up to max_rows query
 // rows (tokens x query heads) per KV head.
-size_t attn_ws_bytes(int max_rows, int D, const DeviceInfo& dev);
+size_t attn_ws_bytes(long long max_rows, int D, const DeviceInfo& dev);
 // Tensor map of a cache of `rows` rows of D 16-bit elements, seen as D/64 slabs
 // of 64 elements: boxes of box_rows rows of box_slabs slabs in the 128-byte
 // swizzle, laid out slab after slab.
@@ -65,7 +65,7 @@ int encode_cache_rows(CUtensorMap* tm, const void* base, bool bf16, int D, uint6
 int encode_query_rows(CUtensorMap* tm, const void* base, bool bf16, int D, int n_q, int T, long long stride,
                       uint32_t heads, uint32_t tokens);
 // Few query rows per KV head (k_attn_decode.cu).
-bool attn_decode_fits(int max_rows, int D);
+bool attn_decode_fits(long long max_rows, int D);
 size_t attn_decode_ws_bytes(int max_rows, int D, const DeviceInfo& dev);
 int launch_attn_decode(const AttnParams& a, const q4_kv_cache& c, void* ws, const DeviceInfo& dev, cudaStream_t s);
 // Tiles of 128 query rows (k_attn_tile.cu).

@@ -99,7 +99,7 @@ int kv_append(const q4_kv_cache* cache, int T, const void* k, long long k_stride
 size_t kv_attention_ws_bytes(int max_q, int n_q, int n_kv, int head_dim) {
   DeviceInfo dev;
   if (max_q < 1 || n_kv < 1 || n_q < n_kv || head_dim < 1 || current_device(&dev) != Q4_OK) return 0;
-  return attn_ws_bytes(max_q * (n_q / n_kv), head_dim, dev);
+  return attn_ws_bytes((long long)max_q * (n_q / n_kv), head_dim, dev);
 }
 
 int kv_attention(const q4_kv_cache* cache, int T, int max_q, const void* q, long long q_stride, int n_q, float scale,

@@ -404,6 +404,17 @@ def test_attention_same_bits_again_streams_and_graphs(cuda_lib, new, D):
     assert torch.equal(out3, want) and torch.equal(lse3, wl)
 
 
+def test_attention_workspace_of_any_size(cuda_lib):
+    """Products of its arguments that pass 32 bits ask for the tiles' workspace, not for
+    the smaller one of a few rows."""
+    lib = cuda_lib.load()
+    for D in (64, 128, 256, 512):
+        tiles = lib.kv_attention_ws_bytes(4096, 8, 1, D)
+        assert tiles > lib.kv_attention_ws_bytes(1, 8, 1, D)
+        for max_q, n_q in ((2 ** 29, 8), (2 ** 30, 128), (2 ** 31 - 1, 128), (3 * 2 ** 29, 8)):
+            assert lib.kv_attention_ws_bytes(max_q, n_q, 1, D) == tiles, (max_q, n_q, D)
+
+
 def test_attention_longer_than_max_q(cuda_lib):
     """A sequence with more tokens than max_q: its first max_q tokens, and the flag."""
     q4w = cuda_lib
