@@ -681,7 +681,8 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_tokens, kv_lens, steps=Non
 
 @functools.lru_cache(maxsize=256)
 def _attention_ws_bytes(max_q, n_q, n_kv, head_dim, device):
-    n = load().kv_attention_ws_bytes(max_q, n_q, n_kv, head_dim)
+    with torch.cuda.device(device):   # the size goes by the current device's SMs
+        n = load().kv_attention_ws_bytes(max_q, n_q, n_kv, head_dim)
     if n == 0:
         raise Q4Error(f"no workspace size for max_q={max_q}, n_q={n_q}, n_kv={n_kv}, head_dim={head_dim} on this device")
     return n
@@ -690,7 +691,9 @@ def _attention_ws_bytes(max_q, n_q, n_kv, head_dim, device):
 def kv_attention_ws(max_q, n_q, n_kv, head_dim, device):
     """A workspace for kv_attention calls of these sizes that do not overlap."""
     device = torch.device(device)
-    n = _attention_ws_bytes(max_q, n_q, n_kv, head_dim, device.index)
+    if device.type != "cuda":
+        raise Q4Error(f"a workspace lies on a CUDA device, not on {device}")
+    n = _attention_ws_bytes(max_q, n_q, n_kv, head_dim, torch.cuda.current_device() if device.index is None else device.index)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 

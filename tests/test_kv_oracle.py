@@ -246,3 +246,39 @@ def test_binding_checks_sizes(fake):
     q4w.kv_attention(a["q"][:0], *c)
     q4w.logits_sample(torch.zeros(0, 50), torch.zeros(0))
     assert len(fake.calls) == 3
+
+
+def test_workspace_sizes_belong_to_their_device(monkeypatch):
+    """Two devices of different sizes: a size is that of the device that the workspace is
+    for, whatever device is current and in whatever order they are asked for."""
+    current = [0]
+
+    class Lib:
+        def kv_attention_ws_bytes(self, *a):
+            return (1000, 3000)[current[0]]
+
+    class Device:
+        def __init__(self, i):
+            self.i = i
+
+        def __enter__(self):
+            self.old, current[0] = current[0], self.i
+
+        def __exit__(self, *a):
+            current[0] = self.old
+
+    monkeypatch.setattr(q4w, "load", lambda: Lib())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: (n, str(device)))
+    q4w._attention_ws_bytes.cache_clear()
+    try:
+        ws = lambda d: q4w.kv_attention_ws(1, 8, 1, 256, d)[0]   # noqa: E731
+        assert [ws("cuda"), ws("cuda:1"), ws("cuda:0")] == [1000, 3000, 1000]
+        current[0] = 1
+        assert [ws("cuda"), ws("cuda:0"), ws(torch.device("cuda", 1))] == [3000, 1000, 3000]
+        assert current[0] == 1
+        with pytest.raises(q4w.Q4Error):
+            q4w.kv_attention_ws(1, 8, 1, 256, "cpu")
+    finally:
+        q4w._attention_ws_bytes.cache_clear()
