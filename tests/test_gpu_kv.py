@@ -262,6 +262,15 @@ def test_attention_any_number_of_query_rows(cuda_lib, D, hq, new):
     check_attention(cuda_lib, Case([new, 1, new], [new, 100, 300 + new], hq, 1, D, 16, BF16, seed=hq))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("rows", [7, 8, 9, 15, 16, 17, 31, 32, 33, 127, 128, 129, 255, 256, 257])
+def test_attention_rows_next_to_the_kernels_limits(cuda_lib, D, rows):
+    """Rows per KV head around the sizes at which another kernel or tile begins, as
+    tokens of one head and as heads of few tokens."""
+    for hq, new in [(1, rows)] + [(h, rows // h) for h in (rows, rows // 2, 3) if h <= 128 and rows % h == 0 and h > 1]:
+        check_attention(cuda_lib, Case([new, 1, new], [new, 70, 190 + new], hq, 1, D, 16, F16, seed=rows + hq))
+
+
 @pytest.mark.parametrize("D,hq,hkv", [(64, 8, 2), (256, 8, 1), (512, 8, 1), (128, 4, 4)])
 @pytest.mark.parametrize("new", [1, 2, 4, 9, 70])
 @pytest.mark.parametrize("window", [1, 17, 100, 512])

@@ -1,5 +1,8 @@
 """logits_sample against the fp64 oracle: tokens exactly, log probabilities to
 the rounding of an fp32 (eps/2 of the value) and the weights' 2^-28."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -275,3 +278,39 @@ def test_zero_with_a_wide_set(cuda_lib, V):
         check(cuda_lib, z, torch.full_like(u, 2.0 ** -24), p=p)
     check(cuda_lib, z, u, k=5000, p=0.9999999)
     check(cuda_lib, z, u, k=5000)
+
+
+def test_top_p_over_the_largest_vocabulary(cuda_lib):
+    """131072 indices a CTA: short weights of 14 bits, every segment."""
+    z, u = rows(2, 1048576, seed=13)
+    check(cuda_lib, z, u, p=0.9, t=2.0)
+    check(cuda_lib, z[:1], u[:1], p=0.99, m=0.002)
+    check(cuda_lib, z[:1], torch.zeros(1, device="cuda"), p=0.9999, t=3.0)
+
+
+@pytest.mark.parametrize("V", [131072, 1048575, 1048576])
+@pytest.mark.parametrize("p", [1e-7, 0.25, 0.7, 1 - 2.0 ** -24])
+def test_equal_logits_of_the_largest_vocabulary_under_top_p(cuda_lib, V, p):
+    """One bin holds every weight (2^31 a CTA at the largest size); the set is the lowest
+    indices, the token where u points, in exact fractions."""
+    us = [0.0, 2.0 ** -24, 0.3, 0.999, 1 - 2.0 ** -24]
+    u = torch.tensor(us, device="cuda")
+    P = Fraction(float(torch.tensor(p, dtype=F32)))
+    n = math.ceil(P * V)
+    for m in (None, 0.5):
+        tok, lp = cuda_lib.logits_sample(torch.full((5, V), -2.5, device="cuda"), u, None, None, torch.full((5,), p, device="cuda"),
+                                         None if m is None else torch.full((5,), m, device="cuda"))
+        torch.cuda.synchronize()
+        assert tok.tolist() == [math.floor(Fraction(float(x)) * n) for x in u]
+        assert np.allclose(lp.cpu().numpy(), -np.log(n), rtol=2.0 ** -23, atol=0)
+
+
+def test_rows_of_eight_ctas_that_read_again(cuda_lib):
+    """More rows than fit one CTA an SM, fewer than take four: every kind of row."""
+    z, u = rows(16, 262144, seed=21)
+    t = torch.tensor([0.0, 0.7, 1.0, 1.6] * 4, device="cuda")
+    k = torch.tensor([0, 0, 50, 0, 4000, 0, 0, 1] * 2, dtype=torch.int32, device="cuda")
+    p = torch.tensor([1.0, 0.9, 0.95, 1.0, 0.8, 0.99, 0.5, 1.0] * 2, device="cuda")
+    m = torch.tensor([0.0] * 12 + [0.02] * 4, device="cuda")
+    check(cuda_lib, z, u, t, k, p, m)
+    check(cuda_lib, z[:13], torch.zeros(13, device="cuda"), p=0.95)
