@@ -327,8 +327,8 @@ int lmhead_softcap_argmax_noalloc(const uint8_t* codes, const uint16_t* scales,
  * cu_tokens[s] .. cu_tokens[s+1] - 1 of the call, and kv_lens[s] is the length
  * of its cache WITH them, so token t is at position
  *   P(t) = kv_lens[s] - cu_tokens[s+1] + t.
- * Tokens at or behind cu_tokens[n_seqs] are padding: nothing is read or
- * written for them.  A sequence may have no new tokens, or a cache length of
+ * Tokens at or behind cu_tokens[n_seqs] are padding: nothing is written for
+ * them, and what their rows hold does not matter.  A sequence may have no new tokens, or a cache length of
  * zero.  The arrays below are device memory; the struct itself is HOST memory,
  * read during the call only. */
 typedef struct q4_kv_cache {

@@ -13,7 +13,8 @@ namespace attn {
 // parts of the few rows of a single long sequence are read by 16 groups side by
 // side, as there are no other tasks: 16 us with 4 groups, 8 with 16.  Every block
 // reads all the records, so the tasks of the few items that were split spread over
-// the device whatever CTA recorded them.
+// the device whatever CTA recorded them.  (Two blocks on an SM leave a thread 64
+// registers, and 108 bytes are spilled.)
 constexpr int kJoinThr = 512;
 
 // log2 of P; lg_dv: log2 of the columns.
@@ -44,7 +45,7 @@ __global__ void __launch_bounds__(kJoinThr, 2) join_kernel(const AttnSplit p, in
   __shared__ SplitRec rec_sh[kJoinThr];
   __shared__ int warp_sh[kJoinThr / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lg_dv = 31 - __clz(dv);   // 64, 128 or 256
+  const int lg_dv = 31 - __clz(dv);   // 64 to 512
   pdl_wait();
   {
     int n = 0;

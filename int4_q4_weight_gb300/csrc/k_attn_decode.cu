@@ -46,6 +46,7 @@ struct Shape {
   // A warp holds NT D / 4 + NT D / 8 registers of O and Q.  Twelve warps where
   // that leaves them without spills: 8 rows of head size 64 stream at 6.2 TB/s,
   // with eight warps at 5.4; 16 rows of head size 128 at 5.4 (spills), with eight 6.3.
+  // Head size 512 takes 255 registers with four warps and spills 32 bytes.
   static constexpr int kWarps = D == 512 ? 4 : NT * D <= 128 ? 12 : 8;
   static constexpr int kSlotBytes = kUnit * D * 2;
   static constexpr int kSlots = kRingBytes / kWarps / kSlotBytes;   // 3, 3, 6, 12: K and V alternate
@@ -132,7 +133,7 @@ struct Walk {
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__((Shape<D, NT>::kThr), 1) decode_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, NT>;
-  constexpr int W = S::kWarps, SLOTS = S::kSlots, KS = D / 16, SLABS = D / 64;
+  constexpr int W = S::kWarps, SLOTS = S::kSlots, KS = D / 16;
   extern __shared__ __align__(1024) uint8_t ring[];
   float* merge = reinterpret_cast<float*>(ring + kRingBytes);
   __shared__ float2 ml_sh[W][8 * NT];

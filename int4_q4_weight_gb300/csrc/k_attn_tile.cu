@@ -42,10 +42,14 @@
 // keys.  Parts are joined by a second kernel in the order of the keys.
 //
 // Measured: four ragged prompts of up to 4096 tokens over contexts of up to 8192
-// (8 query heads on 1 KV head of 256, 326 GFLOP): 215 us with the join, 1.5
-// PFLOP/s, the tensor pipe active for 80 % of the cycles of the busy SMs.  A step
-// takes 2350 cycles; what else is lost lies at the ends of items, where O is read
-// out before the next item may write it, and in the join.
+// (8 query heads on 1 KV head of 256, 326 GFLOP): 215 us with the join from a graph,
+// 1.5 PFLOP/s, and 228 us a call from Python, 1.43; the tensor pipe active for 79 % of
+// the cycles of the busy SMs.  A step takes 2350 cycles; what else is lost lies at the
+// ends of items, where O is read out before the next item may write it, and in the
+// join.  The same prompts with other heads, from a graph: 8 on 1 of 512 (653 GFLOP,
+// the scores formed twice) 590 us, 1.11 PFLOP/s; 16 on 2 of 128
+// (326 GFLOP) 336 us, 0.97; 32 on 4 of 64, where half of the second product is zeros,
+// 581 us, 0.56.
 #include <cuda.h>
 
 #include "q4w_attn.cuh"

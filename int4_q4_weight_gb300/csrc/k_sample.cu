@@ -565,9 +565,10 @@ __device__ __forceinline__ bool narrow(const Part<T, KEEP>& part, Shared& sh, co
   u64 inside = (u64)((float)(sh.c_hi - sh.c_lo) / (0.91f * unit)) + 1;   // at most: a weight is 0.917 units or more
   float m_lo = (float)sh.m_lo * (1.f - eps), m_hi = (float)sh.m_lo * (1.f + eps);   // the mass before the range
   uint32_t k_lo = first_key(s, (float)(bin_hi + 1)), k_hi = bin == 0 ? key_of(s.top) : first_key(s, (float)bin) - 1;
-  // Three levels of 1024 reach single keys from any range; a level may also take
-  // less off, where the bounds are wide.  (A level takes 4 us of a few rows, the
-  // sorting of 2048 elements 11 us more than that of 1024.)
+  // Three levels of 1024 take up to 2^30 off the range, less where the bounds are wide;
+  // what is still too many then (a flat row's range is near 2^32 keys) goes the way of
+  // B to D.  (A level takes 4 us of a few rows, the sorting of 2048 elements 11 us more
+  // than that of 1024.)
   for (int level = 0; inside > (u64)kSortFew && level < 3; ++level) {
     int shift = 0;
     while (((k_hi - k_lo) >> shift) >= (uint32_t)kBins) ++shift;
@@ -793,7 +794,7 @@ __global__ void __launch_bounds__(kThr, KEEP ? 1 : 2) sample_kernel(const __grid
       for (int i = n + threadIdx.x; i < n2; i += kThr) sh.list[i] = ~0ull;
       bitonic(sh.list, n2);
     }
-    // cut: thread i holds elements 2 i and 2 i + 1
+    // cut: thread i holds the kPer elements from kPer i on
     constexpr int kPer = kCap / kThr;
     u64 w[kPer], mass_k = 0, sum = 0;
     const int nk = has_k ? min(n, k_in) : n;
