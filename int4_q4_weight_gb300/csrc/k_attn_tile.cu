@@ -47,7 +47,7 @@
 // the cycles of the busy SMs.  A step takes 2350 cycles; what else is lost lies at the
 // ends of items, where O is read out before the next item may write it, and in the
 // join.  The same prompts with other heads, from a graph: 8 on 1 of 512 (653 GFLOP,
-// the scores formed twice) 590 us, 1.11 PFLOP/s; 16 on 2 of 128
+// the scores formed twice) 585 us, 1.12 PFLOP/s; 16 on 2 of 128
 // (326 GFLOP) 336 us, 0.97; 32 on 4 of 64, where half of the second product is zeros,
 // 581 us, 0.56.
 #include <cuda.h>
@@ -597,6 +597,11 @@ __global__ void __launch_bounds__(kThr, 1) tile_kernel(const __grid_constant__ P
       // values that no row of the tile sees may be anything, and 0 times
       // infinity is no zero: they are cleared in shared memory
       if (k0 < w.x.lo || k0 + kKeys > w.x.end) {
+        // The parity tells two neighbouring phases apart.  With several slots the one
+        // before has landed (its step is NVS back, and this step's scores were issued
+        // after the values two steps back).  With one it is the step before, whose
+        // values may still be on their way: they have been used first.
+        if (NVS == 1 && j > 0) wait_values(j - 1);
         wait(full0 + 8 * (NKS + j % NVS), (j / NVS) & 1);
         const uint32_t vb = v_ring0 + j % NVS * S::kVSlot;
         // a thread clears one 16-byte piece of a row of every slab

@@ -298,6 +298,25 @@ def test_attention_several_steps_and_items_per_cta(cuda_lib, D, n, kv):
     check_attention(cuda_lib, Case(n, kv, 8, 1, D, 64, F16, seed=D))
 
 
+@pytest.mark.parametrize("D,hq,hkv,seqs,new", [(512, 16, 2, 100, 9), (512, 8, 8, 20, 90), (512, 64, 1, 200, 1), (256, 32, 2, 200, 9), (128, 40, 2, 200, 9),
+                                               (64, 80, 2, 200, 9)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_attention_many_short_items_one_after_the_other(cuda_lib, D, hq, hkv, seqs, new, window):
+    """Items of a few steps, most of which end inside a step, whose keys come late (the
+    cache is larger than L2): right, and the same bits every time."""
+    g = np.random.default_rng(D + seqs)
+    n = [int(x) for x in g.integers(1, new + 1, seqs)]
+    kv = [x + int(g.choice([g.integers(0, 40), g.integers(100, 600), g.integers(0, 1500)])) for x in n]
+    c = Case(n, kv, hq, hkv, D, 16, BF16, seed=seqs).stale(float("inf"))
+    out, lse = check_attention(cuda_lib, c, window=window)
+    again, flush = torch.empty_like(out), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(60):
+        if i % 2:
+            flush.fill_(i)
+        cuda_lib.kv_attention(c.q, *c.tables(), max_q=max(n), window=window, out=again)
+        assert torch.equal(out, again), i
+
+
 @pytest.mark.parametrize("D,hq,hkv,new", [(256, 8, 1, 1), (512, 8, 1, 1), (64, 3, 1, 1), (256, 8, 1, 64), (512, 4, 1, 50), (128, 4, 2, 90)])
 def test_attention_rows_that_see_nothing(cuda_lib, D, hq, hkv, new):
     """A length of zero, and lengths shorter than the new tokens."""
