@@ -433,7 +433,7 @@ int kv_attention(const q4_kv_cache* cache, int T, int max_q, const void* q,
  *   token: int32 [b]; logprob_opt: f32 [b], or NULL.
  *   1 <= b <= 65535; 1 <= V <= 1048576; stride >= V.  No workspace.
  * Masses are sums of integers: weights in units of 2^-42 of the largest, each
- * within about 2^-29 of itself and then cut down to whole units, so a mass of n
+ * within 2^-26 of itself and then cut down to whole units, so a mass of n
  * weights is up to n 2^-42 too small and a weight below 2^-42 is no part of it;
  * for u = 0 the token is the first of S, whatever its weight (one below 2^-128
  * counts as zero).

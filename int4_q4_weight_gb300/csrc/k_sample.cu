@@ -20,7 +20,8 @@
 // through a degree-6 polynomial of 2^(-f/8) to a 28-bit mantissa; the weight is
 // mantissa * 2^(-(n mod 8)/8) * 2^-(n div 8), cut off to units of 2^-42.
 // Integer sums have no order, so atomics and cluster reductions give the same
-// bits on every run.  A weight is off by about 2^-29 of itself, and cut downwards by
+// bits on every run.  A weight is off by up to 2^-26 of itself (2^-28.8 in the
+// root mean square: the polynomial in fp32 is most of it), and cut downwards by
 // less than a unit: a sum of n weights is up to n 2^-42 of the largest too small, and
 // nothing is left of a weight below 2^-42.  The log probability is therefore formed
 // from the chosen logit, ln of the mass alone from the integers; and u = 0, which asks
