@@ -604,9 +604,20 @@ def kv_rope_steps(rot_dim, theta=10000.0, device="cuda", freqs=None):
 # helper calls per tensor and ctypes structures.
 
 # Memory of torch's caching allocator on a stream, without a tensor around it: a workspace that
-# lives for one call (1 us; a tensor made and dropped between launches costs 5).
-_raw_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
-_raw_free = torch._C._cuda_cudaCachingAllocator_raw_delete
+# lives for one call (1 us; a tensor made and dropped between launches costs 5).  The calls are
+# private ones of torch's CUDA builds: where they are missing, a tensor is held instead.
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+if _raw_alloc is None or _raw_free is None:
+    _held = {}
+
+    def _raw_alloc(size, stream):
+        t = torch.empty(size, dtype=torch.uint8, device="cuda")   # on the current stream, which `stream` is
+        _held[t.data_ptr()] = t
+        return t.data_ptr()
+
+    def _raw_free(ptr):
+        del _held[ptr]
 
 
 def _heads(t, dtype, heads, dim, T, name):

@@ -1,6 +1,9 @@
 """On the CPU: the refusals of the quantised cache's entry points and of draft_verify, the
 binding's size checks, and the oracle of draft_verify against closed forms."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -150,3 +153,28 @@ def test_rounding_a_scale_up():
         assert up == float(np.float16(up)) and up >= x and (up == 0 or float(np.nextafter(np.float16(up), np.float16(0))) < x)
     codes, scales, bad = O8.quantise(np.linspace(-3, 3, 64)[None])
     assert not bad.any() and (np.abs(O8.values(codes, scales) - np.linspace(-3, 3, 64)) <= np.repeat(scales, 32, -1) / 2).all()
+
+
+@pytest.mark.parametrize("gone", [("alloc",), ("delete",), ("alloc", "delete")])
+def test_the_package_without_the_private_allocator_calls(gone):
+    """A build of torch that lacks them: the package is imported, its host checks answer, and a
+    workspace is a tensor that is held until it is given back."""
+    code = f"""
+import torch
+for n in {gone!r}:
+    delattr(torch._C, "_cuda_cudaCachingAllocator_raw_" + n)
+import int4_q4_weight_gb300 as q4w
+assert q4w.load().kv_read_q8(None, 1, None, None, None, None) != 0
+empty = torch.empty
+torch.empty = lambda n, dtype, device: empty(n, dtype=dtype)
+a, b = q4w._raw_alloc(4096, 0), q4w._raw_alloc(4096, 0)
+assert a != b and a and b
+q4w._raw_free(a)
+assert list(q4w._held) == [b]
+q4w._raw_free(b)
+assert not q4w._held
+"""
+    q4w.build()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
