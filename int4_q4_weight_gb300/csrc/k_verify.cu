@@ -632,6 +632,44 @@ __global__ void __launch_bounds__(kThr) choose_kernel(const __grid_constant__ Pa
 
 constexpr double kSumUnit = 2.2737367544323206e-13;   // 2^-42
 
+// Masses of p_n's row: those of the eight indices from i on, without the index that is left out.
+__device__ __forceinline__ void weigh_target(const Shared& sh, const Scale& s, int without, int i, const float (&v)[8], u64 (&w)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const Pair m = mantissas(s, v[j], v[j + 1]);
+    w[j] = sample::weight_of(sh.eighth, m.mant[0], m.n[0]), w[j + 1] = sample::weight_of(sh.eighth, m.mant[1], m.n[1]);
+  }
+  if ((unsigned)(without - i) < 8u) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = i + j != without ? w[j] : 0ull;
+  }
+}
+// The draw from p_n alone, wherever it is made: by the segments' masses of weigh_target(), and with u = 0
+// the first index that weighs anything, be it less than a unit.  False: nothing does.
+template <typename T, typename L, typename F>
+__device__ __forceinline__ bool draw_target(const Params& p, Shared& sh, const Row<T>& row, const Scale& s, int without, const u64* seg, float u,
+                                            L logs, F found) {
+  if (u != 0.f)
+    return draw(p, sh, seg, u, [&](int i, u64 (&w)[8], float (&v)[8]) {
+      row.load(i, v);
+      weigh_target(sh, s, without, i, v, w);
+    }, logs, found);
+  u64 mass = 0;
+  for (int g = threadIdx.x; g < p.n_segs; g += kThr) mass += __ldcg(seg + g);
+  block_incl(mass, sh.red, &mass);
+  if (threadIdx.x == 0) sh.first = 0x7fffffff, logs(mass);
+  __syncthreads();
+  for (int i0 = 0; i0 < p.V; i0 += kThr) {
+    const int i = i0 + threadIdx.x;
+    const bool some = i < p.V && i != without && eighths(s, capped(s, as_float(row.z[i]))) < (float)sample::kBins;
+    if (some) atomicMin(&sh.first, i);
+    if (__syncthreads_or(some)) break;
+  }
+  if (sh.first == 0x7fffffff) return false;
+  if (threadIdx.x == 0) found(sh.first, as_float(row.z[sh.first]));
+  return true;
+}
+
 // Exact masses of the listed rows, and the tokens that are drawn from p_n alone.  The CTAs behind
 // the first p.ctas form the log probabilities of the drafts that stand.
 // FEW: there was no choose_kernel, every CTA chooses for all of the few users.  (One user of four
@@ -685,22 +723,11 @@ __global__ void __launch_bounds__(kThr, kResident) sums_kernel(const __grid_cons
     const int user = c.user, n = c.n, without = c.without;
     const Scale s = make_scale(c.top, c.t, 0.f);
     const Row<T> row(row_of<T>(p, user, c.drafted ? k + 1 + n : n), p.V);
-    auto weigh = [&](int i, const float (&v)[8], u64 (&w)[8]) {
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const Pair m = mantissas(s, v[j], v[j + 1]);
-        w[j] = sample::weight_of(sh.eighth, m.mant[0], m.n[0]), w[j + 1] = sample::weight_of(sh.eighth, m.mant[1], m.n[1]);
-      }
-      if ((unsigned)(without - i) < 8u) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = i + j != without ? w[j] : 0ull;
-      }
-    };
     u64* seg = p.seg + (long long)user * 2 * p.n_segs;
     u64 mine = 0;
     row.sweep(first + warp, g1, [&](int g, const float (&v)[8]) {
       u64 w[8], sum = 0;
-      weigh(g * kSeg + 8 * lane, v, w);
+      weigh_target(sh, s, without, g * kSeg + 8 * lane, v, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum += w[j];
       sum = lanes_sum(sum);
@@ -722,28 +749,7 @@ __global__ void __launch_bounds__(kThr, kResident) sums_kernel(const __grid_cons
       p.tokens[(long long)user * (k + 1) + n] = i;
       if (p.logprobs) p.logprobs[(long long)user * (k + 1) + n] = log_prob(z, c.top, sh.per_t, sh.log_mass);
     };
-    const float u = random_of(p, user, k);
-    bool drawn = false;
-    if (u == 0.f) {   // the first that weighs anything, be it less than a unit
-      u64 mass = 0;
-      for (int g = threadIdx.x; g < p.n_segs; g += kThr) mass += __ldcg(seg + g);
-      block_incl(mass, sh.red, &mass);
-      if (threadIdx.x == 0) sh.first = 0x7fffffff, logs(mass);
-      __syncthreads();
-      for (int i0 = 0; i0 < p.V; i0 += kThr) {
-        const int i = i0 + threadIdx.x;
-        const bool some = i < p.V && i != without && eighths(s, capped(s, as_float(row.z[i]))) < (float)sample::kBins;
-        if (some) atomicMin(&sh.first, i);
-        if (__syncthreads_or(some)) break;
-      }
-      drawn = sh.first != 0x7fffffff;
-      if (drawn && threadIdx.x == 0) found(sh.first, as_float(row.z[sh.first]));
-    } else {
-      drawn = draw(p, sh, seg, u, [&](int i, u64 (&w)[8], float (&v)[8]) {
-        row.load(i, v);
-        weigh(i, v, w);
-      }, logs, found);
-    }
+    const bool drawn = draw_target<T>(p, sh, row, s, without, seg, random_of(p, user, k), logs, found);
     // nothing but x_n weighs anything
     if (!drawn && threadIdx.x == 0) logs(0ull), found(without, as_float(row.z[without]));
     __syncthreads();
@@ -761,6 +767,22 @@ __device__ __forceinline__ void divide_table(u64 mass, const uint32_t* eighth, u
   const u64 quotient = (r << 31) + (u64)(((off >> 10) * (long long)r) >> 22);   // 2^126 / m
   by[j] = (uint32_t)min(__umul64hi(quotient, (u64)eighth[j] << 32) >> 30, 0xffffffffull);
   if (j == 0) *shift = 21 - c + 60 - kUnit;
+}
+
+// The next token of a user whose rest is empty: from p_n.  (A function of its own: the kernel does not carry
+// two draws in line.)
+template <typename T>
+static __device__ __noinline__ void rest_from_target(const Params& p, Shared& sh, int unit) {
+  const Unit c = p.rest[unit];
+  const long long at = (long long)c.user * (p.k + 1) + c.n;
+  auto logs = [&](u64) {};   // found() forms them
+  auto found = [&](int i, float z) {
+    p.tokens[at] = i;
+    if (p.logprobs) p.logprobs[at] = log_prob(z, c.top, 1.0 / (double)c.t, log((double)sh.mass_p * kSumUnit));
+  };
+  __syncthreads();
+  draw_target<T>(p, sh, Row<T>(row_of<T>(p, c.user, c.n), p.V), make_scale(c.top, c.t, 0.f), -1,
+                 p.seg + (long long)c.user * 2 * p.n_segs, random_of(p, c.user, p.k), logs, found);
 }
 
 // Masses of the rest, max(p_n - q_n, 0), and the tokens drawn from it.
@@ -835,14 +857,7 @@ __global__ void __launch_bounds__(kThr, kResident) rest_kernel(const __grid_cons
       rq.load(i, y);
       weigh(v, y, w);
     }, logs, found);
-    if (!drawn) {   // the two are one: from p_n
-      __syncthreads();
-      draw(p, sh, seg - p.n_segs, u, [&](int i, u64 (&w)[8], float (&v)[8]) {
-        rp.load(i, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = weight(sh.eighth, sp, capped(sp, v[j]));
-      }, logs, found);
-    }
+    if (!drawn) rest_from_target<T>(p, sh, unit);   // the two are one
   }
 }
 
