@@ -380,8 +380,9 @@ int kv_append(const q4_kv_cache* cache, int T, const void* k, long long k_stride
  *   y = x / sqrt(mean(x^2) + eps) * w,
  * of the queries (q_norm), the keys (k_norm) and the values (v_norm): f32 weights
  * [head_dim] on the device, NULL for no norm of that kind (all ones: a norm without
- * weights).  q_norm only with q.  eps >= 0, finite.  The sum of squares is fp32
- * (magnitudes above 10^18 leave it), still one rounding to the cache's type.
+ * weights).  q_norm only with q.  eps >= 0, finite.  The arithmetic is fp32, for rows
+ * of any finite magnitude, with one rounding to the cache's type; a row of zeros with
+ * eps = 0 is 0 / 0, NaN.
  * Everything else is as for kv_append.                                     */
 int kv_append_norm(const q4_kv_cache* cache, int T, const void* k, long long k_stride,
                    const void* v, long long v_stride, int in_dtype, const void* q,

@@ -18,7 +18,8 @@
 // other, and while they run nothing else would be in flight.
 //
 // Two more forms of the same pass: with a norm of each head before the rotation,
-//   y = x rsqrt(mean x^2 + eps) w   (fp32, the D / 16 threads of a row sum by shuffles),
+//   y = x rsqrt(mean x^2 + eps) w   (fp32, the D / 16 threads of a row sum by shuffles; a row whose
+//   squares leave fp32 is summed again, scaled by a power of two),
 // and, after it, into a cache of int8 codes with a scale per 32 elements: the scale is the
 // block's largest magnitude / 127, rounded up to fp16, so that no code is cut off and a
 // value is half a scale off at most; a thread's two runs of eight lie in one block each,
@@ -113,6 +114,10 @@ __device__ __forceinline__ void scale8(float (&x)[8], float f, const float* w, i
 #pragma unroll
   for (int k = 0; k < 8; k += 2) f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), f2_mul(f2, f2_pack(ws[k], ws[k + 1]))), x[k], x[k + 1]);
 }
+
+// Where a mean of squares keeps its digits: what is lost below the normal numbers is 2^-40 of it, and
+// the sum of 512 is finite.
+constexpr float kLeastMean = 7.8886091e-31f, kMostMean = 1.3292280e36f;   // 2^-100, 2^120
 
 constexpr float kMaxScale = 515.5f;   // 127 of it are a finite fp16 number, as the attention needs
 // The largest magnitude as bits: a NaN's are above an infinity's.
@@ -232,19 +237,37 @@ __global__ void __launch_bounds__(kThr, MODE == kPlain ? 0 : MODE == kNorm ? 7 :
     if constexpr (MODE != kPlain) {
       const float* w = is_q ? p.q_norm : is_k ? p.k_norm : p.v_norm;
       if (w) {
-        f2_t sums = f2_pack(0.f, 0.f);
+        float eps = p.eps, mean;
+#pragma unroll 1
+        for (bool again = std::is_same<IN, __half>::value;; again = true) {
+          f2_t sums = f2_pack(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const f2_t x = f2_pack(a[i], a[i + 1]), y = f2_pack(b[i], b[i + 1]);
-          sums = f2_fma(x, x, f2_fma(y, y, sums));
+          for (int i = 0; i < 8; i += 2) {
+            const f2_t x = f2_pack(a[i], a[i + 1]), y = f2_pack(b[i], b[i + 1]);
+            sums = f2_fma(x, x, f2_fma(y, y, sums));
+          }
+          float sum, odd;
+          f2_unpack(sums, sum, odd);
+          sum += odd;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            if (chunks > o) sum += __shfl_xor_sync(peers, sum, o);
+          mean = fmaf(sum, p.inv_d, eps);
+          if (again || (mean >= kLeastMean && mean <= kMostMean)) break;
+          // Once more, the row and the root of eps times a power of two that leaves the larger of them in
+          // [1, 2).  (The lanes of a row have the same sum, bit for bit.)
+          uint32_t top = max(top_bits(a), top_bits(b));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            if (chunks > o) top = max(top, __shfl_xor_sync(peers, top, o));
+          int e = (int)(top >> 23) - 127;
+          if (eps > 0.f) e = max(e, ((int)(__float_as_uint(eps) >> 23) - 127) >> 1);
+          const float by = __uint_as_float((uint32_t)(127 - min(max(e, -126), 126)) << 23);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] *= by, b[i] *= by;
+          eps = eps * by * by;
         }
-        float sum, odd;
-        f2_unpack(sums, sum, odd);
-        sum += odd;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          if (chunks > o) sum += __shfl_xor_sync(peers, sum, o);
-        const float f = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+        const float f = rsqrtf(mean);
         scale8(a, f, w, lo);
         scale8(b, f, w, hi);
       }

@@ -594,3 +594,82 @@ def test_a_step_with_norms_an_int8_cache_and_drafted_tokens(cuda_lib):
         k, v, q = (normal(c.gen, 8, h, 128, dtype=F32) for h in (2, 2, 8))
         c.q = q4w.kv_append_q8(k, v, *c.tables(), q_norm=w, k_norm=w, steps=steps, q=q)
         check_attention(q4w, c)
+
+
+def rows_of_any_size(D, inp, heads=2):
+    """Normal rows times 10^-42 (subnormal numbers) to 10^37, and rows that span forty decades."""
+    g = np.random.default_rng(D)
+    scales = [1e-42, 1e-38, 1e-30, 1e-23, 1e-19, 1e-15, 1.0, 1e15, 1e19, 1e25, 1e37]
+    x = np.stack([g.standard_normal((heads, D)) * s for s in scales] + [g.standard_normal((heads, D)) * 10.0 ** g.uniform(a, b, (heads, D)) for a, b in ((-40, 0), (-20, 20), (0, 37))])
+    return torch.from_numpy(x.astype(np.float32)).to(inp).cuda()
+
+
+@pytest.mark.parametrize("plain", [True, False])
+@pytest.mark.parametrize("D", [64, 128, 512])
+@pytest.mark.parametrize("inp", [F32, BF16])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-30, 1e-6, 1e36])
+def test_append_norms_of_rows_of_any_size(cuda_lib, plain, D, inp, eps):
+    """Squares that fp32 does not hold, above and below, next to rows whose squares it does: every element
+    to the 1.2e-6 of a norm and its rounding (bf16: half a step, 2^-134 where it is subnormal).  (10^-42 is
+    zero in bf16, whose least number is 2^-133: with eps = 0 that row is 0 / 0.)"""
+    q4w = cuda_lib
+    eps = float(np.float32(eps))
+    x = rows_of_any_size(D, inp)
+    T, half = x.shape[0], torch.finfo(BF16).eps / 2
+    c = Case([T], [T], 2, 2, D, 16, BF16, plain=plain)
+    w = normal(c.gen, D, dtype=F32, std=0.3) + 1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call, more = (q4w.kv_append_norm, {}) if plain else (q4w.kv_append_q8, {"dtype": BF16})
+    q = call(x, x, *c.tables(), q_norm=w, k_norm=w, v_norm=w, eps=eps, q=x, err=err, **more)
+    with np.errstate(invalid="ignore"):
+        ref = O8.norm(f64(x), f64(w), eps)
+    empty = np.isnan(ref)
+    assert empty.any() == (eps == 0 and inp is BF16) and int(err) == int(not plain and empty.any())
+    tol = (half * 1.01 + 1.2e-6) * np.abs(ref) + 2.0 ** -134
+
+    def near(got, t):
+        return np.array_equal(np.isnan(got), empty[t]) and np.all((np.abs(got - ref[t]) <= tol[t]) | empty[t])
+
+    assert near(f64(q), slice(None))
+    table = c.table.cpu().numpy()[0]
+    for t in range(T):
+        for cache in (c.kc, c.vc):
+            page, row = int(table[t // 16]), t % 16
+            if plain:
+                assert near(f64(cache[page, :, row]), t), t
+                continue
+            codes, scales = f64(cache[0][page, :, row]), f64(cache[1][page, :, row])
+            if empty[t].any():
+                assert not codes.any() and not scales.any()
+                continue
+            # (what is quantised is an fp32 number: below 2^-126 it is a multiple of 2^-149)
+            wide, off = np.repeat(scales, 32, axis=-1), 1.2e-6 * np.abs(ref[t]) + 2.0 ** -149
+            top = np.abs(ref[t].reshape(2, -1, 32)).max(-1)
+            assert np.all(np.abs(codes * wide - ref[t]) <= wide / 2 * (1 + 1e-5) + off), t
+            assert np.all(scales * 127 <= top * (1 + 1.2e-6) * (1 + 2.0 ** -10) + 127 * 2.0 ** -24), t
+
+
+@pytest.mark.parametrize("inp", [F32, F16, BF16])
+@pytest.mark.parametrize("plain", [True, False])
+def test_append_norms_of_rows_of_zeros(cuda_lib, inp, plain):
+    """Zeros with any eps above 0; 0 / 0, which is NaN, without: the int8 cache stores zeros and sets err."""
+    q4w = cuda_lib
+    for eps in (0.0, 1e-44, 1e-6, 3e38):
+        c = Case([3], [3], 1, 1, 64, 16, BF16, plain=plain)
+        x = torch.zeros(3, 1, 64, dtype=inp, device="cuda")
+        x[1] = 1
+        w = torch.ones(64, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        call, more = (q4w.kv_append_norm, {}) if plain else (q4w.kv_append_q8, {"dtype": BF16})
+        q = call(x, x, *c.tables(), q_norm=w, k_norm=w, v_norm=w, eps=eps, q=x, err=err, **more)
+        zeros = q[[0, 2]]
+        assert bool(zeros.isnan().all()) if eps == 0.0 else not zeros.any()
+        page = int(c.table[0, 0])
+        for cache in (c.kc, c.vc):
+            if plain:
+                got = cache[page, 0, [0, 2]]
+                assert bool(got.isnan().all()) if eps == 0.0 else not got.any()
+            else:
+                assert not cache[0][page, 0, [0, 2]].any() and not cache[1][page, 0, [0, 2]].any()
+        assert int(err) == (0 if plain or eps > 0 else 1)
+        assert float(q[1, 0, 0]) == (1.0 if eps < 1 else float(torch.tensor(3e38 ** -0.5).to(BF16)))
