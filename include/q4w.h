@@ -471,8 +471,9 @@ int kv_attention(const q4_kv_cache* cache, int T, int max_q, const void* q,
  * absolute error of 2^-32 of the row's largest or less where they are small.  With queries in bf16, elements below 2^-28 of a row's
  * largest lose digits.  Scales are at most 515.5, as kv_append_q8 leaves them: with
  * larger or infinite ones the tokens that see them get no defined result.
- * ws: kv_attention_q8_ws_bytes() bytes; it grows with T and n_q where max_q makes
- * many query rows per KV head.                                            */
+ * ws: kv_attention_q8_ws_bytes() bytes.  Where max_q makes many query rows per KV head
+ * it grows with T and n_q, for queries in bf16; with fp16 ones T = 0 gives the size of
+ * calls of any T.                                                         */
 size_t kv_attention_q8_ws_bytes(int T, int max_q, int n_q, int n_kv, int head_dim);
 int kv_attention_q8(const q4_kv_cache_q8* cache, int T, int max_q, const void* q,
                     long long q_stride, int n_q, float scale, int window, void* out,

@@ -844,22 +844,38 @@ def _attention_ws_bytes(max_q, n_q, n_kv, head_dim, device, T=None):
     return n
 
 
-def _attention_ws(max_q, n_q, n_kv, head_dim, device, T=None):
+@functools.lru_cache(maxsize=256)
+def _attention_q8_grows(max_q, n_q, n_kv, head_dim, device):
+    """Whether the workspace of bf16 queries grows with their tokens."""
+    sizes = (max_q, n_q, n_kv, head_dim, device)
+    return _attention_ws_bytes(*sizes, 1) > _attention_ws_bytes(*sizes, 0)
+
+
+def _attention_q8_ws_bytes(T, dtype, *sizes):
+    # (T is no part of the key where the size does not go by it)
+    return _attention_ws_bytes(*sizes, T if dtype is torch.bfloat16 and _attention_q8_grows(*sizes) else 0)
+
+
+def _ws_device(device):
     device = torch.device(device)
     if device.type != "cuda":
         raise Q4Error(f"a workspace lies on a CUDA device, not on {device}")
-    n = _attention_ws_bytes(max_q, n_q, n_kv, head_dim, torch.cuda.current_device() if device.index is None else device.index, T)
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    return device, torch.cuda.current_device() if device.index is None else device.index
 
 
 def kv_attention_ws(max_q, n_q, n_kv, head_dim, device):
     """A workspace for kv_attention calls of these sizes that do not overlap."""
-    return _attention_ws(max_q, n_q, n_kv, head_dim, device)
+    device, index = _ws_device(device)
+    return torch.empty(max(_attention_ws_bytes(max_q, n_q, n_kv, head_dim, index), 16), dtype=torch.uint8, device=device)
 
 
-def kv_attention_q8_ws(T, max_q, n_q, n_kv, head_dim, device):
-    """A workspace for kv_attention_q8 calls of up to T tokens that do not overlap."""
-    return _attention_ws(max_q, n_q, n_kv, head_dim, device, T)
+def kv_attention_q8_ws(T, max_q, n_q, n_kv, head_dim, device, dtype=torch.bfloat16):
+    """A workspace for kv_attention_q8 calls of up to T tokens that do not overlap; dtype: of their
+    queries (one for bfloat16 serves float16 too)."""
+    device, index = _ws_device(device)
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise Q4Error(f"the queries' type must be torch.float16 or torch.bfloat16, got {dtype}")
+    return torch.empty(max(_attention_q8_ws_bytes(T, dtype, max_q, n_q, n_kv, head_dim, index), 16), dtype=torch.uint8, device=device)
 
 
 def kv_attention(q, k_cache, v_cache, block_table, cu_tokens, kv_lens, max_q=None, scale=None, window=0, out=None,
@@ -908,7 +924,8 @@ def _attention(name, cache, dtype, n_kv, D, q, max_q, scale, window, out, lse, w
         raise Q4Error(f"n_q={n_q} must be a multiple of n_kv={n_kv}")
     stream, mine = _stream(), None
     if ws is None:
-        size = _attention_ws_bytes(max_q, n_q, n_kv, D, q.get_device(), T if name == "kv_attention_q8" else None)
+        sizes = (max_q, n_q, n_kv, D, q.get_device())
+        size = _attention_q8_ws_bytes(T, dtype, *sizes) if name == "kv_attention_q8" else _attention_ws_bytes(*sizes)
         ws_ptr = mine = _raw_alloc(size, stream)
     else:
         _dev(ws, torch.uint8, "ws")

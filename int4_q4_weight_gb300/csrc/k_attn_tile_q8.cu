@@ -69,7 +69,7 @@ static int launch_t(Params& p, int D, const DeviceInfo& dev, cudaStream_t s) {
 
 }  // namespace tile
 
-// The parts, then the rows of bf16 queries as fp16 and their factors.
+// The parts, then T tokens' rows of bf16 queries as fp16 and their factors (0 tokens: fp16 queries).
 size_t attn_tile_q8_ws_bytes(long long T, int n_q, int D, const DeviceInfo& dev) {
   return attn_tile_ws_bytes(D, dev) + attn_up256((size_t)T * n_q * D * 2) + attn_up256((size_t)T * n_q * 4);
 }

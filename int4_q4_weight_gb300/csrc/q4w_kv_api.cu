@@ -212,7 +212,7 @@ int kv_attention(const q4_kv_cache* cache, int T, int max_q, const void* q, long
 
 size_t kv_attention_q8_ws_bytes(int T, int max_q, int n_q, int n_kv, int head_dim) {
   DeviceInfo dev;
-  if (T < 1 || max_q < 1 || n_kv < 1 || n_q < n_kv || head_dim < 1 || current_device(&dev) != Q4_OK) return 0;
+  if (T < 0 || max_q < 1 || n_kv < 1 || n_q < n_kv || head_dim < 1 || current_device(&dev) != Q4_OK) return 0;
   return attn_q8_ws_bytes(T, n_q, (long long)max_q * (n_q / n_kv), head_dim, dev);
 }
 
@@ -228,7 +228,8 @@ int kv_attention_q8(const q4_kv_cache_q8* cache, int T, int max_q, const void* q
   if ((st = check_attention(&c, p)) != Q4_OK) return st;
   CHECK_ALIGN(ws);
   DEVICE_OR_RETURN(dev);
-  if ((st = check_ws(ws, ws_bytes, attn_q8_ws_bytes(T, n_q, (long long)max_q * (n_q / c.n_kv), c.head_dim, dev))) != Q4_OK) return st;
+  const int rows_of = c.dtype == Q4_BF16 ? T : 0;   // fp16 queries are read as they are
+  if ((st = check_ws(ws, ws_bytes, attn_q8_ws_bytes(rows_of, n_q, (long long)max_q * (n_q / c.n_kv), c.head_dim, dev))) != Q4_OK) return st;
   return launch_kv_attention_q8(p, c, ws, dev, reinterpret_cast<cudaStream_t>(stream));
 }
 

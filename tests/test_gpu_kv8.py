@@ -673,3 +673,25 @@ def test_append_norms_of_rows_of_zeros(cuda_lib, inp, plain):
                 assert not cache[0][page, 0, [0, 2]].any() and not cache[1][page, 0, [0, 2]].any()
         assert int(err) == (0 if plain or eps > 0 else 1)
         assert float(q[1, 0, 0]) == (1.0 if eps < 1 else float(torch.tensor(3e38 ** -0.5).to(BF16)))
+
+
+@pytest.mark.parametrize("D", [64, 256, 512])
+def test_attention_workspace_of_fp16_queries(cuda_lib, D):
+    """Queries that are read as they are need no room for themselves: a workspace that does not go by T is
+    enough, and nothing is written behind it; bf16 ones are refused with it."""
+    q4w = cuda_lib
+    lib = q4w.load()
+    big = lib.kv_attention_q8_ws_bytes(16384, 2048, 32, 4, D)
+    small = lib.kv_attention_q8_ws_bytes(0, 2048, 32, 4, D)
+    assert big - small >= 16384 * 32 * D * 2
+    assert lib.kv_attention_q8_ws_bytes(0, 1, 8, 1, D) == lib.kv_attention_q8_ws_bytes(16384, 1, 8, 1, D) > 0
+    assert q4w.kv_attention_q8_ws(16384, 2048, 32, 4, D, "cuda", dtype=F16).numel() == small
+    assert q4w.kv_attention_q8_ws(16384, 2048, 32, 4, D, "cuda").numel() == big
+    need = lib.kv_attention_q8_ws_bytes(0, 70, 8, 1, D)
+    held = torch.full((need + 4096,), 201, dtype=torch.uint8, device="cuda")
+    check_attention(q4w, Case([70, 40], [400, 900], 8, 1, D), ws=held[:need])
+    assert bool((held[need:] == 201).all())
+    c = Case([70, 40], [400, 900], 8, 1, D, dtype=BF16)
+    with pytest.raises(q4w.Q4Error, match="ws must hold"):
+        q4w.kv_attention_q8(c.q, *c.tables(), max_q=70, ws=held[:need])
+    check_attention(q4w, c, ws=q4w.kv_attention_q8_ws(c.T, 70, 8, 1, D, "cuda", dtype=BF16))

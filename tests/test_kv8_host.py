@@ -178,3 +178,42 @@ assert not q4w._held
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_workspace_sizes_of_the_quantised_attention(monkeypatch):
+    """T counts for bf16 queries where the size grows with it, and is no part of what is kept elsewhere."""
+    asked = []
+
+    class Lib:
+        def kv_attention_q8_ws_bytes(self, T, max_q, n_q, n_kv, head_dim):
+            asked.append((T, max_q))
+            return 1000 if max_q < 10 else 2000 + 10 * T
+
+    class Device:
+        def __init__(self, i):
+            pass
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *a):
+            pass
+
+    monkeypatch.setattr(q4w, "load", lambda: Lib())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: n)
+    for f in (q4w._attention_ws_bytes, q4w._attention_q8_grows):
+        f.cache_clear()
+    try:
+        ws = lambda T, max_q, **kw: q4w.kv_attention_q8_ws(T, max_q, 8, 1, 256, "cuda", **kw)   # noqa: E731
+        assert [ws(T, 40) for T in (40, 50)] == [2400, 2500]
+        assert [ws(T, 40, dtype=torch.float16) for T in (40, 50)] == [2000, 2000]
+        n = len(asked)
+        assert {ws(T, 1, dtype=d) for T in range(1, 600) for d in (torch.float16, torch.bfloat16)} == {1000}
+        assert len(asked) <= n + 2
+        with pytest.raises(q4w.Q4Error):
+            ws(40, 40, dtype=torch.float32)
+    finally:
+        for f in (q4w._attention_ws_bytes, q4w._attention_q8_grows):
+            f.cache_clear()
