@@ -695,3 +695,17 @@ def test_attention_workspace_of_fp16_queries(cuda_lib, D):
     with pytest.raises(q4w.Q4Error, match="ws must hold"):
         q4w.kv_attention_q8(c.q, *c.tables(), max_q=70, ws=held[:need])
     check_attention(q4w, c, ws=q4w.kv_attention_q8_ws(c.T, 70, 8, 1, D, "cuda", dtype=BF16))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [17, 20, 24, 25, 31, 32, 33])
+def test_attention_bf16_rows_next_to_the_kernels_limits(cuda_lib, D, rows):
+    """17 to 32 rows per KV head of bf16 queries, which are scaled and take one piece of P: as tokens of one
+    head and as heads of few tokens, with rows of magnitudes that fp16 does not hold."""
+    for hq, new in [(1, rows)] + [(h, rows // h) for h in (rows, rows // 2, 4) if h > 1 and rows % h == 0]:
+        c = stale(Case([new, 1, new], [new, 70, 190 + new], hq, 1, D, 16, BF16, seed=rows + hq), float("inf"))
+        check_attention(cuda_lib, c)
+        check_attention(cuda_lib, c, window=60)
+        c.q[-1] *= 1e30
+        c.q[0] *= 1e-30
+        check_attention(cuda_lib, c, scale=1e-30)
