@@ -65,7 +65,7 @@
 //
 // Bound: the latency of the roles, which share four schedulers.  Four prompts of up to
 // 2048 tokens over up to 8192 keys (8 heads on 1 of 256, 181 GFLOP of a 16-bit cache's products), bf16:
-// 209 us with queries and join, 16-bit cache 124; a step takes 4200 cycles, three quarters of them
+// 211 us with queries and join, 16-bit cache 124; a step takes 4200 cycles, three quarters of them
 // products.  What brought it there from 330: three warps each for K and V could not widen a step
 // in its time (an instruction of theirs takes 12 cycles), so fourteen; a table lookup and
 // walk per step for all of them in one warp (a ring of plans); reads for the next slot behind all
@@ -843,8 +843,12 @@ __global__ void __launch_bounds__((Shape<D, Q8>::kThreads), 1) tile_kernel(const
     // the masked scores' infinity to infinity
     float sc = a.scale == 0.f ? 1e-30f : a.scale * 1.4426950408889634f;
     float m = -CUDART_INF_F, l = 0.f;
-    [[maybe_unused]] float mr = 0.f;   // int8 cache: the score that m lies `below` under, not scaled: any two
-                                       // scores of bf16 queries, up to 2^100, then have an exact difference
+    // int8 cache: the reference lies `below` under the largest score, which is held unscaled (neg: with its sign
+    // turned).  Differences of scores are then exact, and none passes the reference by more than `move`, however
+    // large they are (of bf16 queries, up to 2^100): `most` is the magnitude where it moves, rounded down.  m, with
+    // the rounding of an fp32 number of its size, is formed where a part or a log-sum is written.
+    [[maybe_unused]] float neg = 0.f, most = -CUDART_INF_F;
+    [[maybe_unused]] auto top_of = [&]() { return most == -CUDART_INF_F ? most : sc < 0.f ? neg : -neg; };
     bool first = true, opens = w.local == 0, dead = false;
     const int row_tok = row < p.tokens * p.group ? row / p.group : 1 << 28, row_head = row % p.group;
     int lo = 0, hi = -1, tok = 0;
@@ -872,7 +876,7 @@ __global__ void __launch_bounds__((Shape<D, Q8>::kThreads), 1) tile_kernel(const
       lo = kv_first(pos, a.window);
       hi = min(pos, w.x.end - 1);
       m = -CUDART_INF_F, l = 0.f;
-      mr = 0.f;
+      neg = 0.f, most = -CUDART_INF_F;
       first = true;
     };
     if (n_steps > 0) begin();
@@ -945,13 +949,22 @@ __global__ void __launch_bounds__((Shape<D, Q8>::kThreads), 1) tile_kernel(const
         row_sh[half][j & 1][row] = Q8 || mx == -CUDART_INF_F ? mx : mx * fabsf(sc);
       }
       meet();
-      float mx = fmaxf(row_sh[0][j & 1][row], row_sh[1][j & 1][row]);
-      [[maybe_unused]] const float raw = mx;   // int8 cache: not scaled yet
-      if constexpr (Q8) mx *= fabsf(sc);
-      if (__any_sync(0xffffffffu, mx > m + Reference<P16>::move)) {
-        const float m2 = fmaxf(m, mx - Reference<P16>::below), f = m2 == -CUDART_INF_F ? 1.f : ex2(m - m2);
-        if (Q8 && m2 > m) mr = sc < 0.f ? -raw : raw;
-        m = m2;
+      const float mx = fmaxf(row_sh[0][j & 1][row], row_sh[1][j & 1][row]);   // (int8 cache: not scaled)
+      if (__any_sync(0xffffffffu, mx > (Q8 ? most : m + Reference<P16>::move))) {
+        float f;
+        if constexpr (Q8) {
+          const float top = top_of(), t2 = fmaxf(top, mx);
+          f = 1.f;
+          if (t2 > top) {
+            f = ex2((top - t2) * fabsf(sc));
+            neg = sc < 0.f ? t2 : -t2;
+            most = __fadd_rd(t2, (Reference<P16>::move - Reference<P16>::below) / fabsf(sc));
+          }
+        } else {
+          const float m2 = fmaxf(m, mx - Reference<P16>::below);
+          f = m2 == -CUDART_INF_F ? 1.f : ex2(m - m2);
+          m = m2;
+        }
         l *= f;
         if (!first) {   // O holds the steps before: let the last one finish
           wait_values(j - 1);
@@ -966,7 +979,7 @@ __global__ void __launch_bounds__((Shape<D, Q8>::kThreads), 1) tile_kernel(const
           }
         }
       }
-      const float mb = m == -CUDART_INF_F ? 0.f : m;
+      [[maybe_unused]] const float mb = m == -CUDART_INF_F ? 0.f : m;
       {
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         [[maybe_unused]] f2_t pairs[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
@@ -976,7 +989,7 @@ __global__ void __launch_bounds__((Shape<D, Q8>::kThreads), 1) tile_kernel(const
           scores_of(h);
           uint32_t u[N];
           if constexpr (Q8) {
-            const f2_t neg = f2_pack(-mr, -mr), by = f2_pack(sc, sc), add = f2_pack(Reference<P16>::below, Reference<P16>::below);
+            const f2_t ref = f2_pack(neg, neg), by = f2_pack(sc, sc), add = f2_pack(Reference<P16>::below, Reference<P16>::below);
             constexpr int M = SPLIT_P ? 8 : N;   // pairs at once: two pieces of eight take the registers of one of 16
 #pragma unroll
             for (int g = 0; g < N; g += M) {
@@ -984,7 +997,7 @@ __global__ void __launch_bounds__((Shape<D, Q8>::kThreads), 1) tile_kernel(const
 #pragma unroll
               for (int i = g; i < g + M; ++i) {
                 float x0, x1;
-                f2_unpack(f2_fma(f2_add(f2_pack(s[2 * i], s[2 * i + 1]), neg), by, add), x0, x1);
+                f2_unpack(f2_fma(f2_add(f2_pack(s[2 * i], s[2 * i + 1]), ref), by, add), x0, x1);
                 const float e0 = ex2(x0), e1 = ex2(x1);
                 pairs[i & 1] = f2_add(pairs[i & 1], f2_pack(e0, e1));
                 u[i] = Half16<P16>::pack(e0, e1);
@@ -1057,6 +1070,7 @@ __global__ void __launch_bounds__((Shape<D, Q8>::kThreads), 1) tile_kernel(const
       row_sh[half][j & 1][row] = l;   // every maximum in it has been read: the step's products are complete
       meet();
       l = row_sh[0][j & 1][row] + row_sh[1][j & 1][row];
+      if constexpr (Q8) m = top_of() * fabsf(sc) - Reference<P16>::below;
       const long long orow = (long long)(w.s.cu + tok) * a.n_q + w.head * p.group + row_head;
       const long long slot = (2ll * pair + (opens ? 1 : 0)) * 2 + rank;
       const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -709,3 +709,34 @@ def test_attention_bf16_rows_next_to_the_kernels_limits(cuda_lib, D, rows):
         c.q[-1] *= 1e30
         c.q[0] *= 1e-30
         check_attention(cuda_lib, c, scale=1e-30)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("seqs", [1, 120])
+def test_attention_huge_scores_a_step_apart(cuda_lib, dtype, sign, seqs):
+    """Two keys in different steps of the tile kernel whose scores are neighbouring numbers of fp32, 2^15 or more
+    apart after the scale.  In one CTA (most items of 120 sequences) their difference is exact and the larger takes
+    everything.  Parts of several CTAs (one sequence) are joined by references that are fp32 numbers: the scaled
+    scores are one such number, here by construction, so the two may share the row.  Never anything else."""
+    c = Case([40] * seqs, [400] * seqs, 8, 1, 64, 16, dtype)
+    big, one = (2.0 ** 15, 2.0 ** -5) if dtype is F16 else (2.0 ** 20, 1.0)
+    scale = 2.0 ** 20
+    # scores big * 12 + one * i: i steps of fp32 above 1.5 2^k
+    sc = np.float32(np.float32(scale) * np.float32(1.4426950408889634))
+    score = [np.float32(12 * big + one * i) for i in range(100)]
+    same = [i for i in range(1, 99) if score[i] < score[i + 1] and score[i] * sc == score[i + 1] * sc]
+    assert same
+    for x in (c.kc, c.vc):
+        x[0].zero_()
+        x[1].fill_(1.0)
+    c.q.zero_()
+    c.q[..., 0], c.q[..., 1] = big, one
+    table = c.table.long()
+    for i in same[:3]:
+        for pos, step, value in ((3, i, 50), (200, i + 1, 100)):
+            pages = table[:, pos // 16]
+            c.kc[0][pages, 0, pos % 16, 0], c.kc[0][pages, 0, pos % 16, 1], c.vc[0][pages, 0, pos % 16] = sign * 12, sign * step, value
+        out, _ = cuda_lib.kv_attention_q8(c.q, *c.tables(), max_q=40, scale=sign * scale)
+        assert bool(((out >= 50) & (out <= 100)).all())
+        assert seqs == 1 or float((out == 100).float().mean()) > 0.5
