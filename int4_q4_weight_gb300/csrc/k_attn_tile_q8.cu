@@ -5,9 +5,8 @@
 namespace q4w {
 namespace tile {
 
-// bf16 queries as fp16: a row times the power of two that brings its largest element to
-// 2^14 .. 2^15 (at most 2^100), which is exact for elements down to 2^-28 of it.  A warp
-// a row; HBM, of a few per cent of the attention's time.
+// bf16 queries as fp16, a row times query_factor().  A warp a row; HBM, of a few per cent of the
+// attention's time.
 constexpr int kQueryThr = 256;
 template <int D>
 __global__ void __launch_bounds__(kQueryThr) query_kernel(const __nv_bfloat16* q, long long stride, int T, int n_q, __half* out, float* row_scale) {
@@ -27,8 +26,7 @@ __global__ void __launch_bounds__(kQueryThr) query_kernel(const __nv_bfloat16* q
     const float2 f = Half16<__nv_bfloat16>::unpack(x[i]);
     top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
   }
-  const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23);   // 0: nothing to scale, 255: not finite
-  const float f = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(268 - e, 227) << 23) : 1.f;
+  const float f = query_factor(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
   uint32_t* dst = reinterpret_cast<uint32_t*>(out + row * D) + lane * E;
 #pragma unroll
   for (int i = 0; i < E; ++i) {

@@ -100,11 +100,6 @@ __device__ __forceinline__ void store8(OUT* p, const float (&x)[8]) {
                                             Half16<OUT>::pack(x[4], x[5]), Half16<OUT>::pack(x[6], x[7]));
 }
 
-__device__ __forceinline__ f2_t f2_mul(f2_t a, f2_t b) {
-  f2_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // Eight elements times f and their norm weights, from element i on.  The weights come from
 // L1 for every row: held in registers (16) they cost a third of the resident threads.
 __device__ __forceinline__ void scale8(float (&x)[8], float f, const float* w, int i) {

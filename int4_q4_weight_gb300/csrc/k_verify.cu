@@ -188,7 +188,7 @@ struct Running {
       float d0, d1;
       f2_unpack(f2_add(f2_pack(v[2 * j], v[2 * j + 1]), below), d0, d1);
       const f2_t d = f2_pack(fmaxf(d0, c.least), fmaxf(d1, c.least));
-      f2_unpack(f2_fma(d, ch, sample::f2_mul(d, cl)), d0, d1);
+      f2_unpack(f2_fma(d, ch, f2_mul(d, cl)), d0, d1);
       w[j] = f2_pack(ex2(d0), ex2(d1));
     }
 #pragma unroll

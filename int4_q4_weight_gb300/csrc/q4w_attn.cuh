@@ -40,6 +40,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// What a row of bf16 queries is multiplied by to become fp16: the power of two that brings its largest
+// magnitude `top` to 2^14 .. 2^15 (at most 2^100), exact for elements down to 2^-28 of it.  1 where
+// there is nothing to scale, or an element is not finite.
+__device__ __forceinline__ float query_factor(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23);   // exponent + 127
+  return e > 0 && e < 255 ? __uint_as_float((uint32_t)min(14 + 127 + 127 - e, 227) << 23) : 1.f;
+}
+
 // Where a row's running reference m lies (units of log2 e): it is set `below` under the
 // maximum and moved when a score passes it by `move`, so that most steps rescale nothing.
 // The probabilities 2^(s - m) enter the second product in 16 bits.  bf16 has the range of

@@ -385,9 +385,7 @@ __global__ void __launch_bounds__((Shape<D, NT, Q8>::kThr), 1) decode_kernel(con
           }
         float f = 1.f;
         if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-          const int e = (int)(__float_as_uint(top) >> 23);   // exponent + 127; 0: nothing to scale, 255: not finite
-          if (e > 0 && e < 255) f = __uint_as_float((uint32_t)(min(141 - e + 127, 227)) << 23);   // 2^(14 - (e - 127)), at most 2^100
+          f = query_factor(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
         }
         if (lane == 0) row_scale_sh[r] = 1.f / f;
 #pragma unroll

@@ -63,6 +63,11 @@ __device__ __forceinline__ float nib_odd(uint32_t s) {   // bits [19,23) -> 16 +
   return __uint_as_float((s & 0x00780000u) | 0x41800000u);
 }
 
+__device__ __forceinline__ f2_t f2_mul(f2_t a, f2_t b) {
+  f2_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ f2_t f2_add(f2_t a, f2_t b) {
   f2_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));

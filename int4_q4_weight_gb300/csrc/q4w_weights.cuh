@@ -104,11 +104,6 @@ struct Pair {
   uint32_t mant[2];
   int n[2];
 };
-__device__ __forceinline__ f2_t f2_mul(f2_t a, f2_t b) {
-  f2_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ f2_t f2_both(float v) { return f2_pack(v, v); }
 __device__ __forceinline__ Pair mantissas(const Scale& s, float z0, float z1) {
   const f2_t minus = f2_both(-1.f), top = f2_both(s.top), ch = f2_both(s.ch);
