@@ -716,7 +716,10 @@ def _kv_cache_q8(k_cache, v_cache, block_table, cu_tokens, kv_lens, dtype):
     """The checked quantised cache as (the bytes of its q4_kv_cache_q8, n_kv, head_dim)."""
     if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise Q4Error(f"the queries' type must be torch.float16 or torch.bfloat16, got {dtype}")
-    (kc, ks), (vc, vs) = k_cache, v_cache
+    try:
+        (kc, ks), (vc, vs) = k_cache, v_cache
+    except (TypeError, ValueError):
+        raise Q4Error("k_cache and v_cache must each be a pair of codes and scales") from None
     i32, i8, f16 = torch.int32, torch.int8, torch.float16
     if not (kc.dtype is i8 and vc.dtype is i8 and ks.dtype is f16 and vs.dtype is f16 and block_table.dtype is i32 and cu_tokens.dtype is i32
             and kv_lens.dtype is i32 and _here(kc) and _here(vc) and _here(ks) and _here(vs) and _here(block_table) and _here(cu_tokens)

@@ -217,3 +217,17 @@ def test_workspace_sizes_of_the_quantised_attention(monkeypatch):
     finally:
         for f in (q4w._attention_ws_bytes, q4w._attention_q8_grows):
             f.cache_clear()
+
+
+@pytest.mark.parametrize("cache", [torch.zeros(3, 2, 16, 64, dtype=torch.int8), torch.zeros(()), None, (torch.zeros(3),), (1, 2, 3)])
+def test_a_quantised_cache_is_a_pair(fake, cache):
+    """A cache without its scales is refused by name, not by Python's unpacking."""
+    pair = (torch.zeros(3, 2, 16, 64, dtype=torch.int8), torch.zeros(3, 2, 16, 2, dtype=torch.float16))
+    cu, lens, table = torch.tensor([0, 1], dtype=torch.int32), torch.tensor([1], dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
+    rows, q = torch.zeros(1, 2, 64), torch.zeros(1, 2, 64, dtype=torch.float16)
+    for k, v in ((cache, pair), (pair, cache)):
+        for call in (lambda: q4w.kv_read_q8(k, v, table, cu, lens, 1), lambda: q4w.kv_append_q8(rows, rows, k, v, table, cu, lens),
+                     lambda: q4w.kv_attention_q8(q, k, v, table, cu, lens)):
+            with pytest.raises(q4w.Q4Error, match="pair of codes and scales"):
+                call()
+    assert not fake.calls
