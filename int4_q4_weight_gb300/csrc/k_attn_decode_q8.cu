@@ -5,7 +5,11 @@
 namespace q4w {
 namespace dec {
 
-// The largest NT, as many as O leaves registers for.
+// The largest NT: O takes NT D / 4 registers, so 128 of them (at head size 64, where 64 rows would still fit,
+// four is the most that is built).  This kernel and the tile kernel at the most rows, one KV head, fp16 (bf16),
+// us, 64 users of 593000 keys in all: 24 heads of 64 71 and 150 (63, 134), 24 of 128 96 and 195 (89, 148), 16 of
+// 256 99 and 207 (93, 174), 8 of 512 122 and 676; 8 users of 19000 keys: 16.6 and 22.5, 25.3 and 25.1 (25.8,
+// 24.1), 23 and 28, 24 and 47.
 constexpr int max_nt_q8(int D) { return D == 512 ? 1 : D == 256 ? 2 : 4; }
 
 template <typename T>

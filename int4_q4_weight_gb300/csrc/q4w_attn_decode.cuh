@@ -85,11 +85,18 @@ struct Shape<D, NT, false> {
 // The int8 cache: a ring of codes, one of their scales, the queries.
 template <int D, int NT>
 struct Shape<D, NT, true> {
-  static constexpr int kWarps = NT * D <= 256 ? 12 : 8;
+  // Twelve warps have 168 registers each, eight 255, and beyond NT D = 256 the merge of twelve does not fit
+  // shared memory.  Twelve and eight, one KV head, fp16 (bf16), us, 64 users of 593000 keys in all | 8 users of
+  // 19000: 8 rows of 64 32.3 and 33.8 | 11.1 and 10.3; 8 of 128 43.3 and 44.7 | 12.4 and 11.5; 8 of 256 71.7 and
+  // 74.6 | 14.5 and 16.9; 32 of 64 71.6 and 63.3 (64.1, 62.4) | 16.6 and 19.5.  16 of 128 62.3 and 53.5 (56.6,
+  // 50.7) | 15.5 and 13.3: there two runs of twelve warps spill.
+  static constexpr int kWarps = NT * D <= 256 && !(NT == 2 && D == 128) ? 12 : 8;
   // Two runs of 16 keys a unit where a slot of the ring and the registers hold them: the walk, the
   // copies' addresses, the waits and the reference are once a unit, and the queries' fragments are
-  // read once.  64 users of up to 16000 keys, bf16, two runs against one: 4 heads on 1 of 128 66 us
-  // and 76, of 64 82 and 100; 16 on 1 of 128 92 and 96 (fp16 103 and 101, with spills).
+  // read once.  The same users, two runs and one: 8 rows of 64 32.3 and 36.4 | 11.2 and 11.2, 16 of 64 39.7 and
+  // 42.4 | 12.9 and 12.3, 8 of 128 43.3 and 46.7 | 12.4 and 12.2, 16 of 128 53.8 and 62.1 (50.7, 60.6) | 13.2 and
+  // 17.2; 32 of 64 89 and 71.6 (76, 64) | 23.9 and 16.7, 32 of 128 121 and 97 (88, 92) | 21.6 and 25.5, both with
+  // hundreds of bytes of spills.
   static constexpr int U = D <= 128 && NT <= 2 ? 2 : 1;
   static constexpr int kSlotBytes = U * kUnit * D;
   static constexpr int kScaleBytes = U * kUnit * (D / 32) * 2;      // of a slot
