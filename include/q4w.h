@@ -405,6 +405,7 @@ typedef struct q4_kv_cache_q8 {
  * NULL).  For each 32 elements of a row of K or V, after norm and rotation:
  *   scale = fp16(max |x| / 127), rounded up;  code = the integer nearest to
  * x / scale, in [-127, 127]; it stands for code * scale, at most scale / 2 from x.
+ * (The quotient is formed in fp32: within 2^-23 of itself from a half, either side.)
  * Zeros give scale 0 and codes 0.  A block with an infinity or NaN, or whose scale
  * would be above 515.5 (|x| above 65468.5: its values would not all be finite in fp16),
  * is stored as zeros and sets *err to 1.                                    */
@@ -466,7 +467,8 @@ int kv_attention(const q4_kv_cache* cache, int T, int max_q, const void* q,
 /* kv_attention_q8: kv_attention over a quantised cache (kv_append_q8 first).
  * q and out have the 16-bit type cache->c.dtype; everything that is said of
  * kv_attention holds, but for the arithmetic: scores take the exact values of K (to an
- * absolute 2^-25 where these are below 2^-3), V enters the second product as
+ * absolute 2^-25 where these are below 2^-3) and are fp32 numbers, as is the reference by
+ * which parts of a long sequence are joined (2^-24 of itself), V enters the second product as
  * fp16(code * scale), the probabilities as fp16 (in two pieces where q is fp16) with an
  * absolute error of 2^-32 of the row's largest or less where they are small.  With queries in bf16, elements below 2^-28 of a row's
  * largest lose digits.  Scales are at most 515.5, as kv_append_q8 leaves them: with

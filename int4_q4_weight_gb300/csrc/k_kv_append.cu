@@ -29,7 +29,9 @@
 // 75 us, 5.6 TB/s, half of it writes.  Blocks of 128 threads so that few finish
 // late; more resident blocks, or two rows ahead, were slower.  8 tokens: 3.2 us.
 // With norms: 8 ragged prompts, 21000 tokens of 16 + 16 heads of 128, bf16 (348 MB): 71 us, 4.9 TB/s
-// (78 before norms and rotation took two elements an instruction: issue bounds it).
+// (78 before norms and rotation took two elements an instruction: 20 of them an element, issue active for
+// 64 % of the cycles); f32 (522 MB) 87 us, 6.0 TB/s.  Quantised: 8 prompts of 8 + 2 heads of 256, bf16 (207 MB)
+// 54 us, 3.8 TB/s, 22 instructions an element; f32 (316 MB) 68 us, 4.6.
 #include <type_traits>
 
 #include "q4w_codes.cuh"
@@ -140,9 +142,10 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], __half scale) {
   return make_uint2(four(0), four(4));
 }
 
-// Resident blocks: with norms seven (72 registers; six 79 us, eight, which spill, 88 us for
-// eight ragged prompts of 16 + 16 heads of 128), quantised six (five 70, six 64, eight 70 us
-// for eight prompts of 8 + 2 heads of 256, with reading back).
+// Resident blocks: with norms seven (72 registers, 8 bytes of spills for fp16 input).  Eight ragged prompts of
+// 16 + 16 heads of 128, bf16 | fp16 | f32 input, us: five 71 | 78 | 93, six 73 | 72.5 | 86, seven 71.5 | 72 | 87,
+// eight 74.5 | 79 | 118.  Quantised six (80 registers, 4 bytes of spills for fp16, 36 for f32); eight prompts of
+// 8 + 2 heads of 256: five 59 | 58 | 68, six 54 | 54 | 68, seven 57 | 56 | 84, eight 65 | 65 | 93.
 template <typename IN, typename OUT, int MODE>
 __global__ void __launch_bounds__(kThr, MODE == kPlain ? 0 : MODE == kNorm ? 7 : 6) append_kernel(const __grid_constant__ Params p) {
   __shared__ int first_sh;

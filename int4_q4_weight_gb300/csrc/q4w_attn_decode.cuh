@@ -42,9 +42,10 @@
 //      whatever the queries' type.
 // bf16 queries become fp16 by a power of two for each row that brings its largest
 // element to 2^14: exact down to 2^-28 of it.  Queries lie in shared memory in the order
-// of the fragments, which leaves registers for O of 16 rows of head size 256.
+// of the fragments, which leaves registers for O of 16 rows of head size 256 (fp16: but for 8 bytes).
 // Bound: HBM at head size 512 (64 users of up to 16384 keys 122 us, 5.4 TB/s: a key costs 34
-// instructions an SM and 1088 bytes, 47 cycles); instructions below: 4.9 TB/s at 128, 3.9 at 64.
+// instructions an SM and 1088 bytes, 47 cycles); instructions below: 64 users over 323 MB, 8 heads on 1 of 256,
+// 128, 64 at 4.5, 4.8, 3.8 TB/s, 16 on 1 at 3.4, 3.8, 3.1 (bf16; fp16 3.3, 3.6, 2.9).
 #pragma once
 
 #include <math_constants.h>

@@ -65,8 +65,8 @@
 //
 // Bound: the latency of the roles, which share four schedulers.  Four prompts of up to
 // 2048 tokens over up to 8192 keys (8 heads on 1 of 256, 181 GFLOP of a 16-bit cache's products), bf16:
-// 211 us with queries and join, 16-bit cache 124; a step takes 4200 cycles, three quarters of them
-// products.  What brought it there from 330: three warps each for K and V could not widen a step
+// 211 us with queries and join, 16-bit cache 124; fp16, with a product more, 234.  A step takes 4200
+// cycles, three quarters of them products.  What brought it there from 330: three warps each for K and V could not widen a step
 // in its time (an instruction of theirs takes 12 cycles), so fourteen; a table lookup and
 // walk per step for all of them in one warp (a ring of plans); reads for the next slot behind all
 // the stores (between them they share the scoreboards that the stores wait by); the issuing
@@ -105,7 +105,7 @@ struct Shape {
   static constexpr int kN = D == 64 ? 128 : kDV;             // columns of the MMA (D = 64: the odd CTA's are zeros)
   static constexpr int kKD = D < 256 ? D : 256;   // dims of a K slot
   static constexpr int kNK = (Q8 ? 2 : 1) * (D / kKD);       // K slots per step (int8 cache: upper and lower pieces)
-  static constexpr int kKSlot = kKeys / 2 * kKD * 2;         // bytes: 8, 16, 32, 32 KB (int8 cache: 8, 16, 16, 16)
+  static constexpr int kKSlot = kKeys / 2 * kKD * 2;         // bytes: 8, 16, 32, 32 KB
   static constexpr int kVSlot = kKeys * kN;                  // all keys of a step, kN / 2 columns a CTA: 16, 16, 32, 32 KB
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kKSlots = D <= 128 ? 6 : Q8 && D == 256 ? 3 : 2;   // rings of K and of V
