@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(kThr, MODE == kPlain ? 0 : MODE == kNorm ? 7 :
     if constexpr (MODE != kPlain) {
       const float* w = is_q ? p.q_norm : is_k ? p.k_norm : p.v_norm;
       if (w) {
+        // (fp16 input: its squares, from 2^-48 to 2^32, need no second turn)
         float eps = p.eps, mean;
 #pragma unroll 1
         for (bool again = std::is_same<IN, __half>::value;; again = true) {
