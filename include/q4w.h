@@ -536,9 +536,10 @@ int logits_sample(const void* logits, long long stride, int dtype, int b, int V,
  *   ws: draft_verify_ws_bytes(b, k, V) bytes; overlapping calls must not share it.
  * Whether a draft stands goes by sums in fp32, p and q within 2^-16 of themselves (the log
  * probability of a draft accordingly); the token is drawn from integer masses: as in
- * logits_sample where it is drawn from p_n (with u_k = 0 the first index of any weight),
- * in units of 2^-53 from p_n - q_n (with u_k = 0 the first of one unit or more).  The same
- * inputs give the same results on every call.                                */
+ * logits_sample where it is drawn from p_n, in units of 2^-53 from p_n - q_n, p and q within
+ * 2^-28 of themselves (where they are closer to each other than that, what is left of their
+ * difference is of that size); with u_k = 0 it is the first index of any weight, or of any
+ * p_n above q_n.  The same inputs give the same results on every call.          */
 size_t draft_verify_ws_bytes(int b, int k, int V);   /* 0: sizes out of range */
 int draft_verify(const void* logits, long long user_stride, long long row_stride, int dtype,
                  int b, int k, int V, const int32_t* drafts, const float* u,

@@ -28,7 +28,8 @@
 // argument's two roundings (2^-23 ln 2 times up to 20, as a million weights cannot have their mass
 // deeper), and some 53 additions of 2^-24; errors of random signs leave about 2^-23.
 // The rest's probabilities are integers too: the mantissas times 2^(-j/8) / mass, 32 bits formed
-// once per row, so that p - q of an element costs two weights and a subtraction.
+// once per row, so that p - q of an element costs two weights and a subtraction.  They are good to 2^-28
+// of themselves, as the weights are: the law of a token, over drafts drawn from q, to 2^-27.
 //
 // Measured (f32, V = 262144): 64 users with up to four drafts, 0 to 4 there (336 MB read of
 // 604): rows 50 us (6.5 TB/s), sums 36, rest 23, from a graph 110.  One user of four drafts 18.4
@@ -769,17 +770,38 @@ __device__ __forceinline__ void divide_table(u64 mass, const uint32_t* eighth, u
   if (j == 0) *shift = 21 - c + 60 - kUnit;
 }
 
-// The next token of a user whose rest is empty: from p_n.  (A function of its own: the kernel does not carry
-// two draws in line.)
+// The two ends of a rest that masses do not decide, each a function: the kernel does not carry their code in line.
+// The user's next token is i, of logit z.
+__device__ __forceinline__ void write_drawn(const Params& p, const Shared& sh, const Unit& c, int i, float z) {
+  const long long at = (long long)c.user * (p.k + 1) + c.n;
+  p.tokens[at] = i;
+  if (p.logprobs) p.logprobs[at] = log_prob(z, c.top, 1.0 / (double)c.t, log((double)sh.mass_p * kSumUnit));
+}
+// u = 0: the first index with p_n > q_n, be the difference less than a unit.  False: there is none.
+template <typename T>
+static __device__ __noinline__ bool rest_first(const Params& p, Shared& sh, int unit) {
+  const Unit c = p.rest[unit];
+  const T *zp = row_of<T>(p, c.user, c.n), *zq = row_of<T>(p, c.user, p.k + 1 + c.n);
+  const Scale sp = make_scale(c.top, c.t, 0.f), sq = make_scale(c.top_q, c.t, 0.f);
+  const Num mass_p = Num::of(sh.mass_p, 0), mass_q = Num::of(p.mass[2 * c.user + 1], 0);
+  if (threadIdx.x == 0) sh.first = 0x7fffffff;
+  __syncthreads();
+  for (int i0 = 0; i0 < p.V; i0 += kThr) {
+    const int i = i0 + threadIdx.x;
+    const bool some = i < p.V && weight_number(sh.eighth, sq, as_float(zq[i])) * mass_p < weight_number(sh.eighth, sp, as_float(zp[i])) * mass_q;
+    if (some) atomicMin(&sh.first, i);
+    if (__syncthreads_or(some)) break;
+  }
+  if (sh.first == 0x7fffffff) return false;
+  if (threadIdx.x == 0) write_drawn(p, sh, c, sh.first, as_float(zp[sh.first]));
+  return true;
+}
+// The rest is empty: from p_n.
 template <typename T>
 static __device__ __noinline__ void rest_from_target(const Params& p, Shared& sh, int unit) {
   const Unit c = p.rest[unit];
-  const long long at = (long long)c.user * (p.k + 1) + c.n;
-  auto logs = [&](u64) {};   // found() forms them
-  auto found = [&](int i, float z) {
-    p.tokens[at] = i;
-    if (p.logprobs) p.logprobs[at] = log_prob(z, c.top, 1.0 / (double)c.t, log((double)sh.mass_p * kSumUnit));
-  };
+  auto logs = [](u64) {};   // write_drawn() forms them
+  auto found = [&](int i, float z) { write_drawn(p, sh, c, i, z); };
   __syncthreads();
   draw_target<T>(p, sh, Row<T>(row_of<T>(p, c.user, c.n), p.V), make_scale(c.top, c.t, 0.f), -1,
                  p.seg + (long long)c.user * 2 * p.n_segs, random_of(p, c.user, p.k), logs, found);
@@ -851,7 +873,7 @@ __global__ void __launch_bounds__(kThr, kResident) rest_kernel(const __grid_cons
       if (p.logprobs) p.logprobs[(long long)user * (p.k + 1) + c.n] = log_prob(z, c.top, sh.per_t, sh.log_mass);
     };
     const float u = random_of(p, user, p.k);
-    const bool drawn = draw(p, sh, seg, u, [&](int i, u64 (&w)[8], float (&v)[8]) {
+    const bool drawn = u == 0.f ? rest_first<T>(p, sh, unit) : draw(p, sh, seg, u, [&](int i, u64 (&w)[8], float (&v)[8]) {
       float y[8];
       rp.load(i, v);
       rq.load(i, y);
